@@ -29,6 +29,10 @@
  *    copy_blocks_layers / kv_append_layers (every layer in one launch), and
  *    paged_decode_attention_static_workspace (decode with library scratch).
  *    Each cites its passage below.
+ *  - Around them, for a serving loop: the cache in 8-bit floating point
+ *    (kv_append_e4m3, dequantize_blocks, paged_decode_attention_e4m3), the
+ *    pass from the projections to the cache (qk_norm_rope_append), and trees
+ *    of drafted tokens (tree_masks, paged_tree_attention, kv_accept_layers).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -73,7 +77,7 @@
 extern "C" {
 #endif
 
-typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_BF16_OUT_F32 = 2 } pkv_dtype;
+typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_BF16_OUT_F32 = 2, PKV_E4M3 = 4 /* 3 names no type */ } pkv_dtype;
 
 #define PKV_OK 0
 #define PKV_ERR_ARG -1          /* bad scalar argument, null pointer, shape mismatch */
@@ -94,6 +98,7 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_BF16_OUT_F32 = 2 } pkv_dtype;
 #define PKV_DEVERR_TIMEOUT 0x8u     /* a bounded wait inside a kernel ran out: output unspecified */
 #define PKV_DEVERR_LENGTH 0x10u     /* context_len < 0, > max_blocks_per_seq*16 or > max_context_len: clamped */
 #define PKV_DEVERR_POINTER 0x20u    /* a pointer in a per-layer pointer array is null or not 16-byte aligned: skipped */
+#define PKV_DEVERR_INDEX 0x40u      /* a position axis, a draft's parent or an accepted draft out of range: see the call */
 
 /* Human-readable name of a status code (static storage). */
 const char *pkv_status_string(int status);
@@ -424,6 +429,187 @@ int paged_decode_attention_static_workspace(void *out, const void *q, const void
                                             int num_kv_heads, int num_seqs, int num_q_heads, int head_dim,
                                             int max_blocks_per_seq, int num_blocks, int max_context_len,
                                             pkv_dtype dtype, int partition_tokens, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The cache in 8-bit floating point (PKV_E4M3)
+ * ---------------------------------------------------------------------------
+ * k_cache, v_cache: [num_blocks][num_kv_heads] tiles of PKV_E4M3_TILE_BYTES
+ * bytes each, 16-byte aligned: the 16 slots' rows of head_dim e4m3 codes
+ * (4 exponent bits with bias 7, 3 mantissa bits, largest value 448, no
+ * infinities), then the 16 rows' scale bytes. Element d of slot r is
+ *   code[r][d] * 2^(scale[r] - 127).
+ * A row x is quantised with the smallest exponent e for which
+ * max|x| * 2^-e <= 448, kept in [-50, 50] (0 for a row of zeros):
+ *   code = x * 2^-e rounded to e4m3, ties to even;  scale = e + 127.
+ * The scale is a power of two, so x * 2^-e is exact and codes are defined bit
+ * for bit. Rows past 448 * 2^50 saturate; NaN and infinities become NaN and
+ * do not take part in the maximum. Against a 16-bit cache this reads and
+ * writes (head_dim + 1) / (2 head_dim) of the bytes.
+ *
+ * kv_append_e4m3 quantises and writes new tokens, dequantize_blocks reads
+ * blocks back into a bf16 or fp32 cache (for paged_prefill_attention over a
+ * quantised context), paged_decode_attention_e4m3 attends the tiles
+ * themselves, and copy_blocks, swap_blocks and copy_blocks_layers move them
+ * with dtype = PKV_E4M3 (bit-exact).
+ */
+#define PKV_E4M3_TILE_BYTES(head_dim) (16 * ((head_dim) + 1))
+
+/*
+ * kv_append into an e4m3 cache: k, v [num_tokens][num_kv_heads][head_dim] of
+ * `dtype` (PKV_BF16 or PKV_F32). Slots as for kv_append: negative ones are
+ * skipped, slots >= num_blocks * 16 skipped and flagged (PKV_DEVERR_SLOT), and
+ * no slot may be listed twice. k, v and slot_mapping may be page-locked host
+ * memory.
+ */
+int kv_append_e4m3(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                   int num_tokens, int num_kv_heads, int head_dim, int num_blocks, pkv_dtype dtype, void *stream);
+
+/*
+ * For each pair i, every slot of block src_dst_pairs[i][0] of an e4m3 cache is
+ * written, as the values it stands for, into block src_dst_pairs[i][1] of a
+ * cache of `dst_dtype` (PKV_BF16 or PKV_F32; the values are exact in both),
+ * for both caches. Pairs as for swap_blocks: destinations distinct
+ * (pkv_check_swap_pairs), pairs out of range skipped and flagged
+ * (PKV_DEVERR_PAIR); at most 2^30 pairs. Slots never written come out as
+ * whatever their bytes stand for.
+ */
+int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const void *src_k_cache,
+                      const void *src_v_cache, int src_num_blocks, const int64_t *src_dst_pairs, int num_pairs,
+                      int num_kv_heads, int head_dim, pkv_dtype dst_dtype, void *stream);
+
+/*
+ * paged_decode_attention over e4m3 caches: q and out bf16 (PKV_BF16), or q
+ * bf16 and out fp32 (PKV_BF16_OUT_F32); every other argument, an empty
+ * context, masking and errors as for paged_decode_attention. The workspace
+ * holds partial states only: it needs no initial value and may be a buffer
+ * that other decode calls use (the counter header is left alone). Concurrent
+ * calls must not share it.
+ */
+int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_tables, const int32_t *context_lens, float scale,
+                                int num_kv_heads, int num_seqs, int num_q_heads, int head_dim,
+                                int max_blocks_per_seq, int num_blocks, int max_context_len, pkv_dtype dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes paged_decode_attention_e4m3 needs (0 when it needs none). */
+size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len);
+
+/*
+ * ---------------------------------------------------------------------------
+ * From the projections to the cache
+ * ---------------------------------------------------------------------------
+ * One pass over a step's new tokens before attention: the queries and keys of
+ * every head are normalised and rotated to their positions, the queries go to
+ * q_out, the keys and the values into their cache slots.
+ *   norm (with weights):  y = x / sqrt(mean(x^2) + eps) * weight   over the head's head_dim elements
+ *   rotation of the first rot_dim elements: frequency i turns the pair
+ *     (a, b) = (y[i], y[i + rot_dim/2]), or (y[2i], y[2i+1]) if interleaved,
+ *     by the angle positions[axes[i]][t] * inv_freq[i]:
+ *     a' = a cos - b sin,  b' = b cos + a sin;  elements past rot_dim stay.
+ * Everything is computed in fp32 (the angle is reduced in 64 bits, so far
+ * positions keep their accuracy) and rounded once, on the way out.
+ *
+ * q, k, v: [num_tokens][heads][head_dim] of `dtype` (PKV_BF16 or PKV_F32);
+ *   q_stride, k_stride, v_stride are the elements from one token to the next
+ *   (at least heads * head_dim, a multiple of 16 bytes), so the three may be
+ *   slices of one projection's output. q_out: [num_tokens][num_q_heads]
+ *   [head_dim], contiguous; it may be q itself.
+ * q_weight, k_weight: [head_dim] of `dtype`, both or neither (NULL: no norm).
+ * positions: int64 [num_axes][num_tokens]; axes: int32 [rot_dim / 2], the axis
+ *   each frequency follows (NULL: axis 0 for all), e.g. time, height and width
+ *   for images and video. An axis out of range leaves its pairs unturned and
+ *   raises PKV_DEVERR_INDEX.
+ * inv_freq: fp32 [rot_dim / 2]. rot_dim: a multiple of 16, at most head_dim
+ *   (0: no rotation; positions, inv_freq and axes may then be NULL).
+ * slot_mapping: int64 [num_tokens], slots as for kv_append (a token with a
+ *   negative slot still gets its q_out row).
+ * cache_dtype: `dtype`, or PKV_E4M3 (the fp32 rows are quantised as by
+ *   kv_append_e4m3, without a rounding to `dtype` between).
+ */
+int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const void *q_weight, const void *k_weight, float eps,
+                        const int64_t *positions, int num_axes, const float *inv_freq, const int32_t *axes,
+                        int rot_dim, int interleaved, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                        int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+                        pkv_dtype dtype, pkv_dtype cache_dtype, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Trees of drafted tokens
+ * ---------------------------------------------------------------------------
+ * Speculative decoding appends n_s drafted tokens behind each sequence's
+ * context (kv_append, qk_norm_rope_append) and attends them all at once; the
+ * drafts form a tree, and each sees the context and its own ancestors.
+ *
+ * Sequence s owns query rows query_start[s] .. query_start[s+1]-1 (n_s of
+ * them), the drafts at its last n_s cache positions, context_lens[s] - n_s ..
+ * context_lens[s] - 1. Row i of s attends every position before the drafts,
+ * and draft j exactly if bit j % 64 of tree_mask[row][j / 64] is set (its own
+ * bit included; bits from n_s on are ignored). A row that sees nothing yields
+ * zeros.
+ *
+ * q, out, query_start, context_lens, num_queries, max_query_len and
+ *   max_context_len as for paged_prefill_attention (a bad n_s leaves the
+ *   sequence's rows unwritten and raises PKV_DEVERR_LENGTH); rows from
+ *   query_start[num_seqs] on are not touched.
+ * tree_mask: int64 [num_queries][mask_words], mask_words >= ceil(max_query_len / 64).
+ * bf16 only; head_dim 64 or 128; num_q_heads / num_kv_heads at most 64;
+ *   max_query_len at most PKV_TREE_MAX_DRAFTS.
+ * workspace: pkv_tree_workspace_bytes(...) bytes, partial states only: no
+ *   initial value, the counter header of a decode workspace left alone.
+ *   Concurrent calls must not share it.
+ */
+#define PKV_TREE_MAX_DRAFTS 1024
+int paged_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                         const int64_t *tree_mask, int mask_words, float scale, int num_kv_heads, int num_seqs,
+                         int num_q_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int num_queries,
+                         int max_query_len, int max_context_len, pkv_dtype dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/* Workspace bytes paged_tree_attention needs (0 when it needs none). */
+size_t pkv_tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_query_len,
+                                int max_context_len);
+
+/*
+ * tree_mask of paged_tree_attention from the drafts' parents: parents[row] is
+ * the index within the sequence of the row's parent draft, -1 for a child of
+ * the context; a draft comes after its parent. Row i gets the bits of i and
+ * all its ancestors, in ceil(max_query_len / 64) words. A parent that is not
+ * in [-1, i) ends the walk and raises PKV_DEVERR_INDEX. Bad n_s (as above)
+ * raise PKV_DEVERR_LENGTH and leave the sequence's rows unwritten.
+ */
+int tree_masks(int64_t *tree_mask, const int32_t *parents, const int32_t *query_start, int num_seqs, int num_queries,
+               int max_query_len, void *stream);
+
+/*
+ * After verification, the accepted drafts' keys and values move to where the
+ * next step expects them: with base = context_lens[s] - n_s, the row at
+ * position base + accepted[s][j] goes to position base + j for j <
+ * num_accepted[s], in every layer's caches, and new_lens[s] = base +
+ * num_accepted[s]. All of a sequence's rows are read before any is written, so
+ * any list of drafts will do (a path down the tree, repeats included).
+ *
+ * accepted: int32 [num_seqs][max_accepted]; num_accepted: int32 [num_seqs], at
+ *   most min(n_s, max_accepted): outside [0, that] it is clamped and flagged
+ *   (PKV_DEVERR_LENGTH). An accepted[s][j] outside [0, n_s) moves nothing to
+ *   base + j and raises PKV_DEVERR_INDEX; a position in a bad block
+ *   (PKV_DEVERR_BLOCK_ID) is skipped. max_accepted at most
+ *   PKV_MAX_ACCEPTED. A bad n_s (negative, or above the context length)
+ *   moves nothing, raises PKV_DEVERR_LENGTH and gives new_lens[s] =
+ *   context_lens[s].
+ * k_caches, v_caches: pointer arrays as for copy_blocks_layers; bf16 or fp32
+ *   caches. new_lens must not overlap context_lens. The destination blocks
+ *   must belong to one sequence only (copy shared ones first: the drafts'
+ *   append needed that too).
+ */
+#define PKV_MAX_ACCEPTED 64
+int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layers, const int32_t *block_tables,
+                     const int32_t *context_lens, const int32_t *query_start, const int32_t *accepted,
+                     int max_accepted, const int32_t *num_accepted, int32_t *new_lens, int num_seqs,
+                     int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, pkv_dtype dtype,
+                     void *stream);
 
 #ifdef __cplusplus
 }

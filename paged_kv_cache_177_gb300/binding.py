@@ -23,15 +23,19 @@ if not os.path.exists(LIB):
 
 _lib = ctypes.CDLL(LIB)
 
-PKV_F32, PKV_BF16, PKV_BF16_OUT_F32 = 0, 1, 2
+PKV_F32, PKV_BF16, PKV_BF16_OUT_F32, PKV_E4M3 = 0, 1, 2, 4
 PARTITION_AUTO, PARTITION_BALANCED = 0, -1
 DEVERR_BLOCK_ID, DEVERR_SLOT, DEVERR_PAIR, DEVERR_TIMEOUT, DEVERR_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
-DEVERR_POINTER = 0x20
+DEVERR_POINTER, DEVERR_INDEX = 0x20, 0x40
 BLOCK_SIZE = 16
 # the arrival counters at the head of every decode workspace (PKV_DECODE_COUNTER_BYTES)
 DECODE_COUNTER_BYTES = 10240
 
+# largest sizes the tree calls take (PKV_TREE_MAX_DRAFTS, PKV_MAX_ACCEPTED)
+TREE_MAX_DRAFTS, MAX_ACCEPTED = 1024, 64
+
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 def _decl(name, restype, *argtypes):
@@ -65,6 +69,18 @@ _append_layers = _decl("kv_append_layers", _i, _vp, _vp, _vp, _vp, _vp, _i, _i, 
 _check_pairs = _decl("pkv_check_copy_pairs", _i, _vp, _i, _i)
 _validate = _decl("pkv_validate", _i, _vp, _vp, _i, _i, _i, _i, _vp, _vp)
 _validate_slots = _decl("pkv_validate_slots", _i, _vp, _i, _i, _vp, _vp)
+_append_e4m3 = _decl("kv_append_e4m3", _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp)
+_dequantize = _decl("dequantize_blocks", _i, _vp, _vp, _i, _vp, _vp, _i, _vp, _i, _i, _i, _i, _vp)
+_decode_e4m3 = _decl("paged_decode_attention_e4m3", _i, _vp, _vp, _vp, _vp, _vp, _vp, _f, _i, _i, _i, _i, _i, _i, _i,
+                     _i, _vp, _sz, _vp)
+_e4m3_ws = _decl("pkv_e4m3_workspace_bytes", _sz, _i, _i, _i, _i, _i)
+_rope = _decl("qk_norm_rope_append", _i, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp, _f, _vp, _i, _vp, _vp, _i, _i,
+              _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp)
+_tree_masks = _decl("tree_masks", _i, _vp, _vp, _vp, _i, _i, _i, _vp)
+_tree = _decl("paged_tree_attention", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _i, _i, _i, _i, _i, _i, _i, _i,
+              _i, _i, _vp, _sz, _vp)
+_tree_ws = _decl("pkv_tree_workspace_bytes", _sz, _i, _i, _i, _i, _i, _i)
+_accept = _decl("kv_accept_layers", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp)
 _device_error = _decl("pkv_device_error", _i, ctypes.POINTER(ctypes.c_uint32), _i)
 
 
@@ -379,6 +395,18 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_ca
                    _stream_ptr(dev, stream)), "kv_append")
 
 
+def _pool_shape(t: torch.Tensor) -> tuple:
+    """(blocks, kv heads, head_dim, dtype code) of a cache: bf16 or fp32
+    [NB, Hkv, 16, D], or e4m3 tiles (uint8 [NB, Hkv, 16 * (D + 1)])."""
+    if t.dtype == torch.uint8:
+        if t.dim() != 3 or t.shape[2] % BLOCK_SIZE:
+            raise ValueError("an e4m3 cache is uint8 [NB, Hkv, 16 * (D + 1)]")
+        return t.shape[0], t.shape[1], t.shape[2] // BLOCK_SIZE - 1, PKV_E4M3
+    if t.dim() != 4 or t.shape[2] != BLOCK_SIZE:
+        raise ValueError("caches must be [NB, Hkv, 16, D]")
+    return t.shape[0], t.shape[1], t.shape[3], _dtype_code(t)
+
+
 def check_copy_pairs(pairs, num_blocks: int) -> None:
     """Host-side range/overlap check of (src, dst) pairs; raises PagedKVError."""
     arr = np.ascontiguousarray(np.asarray(pairs, dtype=np.int64).reshape(-1, 2))
@@ -387,21 +415,20 @@ def check_copy_pairs(pairs, num_blocks: int) -> None:
 
 def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src_dst_pairs: torch.Tensor, *,
                 host_pairs=None, check: bool = True, stream: Optional[torch.cuda.Stream] = None) -> None:
-    """Copies whole blocks src -> dst of both caches.  ``src_dst_pairs``:
+    """Copies whole blocks src -> dst of both caches (e4m3 tiles too).  ``src_dst_pairs``:
     int64 [n, 2] on the device.  With ``check`` the pairs are range- and
     overlap-checked on the host first (``host_pairs`` if given, else a copy
     of the device pairs, which synchronises).  The pairs may also be a
     pinned host tensor (read in place)."""
     dev = _dev_io([k_cache, v_cache], [src_dst_pairs])
-    dt = _dtype_code(k_cache)
+    NB, Hkv, D, dt = _pool_shape(k_cache)
     if src_dst_pairs.dtype != torch.int64:
         raise TypeError("src_dst_pairs must be int64")
     n = src_dst_pairs.numel() // 2
     if src_dst_pairs.numel() != 2 * n:
         raise ValueError("src_dst_pairs must be [n, 2]")
-    NB, Hkv, P, D = k_cache.shape
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or P != BLOCK_SIZE:
-        raise ValueError("caches must be [NB, Hkv, 16, D] of one dtype")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("both caches must share shape and dtype")
     if check:
         check_copy_pairs(host_pairs if host_pairs is not None else src_dst_pairs.cpu().numpy(), NB)
     _check(_copy(_p(k_cache), _p(v_cache), _p(src_dst_pairs) if n else None, n, Hkv, D, NB, dt,
@@ -427,7 +454,7 @@ def swap_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor, s
                 stream: Optional[torch.cuda.Stream] = None) -> None:
     """Copies block src of the source pool onto block dst of the destination
     pool (both caches) for each pair.  A pool is a CUDA tensor or a pinned
-    host tensor [NB, Hkv, 16, D]; swap-out goes device -> host, swap-in host ->
+    host tensor [NB, Hkv, 16, D], or of e4m3 tiles; swap-out goes device -> host, swap-in host ->
     device.  ``src_dst_pairs``: int64 [n, 2], on the device or pinned."""
     for t in (dst_k, dst_v, src_k, src_v, src_dst_pairs):
         _pool_ok(t)
@@ -435,11 +462,10 @@ def swap_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor, s
         raise TypeError("src_dst_pairs must be int64")
     if not (dst_k.dtype == dst_v.dtype == src_k.dtype == src_v.dtype):
         raise TypeError("pools must share one dtype")
-    dt = _dtype_code(dst_k)
-    NBd, Hkv, P, D = dst_k.shape
+    NBd, Hkv, D, dt = _pool_shape(dst_k)
     NBs = src_k.shape[0]
-    if dst_v.shape != dst_k.shape or src_v.shape != src_k.shape or src_k.shape[1:] != dst_k.shape[1:] or P != BLOCK_SIZE:
-        raise ValueError("pools must be [NB, Hkv, 16, D] with matching block shapes")
+    if dst_v.shape != dst_k.shape or src_v.shape != src_k.shape or src_k.shape[1:] != dst_k.shape[1:]:
+        raise ValueError("pools must have matching block shapes")
     n = src_dst_pairs.numel() // 2
     if check:
         check_swap_pairs(host_pairs if host_pairs is not None else src_dst_pairs.cpu().numpy(), NBs, NBd)
@@ -466,19 +492,17 @@ def layer_pointers(tensors, device=None) -> torch.Tensor:
 def copy_blocks_layers(k_caches, v_caches, src_dst_pairs: torch.Tensor, *, host_pairs=None, check: bool = True,
                        stream: Optional[torch.cuda.Stream] = None, ptrs=None) -> None:
     """copy_blocks over every layer's caches (lists of [NB, Hkv, 16, D] CUDA
-    tensors, one per layer) in one launch.  ``ptrs``: optional prebuilt
+    tensors or e4m3 tiles, one per layer) in one launch.  ``ptrs``: optional prebuilt
     (k_caches, v_caches) pointer arrays from ``layer_pointers``."""
     if len(k_caches) != len(v_caches):
         raise ValueError("one K and one V cache per layer")
     if not k_caches:
         return
     dev = _dev(*k_caches, *v_caches, src_dst_pairs)
-    dt = _dtype_code(k_caches[0])
-    shape = k_caches[0].shape
+    NB, Hkv, D, dt = _pool_shape(k_caches[0])
     for t in (*k_caches, *v_caches):
-        if t.shape != shape or t.dtype != k_caches[0].dtype:
+        if t.shape != k_caches[0].shape or t.dtype != k_caches[0].dtype:
             raise ValueError("every layer's caches must share shape and dtype")
-    NB, Hkv, P, D = shape
     n = src_dst_pairs.numel() // 2
     if check:
         check_copy_pairs(host_pairs if host_pairs is not None else src_dst_pairs.cpu().numpy(), NB)
@@ -516,6 +540,348 @@ def kv_append_layers(ks, vs, slot_mapping: torch.Tensor, k_caches, v_caches, *,
         arrs = list(ptrs) if ptrs is not None else [_ptr_array(x, dev) for x in (ks, vs, k_caches, v_caches)]
         _check(_append_layers(*(_p(a) for a in arrs[:2]), _p(slot_mapping), *(_p(a) for a in arrs[2:]), L, T, Hkv, D,
                               NB, dt, st.cuda_stream), "kv_append_layers")
+
+
+# ---------------------------------------------------------------------------
+# the cache in 8-bit floating point
+# ---------------------------------------------------------------------------
+class _On:
+    """Makes ``device`` current for a launch where it is not already."""
+    __slots__ = ("index", "saved")
+
+    def __init__(self, device: torch.device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.saved = torch.cuda.current_device()
+        if self.saved != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.saved != self.index:
+            torch.cuda.set_device(self.saved)
+
+
+def e4m3_cache(num_blocks: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
+    """An empty e4m3 cache: zeroed tiles, uint8 [NB, Hkv, 16 * (D + 1)] -- the
+    16 slots' rows of D codes, then the 16 rows' scale bytes (element d of
+    slot r stands for code[r][d] * 2^(scale[r] - 127))."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim is 64 or 128")
+    return torch.zeros(num_blocks, num_kv_heads, BLOCK_SIZE * (head_dim + 1), dtype=torch.uint8,
+                       device=device if device is not None else "cuda")
+
+
+def _e4m3_pool(k_cache: torch.Tensor, v_cache: torch.Tensor, head_dim: int) -> tuple:
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+        raise TypeError("e4m3 caches are uint8 tiles")
+    if k_cache.dim() != 3 or k_cache.shape[2] != BLOCK_SIZE * (head_dim + 1) or v_cache.shape != k_cache.shape:
+        raise ValueError("expected e4m3 caches [NB, Hkv, 16 * (D + 1)]")
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def kv_append_e4m3(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                   v_cache: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None) -> None:
+    """kv_append into an e4m3 cache (see ``e4m3_cache``): each row of k and v
+    ([T, Hkv, D], bf16 or fp32) is quantised with the least power-of-two scale
+    that brings its largest magnitude to at most 448, and written to its slot.
+    No slot may be listed twice.  k, v and slot_mapping may be pinned host
+    tensors (read in place)."""
+    dev = _dev_io([k_cache, v_cache], [k, v, slot_mapping])
+    dt = _dtype_code(k)
+    if v.dtype != k.dtype or slot_mapping.dtype != torch.int64:
+        raise TypeError("k and v of one dtype and slot_mapping int64")
+    if k.dim() != 3 or v.shape != k.shape or slot_mapping.shape != (k.shape[0],):
+        raise ValueError("expected k, v [T, Hkv, D] and slot_mapping [T]")
+    T, Hkv, D = k.shape
+    NB, Hkv2 = _e4m3_pool(k_cache, v_cache, D)
+    if Hkv2 != Hkv:
+        raise ValueError("k has another number of kv heads than the cache")
+    with _On(dev):
+        _check(_append_e4m3(_p(k), _p(v), _p(slot_mapping), _p(k_cache), _p(v_cache), T, Hkv, D, NB, dt,
+                            _stream_ptr(dev, stream)), "kv_append_e4m3")
+
+
+def dequantize_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor, src_v: torch.Tensor,
+                      src_dst_pairs: torch.Tensor, *, host_pairs=None, check: bool = True,
+                      stream: Optional[torch.cuda.Stream] = None) -> None:
+    """Writes the values of block src of an e4m3 cache into block dst of a
+    bf16 or fp32 cache [NB, Hkv, 16, D], both caches, for each pair (int64
+    [n, 2] on the device, destinations distinct; ``check`` and ``host_pairs``
+    as for ``swap_blocks``).  Prefill over a quantised context reads the
+    context's blocks back into a scratch cache and attends that."""
+    dev = _dev(dst_k, dst_v, src_k, src_v, src_dst_pairs)
+    NBd, Hkv, D, dt = _pool_shape(dst_k)
+    if dt == PKV_E4M3 or dst_v.shape != dst_k.shape or dst_v.dtype != dst_k.dtype:
+        raise TypeError("the destination caches are bf16 or fp32 [NB, Hkv, 16, D], both alike")
+    NBs, Hkv2 = _e4m3_pool(src_k, src_v, D)
+    if Hkv2 != Hkv:
+        raise ValueError("the caches differ in kv heads")
+    if src_dst_pairs.dtype != torch.int64:
+        raise TypeError("src_dst_pairs must be int64")
+    n = src_dst_pairs.numel() // 2
+    if src_dst_pairs.numel() != 2 * n:
+        raise ValueError("src_dst_pairs must be [n, 2]")
+    if check:
+        check_swap_pairs(host_pairs if host_pairs is not None else src_dst_pairs.cpu().numpy(), NBs, NBd)
+    with _On(dev):
+        _check(_dequantize(_p(dst_k), _p(dst_v), NBd, _p(src_k), _p(src_v), NBs, _p(src_dst_pairs) if n else None, n,
+                           Hkv, D, dt, _stream_ptr(dev, stream)), "dequantize_blocks")
+
+
+def e4m3_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                         max_context_len: int) -> int:
+    """Workspace bytes of paged_decode_attention_e4m3 (0: none needed)."""
+    return int(_e4m3_ws(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len))
+
+
+def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device,
+               stream: Optional[torch.cuda.Stream]) -> tuple:
+    """(tensor or None, bytes) of a call's partial states.  One made here is
+    allocated on the call's stream, whose order keeps it from other work until
+    the call is done."""
+    if workspace is None:
+        if not need:
+            return None, 0
+        with torch.cuda.stream(stream):           # (no-op for None: the current stream)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif _dev(workspace) != dev:
+        raise ValueError("the workspace must be on the caches' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def paged_decode_attention_e4m3(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *,
+                                max_context_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                                stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_decode_attention over e4m3 caches: out[s, hq] = softmax(scale *
+    K_s q[s, hq]) V_s with K and V the values the tiles stand for.
+
+    q: bf16 [S, Hq, D]; out: the same, or fp32; caches from ``e4m3_cache``;
+    block_tables int32 [S, maxB], context_lens int32 [S]; up to 16 query heads
+    to a kv head.  ``max_context_len`` defaults to context_lens.max() (a
+    device sync).  ``workspace``: at least ``e4m3_workspace_bytes(...)`` bytes,
+    no initial value needed; calls that may overlap must not share it.  q,
+    out, block_tables and context_lens may be pinned host tensors."""
+    dev = _dev_io([k_cache, v_cache], [out, q, block_tables, context_lens])
+    if q.dtype != torch.bfloat16 or out.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("q is bf16, out bf16 or fp32")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if q.dim() != 3 or out.shape != q.shape:
+        raise ValueError("expected q and out [S, Hq, D]")
+    S, Hq, D = q.shape
+    NB, Hkv = _e4m3_pool(k_cache, v_cache, D)
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("expected block_tables [S, maxB] and context_lens [S]")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    with _On(dev):
+        ws, ws_bytes = _workspace(_e4m3_ws(S, Hq, Hkv, D, max_context_len), workspace, dev, stream)
+        _check(_decode_e4m3(_p(out), _p(q), _p(k_cache), _p(v_cache), _p(block_tables), _p(context_lens),
+                            float(scale), Hkv, S, Hq, D, block_tables.shape[1], NB, int(max_context_len),
+                            PKV_BF16 if out.dtype == torch.bfloat16 else PKV_BF16_OUT_F32, _p(ws), ws_bytes,
+                            _stream_ptr(dev, stream)), "paged_decode_attention_e4m3")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# from the projections to the cache
+# ---------------------------------------------------------------------------
+def _token_rows(t: torch.Tensor, what: str) -> int:
+    """The stride from one token of [T, H, D] rows to the next; heads must be contiguous."""
+    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"{what} must be [T, heads, D] with contiguous heads")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def qk_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        positions: Optional[torch.Tensor], inv_freq: Optional[torch.Tensor],
+                        slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, *,
+                        q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                        eps: float = 1e-6, axes: Optional[torch.Tensor] = None, interleaved: bool = False,
+                        stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Normalises every head of q and k, turns them to their tokens'
+    positions, writes q to ``q_out`` and k and v to their cache slots, in one
+    pass; see include/pagedkv.h.
+
+    q [T, Hq, D], k and v [T, Hkv, D]: bf16 or fp32, the heads of a token
+    contiguous, tokens any distance apart (slices of one projection's output
+    will do).  q_out: contiguous [T, Hq, D] (q itself if that is contiguous).
+    q_weight, k_weight: [D] of q's dtype, both or neither (no norm).
+    inv_freq: fp32 [R / 2], R = rotated elements of a head, a multiple of 16;
+    None: no rotation.  positions: int64 [T], or [A, T] for A axes, with
+    ``axes`` int32 [R / 2] naming the axis of each frequency (default: the
+    first for all).  ``interleaved``: pairs are neighbours (2i, 2i + 1), not
+    halves (i, i + R / 2).  slot_mapping int64 [T], negative slots skipped.
+    Caches: [NB, Hkv, 16, D] of q's dtype, or e4m3 (``e4m3_cache``)."""
+    dev = _dev(k_cache, v_cache, slot_mapping, q_out)
+    for t in (q, k, v, positions, inv_freq, q_weight, k_weight, axes):
+        if t is not None and t.device != dev:
+            raise ValueError("all tensors must be on the same device")
+    for t in (positions, inv_freq, q_weight, k_weight, axes):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("all tensors but q, k and v must be contiguous")
+    dt = _dtype_code(q)
+    if not (q_out.dtype == k.dtype == v.dtype == q.dtype):
+        raise TypeError("q, k, v and q_out must share one dtype")
+    qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    if k.shape != (T, Hkv, D) or v.shape != k.shape or q_out.shape != q.shape:
+        raise ValueError("expected q, q_out [T, Hq, D] and k, v [T, Hkv, D]")
+    NB, Hkv2, D2, cdt = _pool_shape(k_cache)
+    if (Hkv2, D2) != (Hkv, D) or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("the caches must have k's heads and head_dim, both alike")
+    if cdt not in (dt, PKV_E4M3):
+        raise TypeError("the caches have q's dtype or are e4m3")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise TypeError("slot_mapping must be int64 [T]")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight come together")
+    if q_weight is not None and not (q_weight.dtype == k_weight.dtype == q.dtype
+                                     and q_weight.shape == k_weight.shape == (D,)):
+        raise TypeError("q_weight and k_weight are [D] of q's dtype")
+    rot, num_axes = 0, 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+            raise TypeError("inv_freq must be fp32 [R / 2]")
+        if positions is None or positions.dtype != torch.int64 or positions.dim() not in (1, 2) \
+                or positions.shape[-1] != T:
+            raise TypeError("positions must be int64 [T] or [A, T]")
+        rot, num_axes = 2 * inv_freq.shape[0], positions.shape[0] if positions.dim() == 2 else 1
+        if axes is not None and (axes.dtype != torch.int32 or axes.shape != inv_freq.shape):
+            raise TypeError("axes must be int32 [R / 2]")
+    elif positions is not None or axes is not None:
+        raise ValueError("positions and axes need inv_freq")
+    with _On(dev):
+        _check(_rope(_p(q_out), _p(q), _p(k), _p(v), qs, ks, vs, _p(q_weight), _p(k_weight), float(eps), _p(positions),
+                     num_axes, _p(inv_freq), _p(axes), rot, 1 if interleaved else 0, _p(slot_mapping), _p(k_cache),
+                     _p(v_cache), T, Hq, Hkv, D, NB, dt, cdt, _stream_ptr(dev, stream)), "qk_norm_rope_append")
+    return q_out
+
+
+# ---------------------------------------------------------------------------
+# trees of drafted tokens
+# ---------------------------------------------------------------------------
+def tree_masks(parents: torch.Tensor, query_start: torch.Tensor, max_query_len: int, *,
+               out: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """tree_mask of ``paged_tree_attention`` (int64 [T, ceil(max_query_len /
+    64)]) from the drafts' parents: int32 [T], the index within the sequence
+    of each draft's parent, which comes before it, or -1 for a child of the
+    context.  Row i gets the bits of i and its ancestors."""
+    dev = _dev(parents, query_start)
+    if parents.dtype != torch.int32 or query_start.dtype != torch.int32 or parents.dim() != 1 \
+            or query_start.dim() != 1 or query_start.shape[0] < 1:
+        raise TypeError("parents int32 [T] and query_start int32 [S + 1]")
+    T, words = parents.shape[0], (max_query_len + 63) // 64
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.zeros(T, words, dtype=torch.int64, device=dev)
+    elif out.dtype != torch.int64 or out.shape != (T, words) or _dev(out) != dev:
+        raise ValueError("out must be int64 [T, ceil(max_query_len / 64)]")
+    with _On(dev):
+        _check(_tree_masks(_p(out), _p(parents), _p(query_start), query_start.shape[0] - 1, T, int(max_query_len),
+                           _stream_ptr(dev, stream)), "tree_masks")
+    return out
+
+
+def tree_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_query_len: int,
+                         max_context_len: int) -> int:
+    """Workspace bytes of paged_tree_attention (0: none needed)."""
+    return int(_tree_ws(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len, max_context_len))
+
+
+def paged_tree_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                         tree_mask: torch.Tensor, scale: float, *, max_query_len: Optional[int] = None,
+                         max_context_len: Optional[int] = None, workspace: Optional[torch.Tensor] = None,
+                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of drafted tokens that form a tree over their context: every
+    row sees the context, and draft j of its own sequence if bit j % 64 of
+    tree_mask[row, j // 64] is set; see include/pagedkv.h.
+
+    q, out: bf16 [T, Hq, D], sequence s owning rows query_start[s] ..
+    query_start[s+1]-1, its drafts already in the cache at its last positions;
+    context_lens counts them.  tree_mask: int64 [T, W] (``tree_masks`` makes
+    it from parents).  A row that sees nothing yields zeros.  ``max_query_len``
+    and ``max_context_len`` default to the maxima of the device arrays (a
+    sync).  ``workspace``: at least ``tree_workspace_bytes(...)`` bytes, no
+    initial value needed; calls that may overlap must not share it."""
+    dev = _dev(out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask)
+    if q.dtype != torch.bfloat16 or not (out.dtype == k_cache.dtype == v_cache.dtype == q.dtype):
+        raise TypeError("tree attention is bf16")
+    if not (query_start.dtype == context_lens.dtype == block_tables.dtype == torch.int32):
+        raise TypeError("query_start, context_lens and block_tables are int32")
+    if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]:
+        raise TypeError("tree_mask must be int64 [T, W]")
+    if q.dim() != 3 or out.shape != q.shape or k_cache.dim() != 4:
+        raise ValueError("expected q, out [T, Hq, D] and caches [NB, Hkv, 16, D]")
+    S = context_lens.shape[0]
+    T, Hq, D = q.shape
+    NB, Hkv, P, D2 = k_cache.shape
+    if query_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("query_start must be [S + 1] and block_tables [S, maxB]")
+    if P != BLOCK_SIZE or D2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("caches must be [NB, Hkv, 16, D] with q's head_dim")
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    with _On(dev):
+        ws, ws_bytes = _workspace(_tree_ws(S, Hq, Hkv, D, max_query_len, max_context_len), workspace, dev, stream)
+        _check(_tree(_p(out), _p(q), _p(k_cache), _p(v_cache), _p(block_tables), _p(context_lens), _p(query_start),
+                     _p(tree_mask), tree_mask.shape[1], float(scale), Hkv, S, Hq, D,
+                     block_tables.shape[1] if S else 1, NB, T, int(max_query_len), int(max_context_len), PKV_BF16,
+                     _p(ws), ws_bytes, _stream_ptr(dev, stream)), "paged_tree_attention")
+    return out
+
+
+def kv_accept_layers(k_caches, v_caches, block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     query_start: torch.Tensor, accepted: torch.Tensor, num_accepted: torch.Tensor,
+                     new_lens: torch.Tensor, *, stream: Optional[torch.cuda.Stream] = None,
+                     ptrs=None) -> torch.Tensor:
+    """Moves the accepted drafts' keys and values to consecutive positions
+    behind the context, in every layer's caches, and sets the new lengths:
+    position base + accepted[s, j] -> base + j for j < num_accepted[s], base =
+    context_lens[s] minus the sequence's drafts; new_lens[s] = base +
+    num_accepted[s].
+
+    k_caches, v_caches: lists of [NB, Hkv, 16, D] CUDA tensors (bf16 or fp32),
+    one per layer; accepted int32 [S, M], M at most MAX_ACCEPTED;
+    num_accepted and new_lens int32 [S], new_lens another tensor than
+    context_lens.  ``ptrs``: optional prebuilt (k_caches, v_caches) pointer
+    arrays from ``layer_pointers``."""
+    if len(k_caches) != len(v_caches):
+        raise ValueError("one K and one V cache per layer")
+    if not k_caches:
+        return new_lens
+    dev = _dev(k_caches[0], block_tables, context_lens, query_start, accepted, num_accepted, new_lens)
+    shape, dtype = k_caches[0].shape, k_caches[0].dtype
+    for t in (*k_caches, *v_caches):
+        if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError("every layer's caches must be contiguous, on one device and of one shape and dtype")
+    NB, Hkv, D, dt = _pool_shape(k_caches[0])
+    if dt == PKV_E4M3:
+        raise TypeError("unsupported dtype: bf16 or fp32")
+    for t in (block_tables, context_lens, query_start, accepted, num_accepted, new_lens):
+        if t.dtype != torch.int32:
+            raise TypeError("the metadata tensors are int32")
+    S = context_lens.shape[0]
+    if accepted.dim() != 2 or accepted.shape[0] != S or num_accepted.shape != (S,) or new_lens.shape != (S,) \
+            or query_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("expected accepted [S, M], num_accepted and new_lens [S], query_start [S + 1], "
+                         "block_tables [S, maxB]")
+    st = stream if stream is not None else torch.cuda.current_stream(dev)
+    with _On(dev):
+        if ptrs is None:
+            with torch.cuda.stream(st):   # the pointer arrays are copied in on the launch stream
+                ptrs = (_ptr_array(k_caches, dev), _ptr_array(v_caches, dev))
+        _check(_accept(_p(ptrs[0]), _p(ptrs[1]), len(k_caches), _p(block_tables), _p(context_lens), _p(query_start),
+                       _p(accepted) if accepted.shape[1] else None, accepted.shape[1], _p(num_accepted),
+                       _p(new_lens), S, Hkv, D, max(1, block_tables.shape[1]), NB, dt, st.cuda_stream),
+               "kv_accept_layers")
+    return new_lens
 
 
 def validate(block_tables: torch.Tensor, context_lens: torch.Tensor, num_blocks: int, max_context_len: int,

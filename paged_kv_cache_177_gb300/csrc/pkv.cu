@@ -15,6 +15,9 @@
 #include "pagedkv.h"
 #include "pkv_kernels.cuh"
 #include "pkv_prefill_tc.cuh"
+#include "pkv_e4m3.cuh"
+#include "pkv_rope.cuh"
+#include "pkv_tree.cuh"
 
 namespace {
 
@@ -62,6 +65,14 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int elem_bytes(pkv_dtype dt) { return dt == PKV_BF16 ? 2 : 4; }
 
 bool dtype_ok(pkv_dtype dt) { return dt == PKV_BF16 || dt == PKV_F32; }
+
+// Whole blocks also move in the 8-bit format, whose tiles carry their scales.
+bool move_dtype_ok(pkv_dtype dt) { return dtype_ok(dt) || dt == PKV_E4M3; }
+
+// 16-byte vectors of one (block, kv head) tile.
+int64_t tile_vecs(pkv_dtype dt, int head_dim) {
+    return dt == PKV_E4M3 ? PKV_E4M3_TILE_BYTES(head_dim) / 16 : (int64_t)head_dim * elem_bytes(dt);
+}
 
 // The storage type of q and the caches for a decode dtype (PKV_BF16_OUT_F32
 // reads bf16 and writes fp32).
@@ -559,7 +570,7 @@ int move_impl(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const vo
               const void *src_v_cache, int src_num_blocks, const int64_t *src_dst_pairs, int num_pairs,
               int num_kv_heads, int head_dim, pkv_dtype dtype, void *stream, bool check_only) {
     if (num_pairs < 0 || num_kv_heads <= 0 || src_num_blocks <= 0 || dst_num_blocks <= 0) return PKV_ERR_ARG;
-    if (!dtype_ok(dtype)) return PKV_ERR_UNSUPPORTED;
+    if (!move_dtype_ok(dtype)) return PKV_ERR_UNSUPPORTED;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PKV_OK;
     if (num_pairs > 65535) return PKV_ERR_UNSUPPORTED;
@@ -574,7 +585,7 @@ int move_impl(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const vo
     m.dst[1] = static_cast<uint4 *>(dst_v_cache);
     m.src_num_blocks = src_num_blocks;
     m.dst_num_blocks = dst_num_blocks;
-    m.vec_per_block = (int64_t)num_kv_heads * 16 * head_dim * elem_bytes(dtype) / 16;
+    m.vec_per_block = num_kv_heads * tile_vecs(dtype, head_dim);
     const int threads = 256;
     int64_t chunks = (m.vec_per_block + threads * 4 - 1) / (threads * 4);
     if (chunks > 1024) chunks = 1024;
@@ -597,7 +608,7 @@ int swap_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const 
 int copy_blocks_layers(void *const *k_caches, void *const *v_caches, int num_layers, const int64_t *src_dst_pairs,
                        int num_pairs, int num_kv_heads, int head_dim, int num_blocks, pkv_dtype dtype, void *stream) {
     if (num_pairs < 0 || num_layers < 0 || num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_ARG;
-    if (!dtype_ok(dtype)) return PKV_ERR_UNSUPPORTED;
+    if (!move_dtype_ok(dtype)) return PKV_ERR_UNSUPPORTED;
     if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
     if (num_pairs == 0 || num_layers == 0) return PKV_OK;
     if (num_pairs > 65535 || num_layers > 32767) return PKV_ERR_UNSUPPORTED;
@@ -608,7 +619,7 @@ int copy_blocks_layers(void *const *k_caches, void *const *v_caches, int num_lay
     m.dst_k_layers = reinterpret_cast<uint4 *const *>(k_caches);
     m.dst_v_layers = reinterpret_cast<uint4 *const *>(v_caches);
     m.src_num_blocks = m.dst_num_blocks = num_blocks;
-    m.vec_per_block = (int64_t)num_kv_heads * 16 * head_dim * elem_bytes(dtype) / 16;
+    m.vec_per_block = num_kv_heads * tile_vecs(dtype, head_dim);
     const int threads = 256;
     int64_t chunks = (m.vec_per_block + threads * 4 - 1) / (threads * 4);
     if (chunks > 1024) chunks = 1024;
@@ -1046,3 +1057,5 @@ extern "C" int paged_decode_step(void *out, const void *q, void *k_cache, void *
                            partition_tokens, workspace, workspace_bytes, stream,
                            num_tokens > 0 ? kLaunchAfterAppend : kLaunch);
 }
+
+#include "pkv_serving.cuh"

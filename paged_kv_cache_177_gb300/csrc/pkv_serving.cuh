@@ -1,0 +1,280 @@
+// pkv_serving.cuh -- host side of the serving calls around the cache: the
+// 8-bit cache, the pass from the projections to the cache, and trees of
+// drafted tokens. Included by pkv.cu, whose helpers it uses.
+#pragma once
+
+namespace {
+
+// Arguments that every call over [num_blocks][num_kv_heads] tiles shares.
+int check_pool(int num_kv_heads, int num_blocks, int head_dim) {
+    if (num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_ARG;
+    if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+    if (num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if ((int64_t)num_blocks * num_kv_heads * 16 >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+// The arguments that the attention calls share, into p.
+int attention_params(pkv::DecodeParams &p, void *out, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_tables, const int32_t *context_lens, float scale, int num_kv_heads,
+                     int num_seqs, int num_q_heads, int head_dim, int max_blocks_per_seq, int num_blocks,
+                     int max_context_len, int max_group) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
+        max_context_len < 0)
+        return PKV_ERR_ARG;
+    int rc;
+    if ((rc = check_pool(num_kv_heads, num_blocks, head_dim)) != PKV_OK) return rc;
+    if (num_q_heads % num_kv_heads != 0) return PKV_ERR_ARG;
+    if (num_q_heads / num_kv_heads > max_group) return PKV_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return PKV_ERR_ARG;
+    if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq > INT32_MAX / 16) return PKV_ERR_UNSUPPORTED;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_q_heads / num_kv_heads;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_blocks = num_blocks;
+    p.max_context_len = max_context_len;
+    return PKV_OK;
+}
+
+template <typename T>
+int launch_append_e4m3(const void *k, const void *v, const int64_t *slots, void *kc, void *vc, int num_tokens,
+                       int num_kv_heads, int head_dim, int num_blocks, cudaStream_t st) {
+    const int threads = 256;
+    const long long blocks = ((long long)num_tokens * num_kv_heads * (head_dim / 8) + threads - 1) / threads;
+    if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    auto kern = head_dim == 128 ? pkv::kv_append_e4m3_kernel<T, 128> : pkv::kv_append_e4m3_kernel<T, 64>;
+    kern<<<(unsigned)blocks, threads, 0, st>>>(static_cast<const T *>(k), static_cast<const T *>(v), slots,
+                                               static_cast<uint8_t *>(kc), static_cast<uint8_t *>(vc), num_tokens,
+                                               num_kv_heads, num_blocks);
+    return check_launch();
+}
+
+template <typename T>
+int launch_dequantize(void *dk, void *dv, int dst_nb, const void *sk, const void *sv, int src_nb,
+                      const int64_t *pairs, int num_pairs, int num_kv_heads, int head_dim, cudaStream_t st) {
+    auto kern = head_dim == 128 ? pkv::dequantize_blocks_kernel<T, 128> : pkv::dequantize_blocks_kernel<T, 64>;
+    kern<<<dim3(num_pairs, num_kv_heads), 2 * head_dim, 0, st>>>(
+        static_cast<T *>(dk), static_cast<T *>(dv), static_cast<const uint8_t *>(sk),
+        static_cast<const uint8_t *>(sv), pairs, num_kv_heads, src_nb, dst_nb);
+    return check_launch();
+}
+
+template <typename T, int D>
+int launch_rope(const pkv::RopeParams &p, bool interleaved, bool e4m3, cudaStream_t st) {
+    auto kern = interleaved ? (e4m3 ? pkv::qk_norm_rope_append_kernel<T, D, true, true>
+                                    : pkv::qk_norm_rope_append_kernel<T, D, true, false>)
+                            : (e4m3 ? pkv::qk_norm_rope_append_kernel<T, D, false, true>
+                                    : pkv::qk_norm_rope_append_kernel<T, D, false, false>);
+    const int lanes = (p.num_q_heads + 2 * p.num_kv_heads) * (D / 8);
+    const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
+    kern<<<p.num_tokens, threads, 0, st>>>(p);
+    return check_launch();
+}
+
+}  // namespace
+
+extern "C" {
+
+int kv_append_e4m3(const void *k, const void *v, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                   int num_tokens, int num_kv_heads, int head_dim, int num_blocks, pkv_dtype dtype, void *stream) {
+    if (num_tokens < 0) return PKV_ERR_ARG;
+    int rc;
+    if ((rc = check_pool(num_kv_heads, num_blocks, head_dim)) != PKV_OK) return rc;
+    if (!dtype_ok(dtype)) return PKV_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache) return PKV_ERR_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == PKV_BF16 ? launch_append_e4m3<__nv_bfloat16>(k, v, slot_mapping, k_cache, v_cache, num_tokens,
+                                                                 num_kv_heads, head_dim, num_blocks, st)
+                             : launch_append_e4m3<float>(k, v, slot_mapping, k_cache, v_cache, num_tokens,
+                                                         num_kv_heads, head_dim, num_blocks, st);
+}
+
+int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const void *src_k_cache,
+                      const void *src_v_cache, int src_num_blocks, const int64_t *src_dst_pairs, int num_pairs,
+                      int num_kv_heads, int head_dim, pkv_dtype dst_dtype, void *stream) {
+    if (num_pairs < 0 || dst_num_blocks <= 0) return PKV_ERR_ARG;
+    int rc;
+    if ((rc = check_pool(num_kv_heads, src_num_blocks, head_dim)) != PKV_OK) return rc;
+    if ((rc = check_pool(num_kv_heads, dst_num_blocks, head_dim)) != PKV_OK) return rc;
+    if (!dtype_ok(dst_dtype) || num_pairs > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+    if (num_pairs == 0) return PKV_OK;
+    if (!dst_k_cache || !dst_v_cache || !src_k_cache || !src_v_cache || !src_dst_pairs) return PKV_ERR_ARG;
+    if (!aligned16(dst_k_cache) || !aligned16(dst_v_cache) || !aligned16(src_k_cache) || !aligned16(src_v_cache))
+        return PKV_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dst_dtype == PKV_BF16
+               ? launch_dequantize<__nv_bfloat16>(dst_k_cache, dst_v_cache, dst_num_blocks, src_k_cache, src_v_cache,
+                                                  src_num_blocks, src_dst_pairs, num_pairs, num_kv_heads, head_dim, st)
+               : launch_dequantize<float>(dst_k_cache, dst_v_cache, dst_num_blocks, src_k_cache, src_v_cache,
+                                          src_num_blocks, src_dst_pairs, num_pairs, num_kv_heads, head_dim, st);
+}
+
+size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len) {
+    (void)num_seqs, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)max_context_len;
+    return 0;
+}
+
+int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                const int32_t *block_tables, const int32_t *context_lens, float scale,
+                                int num_kv_heads, int num_seqs, int num_q_heads, int head_dim, int max_blocks_per_seq,
+                                int num_blocks, int max_context_len, pkv_dtype dtype, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    pkv::DecodeParams p{};
+    int rc;
+    if ((rc = attention_params(p, out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, num_seqs,
+                               num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len, 16)) != PKV_OK)
+        return rc;
+    if (dtype != PKV_BF16 && dtype != PKV_BF16_OUT_F32) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
+    const size_t need = pkv_e4m3_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
+    const dim3 grid((num_q_heads + 3) / 4, num_seqs);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == PKV_BF16) {
+        auto kern = head_dim == 128 ? pkv::decode_e4m3_kernel<128, __nv_bfloat16>
+                                    : pkv::decode_e4m3_kernel<64, __nv_bfloat16>;
+        kern<<<grid, 128, 0, st>>>(p);
+    } else {
+        auto kern = head_dim == 128 ? pkv::decode_e4m3_kernel<128, float> : pkv::decode_e4m3_kernel<64, float>;
+        kern<<<grid, 128, 0, st>>>(p);
+    }
+    return check_launch();
+}
+
+int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
+                        int64_t v_stride, const void *q_weight, const void *k_weight, float eps,
+                        const int64_t *positions, int num_axes, const float *inv_freq, const int32_t *axes,
+                        int rot_dim, int interleaved, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                        int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int num_blocks,
+                        pkv_dtype dtype, pkv_dtype cache_dtype, void *stream) {
+    if (num_tokens < 0 || num_q_heads <= 0 || rot_dim < 0) return PKV_ERR_ARG;
+    int rc;
+    if ((rc = check_pool(num_kv_heads, num_blocks, head_dim)) != PKV_OK) return rc;
+    if (!dtype_ok(dtype) || (cache_dtype != dtype && cache_dtype != PKV_E4M3)) return PKV_ERR_UNSUPPORTED;
+    if (num_q_heads > (1 << 20) || rot_dim > head_dim || rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+    if (!q_weight != !k_weight) return PKV_ERR_ARG;
+    if (q_weight && !(eps >= 0.f && std::isfinite(eps))) return PKV_ERR_ARG;
+    const int vec = 16 / elem_bytes(dtype);
+    if (q_stride < (int64_t)num_q_heads * head_dim || k_stride < (int64_t)num_kv_heads * head_dim ||
+        v_stride < (int64_t)num_kv_heads * head_dim)
+        return PKV_ERR_ARG;
+    if (q_stride % vec != 0 || k_stride % vec != 0 || v_stride % vec != 0) return PKV_ERR_ALIGN;
+    if (num_tokens == 0) return PKV_OK;
+    if (!q_out || !q || !k || !v || !slot_mapping || !k_cache || !v_cache) return PKV_ERR_ARG;
+    if (rot_dim > 0 && (!positions || !inv_freq || num_axes <= 0)) return PKV_ERR_ARG;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(q_weight) || !aligned16(k_weight))
+        return PKV_ERR_ALIGN;
+    // rows may be turned in place only where each is read by the lanes that write it
+    if (q_out == q && q_stride != (int64_t)num_q_heads * head_dim) return PKV_ERR_OVERLAP;
+    pkv::RopeParams p{q_out, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, positions, inv_freq, axes,
+                      slot_mapping, k_cache, v_cache, eps, num_axes, rot_dim, num_tokens, num_q_heads, num_kv_heads,
+                      num_blocks};
+    const bool e4 = cache_dtype == PKV_E4M3, il = interleaved != 0;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == PKV_BF16)
+        return head_dim == 128 ? launch_rope<__nv_bfloat16, 128>(p, il, e4, st)
+                               : launch_rope<__nv_bfloat16, 64>(p, il, e4, st);
+    return head_dim == 128 ? launch_rope<float, 128>(p, il, e4, st) : launch_rope<float, 64>(p, il, e4, st);
+}
+
+int tree_masks(int64_t *tree_mask, const int32_t *parents, const int32_t *query_start, int num_seqs, int num_queries,
+               int max_query_len, void *stream) {
+    if (num_seqs < 0 || num_queries < 0 || max_query_len < 0) return PKV_ERR_ARG;
+    if (max_query_len > PKV_TREE_MAX_DRAFTS) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || num_queries == 0 || max_query_len == 0) return PKV_OK;
+    if (!tree_mask || !parents || !query_start) return PKV_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(tree_mask) & 7) != 0) return PKV_ERR_ALIGN;
+    pkv::tree_masks_kernel<<<num_seqs, 64, 0, static_cast<cudaStream_t>(stream)>>>(
+        tree_mask, parents, query_start, num_queries, max_query_len, (max_query_len + 63) / 64);
+    return check_launch();
+}
+
+size_t pkv_tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_query_len,
+                                int max_context_len) {
+    (void)num_seqs, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)max_query_len, (void)max_context_len;
+    return 0;
+}
+
+int paged_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
+                         const int32_t *block_tables, const int32_t *context_lens, const int32_t *query_start,
+                         const int64_t *tree_mask, int mask_words, float scale, int num_kv_heads, int num_seqs,
+                         int num_q_heads, int head_dim, int max_blocks_per_seq, int num_blocks, int num_queries,
+                         int max_query_len, int max_context_len, pkv_dtype dtype, void *workspace,
+                         size_t workspace_bytes, void *stream) {
+    pkv::TreeParams tp{};
+    int rc;
+    if ((rc = attention_params(tp.d, out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
+                               num_seqs, num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len,
+                               64)) != PKV_OK)
+        return rc;
+    if (max_query_len < 0 || num_queries < 0 || mask_words < (max_query_len + 63) / 64) return PKV_ERR_ARG;
+    if (dtype != PKV_BF16 || max_query_len > PKV_TREE_MAX_DRAFTS) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_query_len == 0 || num_queries == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start || !tree_mask)
+        return PKV_ERR_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
+    if ((reinterpret_cast<uintptr_t>(tree_mask) & 7) != 0) return PKV_ERR_ALIGN;
+    const size_t need = pkv_tree_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_query_len,
+                                                 max_context_len);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
+    tp.query_start = query_start;
+    tp.mask = tree_mask;
+    tp.mask_words = mask_words;
+    tp.num_queries = num_queries;
+    tp.max_query_len = max_query_len;
+    const dim3 grid((unsigned)(((long long)max_query_len * num_q_heads + 3) / 4), num_seqs);
+    auto kern = head_dim == 128 ? pkv::tree_attention_kernel<128> : pkv::tree_attention_kernel<64>;
+    kern<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(tp);
+    return check_launch();
+}
+
+int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layers, const int32_t *block_tables,
+                     const int32_t *context_lens, const int32_t *query_start, const int32_t *accepted,
+                     int max_accepted, const int32_t *num_accepted, int32_t *new_lens, int num_seqs,
+                     int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, pkv_dtype dtype,
+                     void *stream) {
+    if (num_layers < 0 || num_seqs < 0 || max_accepted < 0 || max_blocks_per_seq <= 0) return PKV_ERR_ARG;
+    int rc;
+    if ((rc = check_pool(num_kv_heads, num_blocks, head_dim)) != PKV_OK) return rc;
+    if (!dtype_ok(dtype) || max_accepted > PKV_MAX_ACCEPTED || num_layers > 65535 || num_seqs > 65535 ||
+        max_blocks_per_seq > INT32_MAX / 16)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_layers == 0 || num_seqs == 0) return PKV_OK;
+    if (!k_caches || !v_caches || !block_tables || !context_lens || !query_start || !num_accepted || !new_lens ||
+        (max_accepted > 0 && !accepted))
+        return PKV_ERR_ARG;
+    if (new_lens < context_lens + num_seqs && context_lens < new_lens + num_seqs) return PKV_ERR_OVERLAP;
+    pkv::AcceptParams p{k_caches, v_caches, block_tables, context_lens, query_start, accepted, num_accepted, new_lens,
+                        max_accepted, num_kv_heads, max_blocks_per_seq, num_blocks,
+                        head_dim * elem_bytes(dtype) / 16};
+    const size_t smem = (size_t)2 * max_accepted * p.row_vecs * 16;  // at most 64 KiB
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    if (configured_device != dev) {
+        if (cudaFuncSetAttribute(pkv::kv_accept_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 2 * PKV_MAX_ACCEPTED * 128 * 4) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured_device = dev;
+    }
+    pkv::kv_accept_kernel<<<dim3(num_kv_heads, num_layers, num_seqs), 128, smem, static_cast<cudaStream_t>(stream)>>>(
+        p);
+    return check_launch();
+}
+
+}  // extern "C"
