@@ -69,6 +69,79 @@ int launch_dequantize(void *dk, void *dv, int dst_nb, const void *sk, const void
     return check_launch();
 }
 
+// Decode over e4m3 tiles: the persistent kernel's shape, workers and their ring.
+#ifndef PKV_E4M3_WARPS
+#define PKV_E4M3_WARPS 12
+#endif
+#ifndef PKV_E4M3_STAGES
+#define PKV_E4M3_STAGES 4
+#endif
+constexpr int kE4m3Warps = PKV_E4M3_WARPS;
+
+// Contexts this short are not cut: a worker takes whole (sequence, kv head) units and writes
+// their outputs itself, so no merge is launched.
+bool e4m3_whole_units(int max_context_len) { return max_context_len <= 256; }
+
+// 3-D view of an e4m3 cache: x = code within a row, y = slot (16, so rows before the tile read as
+// zeros), z = (block * Hkv + head) tile; the scale bytes behind the rows are left out. The box is the
+// tile's codes, under the swizzle of a row's width.
+int encode_e4m3_map(CUtensorMap *map, const void *cache, int num_blocks, int num_kv_heads, int head_dim) {
+    auto fn = encode_fn();
+    if (!fn) return PKV_ERR_CUDA;
+    cuuint64_t dims[3] = {(cuuint64_t)head_dim, 16, (cuuint64_t)num_blocks * num_kv_heads};
+    cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)PKV_E4M3_TILE_BYTES(head_dim)};
+    cuuint32_t box[3] = {(cuuint32_t)head_dim, 16, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <int D, int NT, typename OutT>
+int launch_decode_e4m3_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, pkv::DecodeParams &p, void *workspace,
+                             cudaStream_t st) {
+    // two column tiles need 168 registers and more: eight warps, which have them
+    constexpr int NS = PKV_E4M3_STAGES, NW = NT == 2 ? 8 : kE4m3Warps;
+    using C = pkv::E4m3Cfg<D, NS, NW>;
+    static_assert(C::smem_bytes(kPersistMaxSeqs) + 64 <= kSmemLimit, "shared memory");
+    auto kern = pkv::decode_e4m3_kernel<D, NT, NS, NW, OutT>;
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    if (configured_device != dev) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::smem_bytes(kPersistMaxSeqs)) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured_device = dev;
+    }
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    const int grid = sms < kPersistMaxCtas ? sms : kPersistMaxCtas;
+    const bool whole = e4m3_whole_units(p.max_context_len);
+    pkv::E4m3Cut *cuts = nullptr;
+    if (!whole) {
+        cuts = reinterpret_cast<pkv::E4m3Cut *>(static_cast<char *>(workspace) + kCounterBytes);
+        p.partials = reinterpret_cast<float *>(cuts + (size_t)kPersistMaxCtas * NW);
+    }
+    kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(tmk, tmv, p, cuts, whole ? 1 : 0);
+    const int rc = check_launch();
+    if (rc != PKV_OK || whole) return rc;
+    return launch_pdl(pkv::e4m3_merge_kernel<D, OutT>, dim3(grid * NW), dim3(256), 0, st, static_cast<OutT *>(p.out),
+                      static_cast<const float *>(p.partials), static_cast<const pkv::E4m3Cut *>(cuts), p.group);
+}
+
+template <typename OutT>
+int launch_decode_e4m3(const CUtensorMap &tmk, const CUtensorMap &tmv, pkv::DecodeParams &p, int head_dim,
+                       void *workspace, cudaStream_t st) {
+    if (head_dim == 128)
+        return p.group <= 8 ? launch_decode_e4m3_shape<128, 1, OutT>(tmk, tmv, p, workspace, st)
+                            : launch_decode_e4m3_shape<128, 2, OutT>(tmk, tmv, p, workspace, st);
+    return p.group <= 8 ? launch_decode_e4m3_shape<64, 1, OutT>(tmk, tmv, p, workspace, st)
+                        : launch_decode_e4m3_shape<64, 2, OutT>(tmk, tmv, p, workspace, st);
+}
+
 template <typename T, int D>
 int launch_rope(const pkv::RopeParams &p, bool interleaved, bool e4m3, cudaStream_t st) {
     auto kern = interleaved ? (e4m3 ? pkv::qk_norm_rope_append_kernel<T, D, true, true>
@@ -122,8 +195,12 @@ int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, 
 }
 
 size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len) {
-    (void)num_seqs, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)max_context_len;
-    return 0;
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_q_heads % num_kv_heads != 0 ||
+        e4m3_whole_units(max_context_len))
+        return 0;
+    const size_t workers = (size_t)kPersistMaxCtas * kE4m3Warps;
+    return kCounterBytes + workers * sizeof(pkv::E4m3Cut) +
+           workers * 2 * (num_q_heads / num_kv_heads) * (2 + (size_t)head_dim) * sizeof(float);
 }
 
 int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -142,17 +219,24 @@ int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, c
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
     const size_t need = pkv_e4m3_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
-    const dim3 grid((num_q_heads + 3) / 4, num_seqs);
+    alignas(64) CUtensorMap tmk, tmv;
+    if ((rc = encode_e4m3_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    if ((rc = encode_e4m3_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == PKV_BF16) {
-        auto kern = head_dim == 128 ? pkv::decode_e4m3_kernel<128, __nv_bfloat16>
-                                    : pkv::decode_e4m3_kernel<64, __nv_bfloat16>;
-        kern<<<grid, 128, 0, st>>>(p);
-    } else {
-        auto kern = head_dim == 128 ? pkv::decode_e4m3_kernel<128, float> : pkv::decode_e4m3_kernel<64, float>;
-        kern<<<grid, 128, 0, st>>>(p);
+    // the kernel keeps the batch's block counts in shared memory: larger batches go in slices
+    for (int s0 = 0; s0 < num_seqs; s0 += kPersistMaxSeqs) {
+        pkv::DecodeParams ps = p;
+        const size_t row = (size_t)s0 * num_q_heads * head_dim;
+        ps.out = static_cast<char *>(out) + row * (dtype == PKV_BF16 ? 2 : 4);
+        ps.q = static_cast<const char *>(q) + row * 2;
+        ps.block_tables = block_tables + (size_t)s0 * max_blocks_per_seq;
+        ps.context_lens = context_lens + s0;
+        ps.num_seqs = num_seqs - s0 < kPersistMaxSeqs ? num_seqs - s0 : kPersistMaxSeqs;
+        rc = dtype == PKV_BF16 ? launch_decode_e4m3<__nv_bfloat16>(tmk, tmv, ps, head_dim, workspace, st)
+                               : launch_decode_e4m3<float>(tmk, tmv, ps, head_dim, workspace, st);
+        if (rc != PKV_OK) return rc;
     }
-    return check_launch();
+    return PKV_OK;
 }
 
 int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v, int64_t q_stride, int64_t k_stride,
