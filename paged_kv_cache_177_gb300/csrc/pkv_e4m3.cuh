@@ -16,6 +16,11 @@
 
 namespace pkv {
 
+template <int N>
+struct IntConst {  // a compile-time number passed to a generic lambda
+    static constexpr int value = N;
+};
+
 constexpr int kE4m3ExpLo = -50, kE4m3ExpHi = 50;  // range of a row's scale exponent
 
 // Two floats to two e4m3 codes (a in the low byte), nearest even, saturating; NaN to NaN.
@@ -178,7 +183,7 @@ __global__ void __launch_bounds__(2 * D)
 // NW warps, each an independent worker with its own ring of NS stages; all (sequence, kv head)
 // units' blocks form one line of T positions, cut into equal ranges, one per worker.
 //
-// The step over one staged (K, V) block, for the group's query heads as the MMA's N:
+// The step over staged (K, V) blocks, for the group's query heads as the MMA's N:
 //   x_t = (scale log2 e) 2^(ek_t + eq) <codes K_t, q'>      q = q' 2^eq, q' in f16
 //   y_t = x_t + ev_t;   m' = max(m, max_t y_t);   w_t = 2^(y_t - m')
 //   l = l 2^(m - m') + sum_t 2^(x_t - m');   O = O 2^(m - m') + sum_t w_t codes V_t
@@ -189,33 +194,39 @@ __global__ void __launch_bounds__(2 * D)
 // matter most, whatever the rows' scales. A row's exponent lies in [-50, 50], so sum 2^(x - m')
 // neither overflows nor loses a term that counts.
 //
-// Codes come from shared memory by ldmatrix as pairs of bytes: a 16-byte chunk of a K row is the 16
-// contraction elements of one MMA (4 t4 .. 4 t4 + 3 in lane t4: the order within a contraction
-// is free as long as q's fragment has it too), and a transposed chunk of V holds two elements of
-// two tokens a register, which one byte permutation sorts into the even and odd rows of O.
+// A tile, codes and scales, is one contiguous run of 16 (D + 1) bytes and comes by one untiled bulk
+// copy: the runs start at any multiple of 16 bytes, and a tiled copy of 128-byte rows from such a
+// start asks L2 for two lines a row (with the arithmetic left out it took 124 us where the
+// bulk copies took 115 us on 256 sequences of 8 heads, 715 MB). So the rows lie in shared memory
+// as in the cache, and fragments are read 16 bytes a lane in the order the MMAs can take them:
+//   K: lane t4 holds chunks t4 and t4 + 4 of its token's row, four codes of each for every MMA (the order of
+//      a contraction is free as long as q's fragment has it too);
+//   V: lane (gq, t4) holds codes (D/8) gq .. of tokens 2 t4, + 1, + 8, + 9; a byte permutation pairs
+//      two tokens' codes of one element, and the MMAs' rows take the lane's elements two by two.
+// These reads meet two- and four-way bank conflicts, 96 shared-memory cycles a block (D = 128) of the
+// about 170 that its bytes take from HBM at one SM's share.
 // =====================================================================================
 template <int D, int NT>
 struct WarpAttnE4m3 {
-    static constexpr int kChunks = D / 16;  // 16-byte chunks of a row = MMAs of a block's QK^T, and of its PV
-    using QRaw = uint2[kChunks][NT];        // q[head gq][16 c + 4 t4 .. + 3], bf16
-    float m[NT][2], l[NT][2], qs[NT][2];    // of heads 2 t4, 2 t4 + 1 of each 8 columns; qs: score scale, log2 domain
-    float acc[kChunks][NT][4];              // [.][.][e]: head 2 t4 + (e & 1), element 16 c + 2 gq + (e >> 1)
-    uint32_t qf[kChunks][NT][2];
-
-    // Shared address of 16-byte chunk c of row r: rows of D bytes under the D-byte TMA swizzle.
-    static __device__ __forceinline__ uint32_t at(uint32_t tile, int r, int c) {
-        return tile + r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
-    }
+    static constexpr int kMmas = D / 16;     // of a block's QK^T, and of its PV
+    static constexpr int kOwn = D / 8;       // output elements of a lane, per head
+    static constexpr int kParts = D / 64;    // 16-byte chunks of a K row that a lane holds
+    using QRaw = uint4[kParts][2][NT];       // q[head gq][64 j + 16 t4 .. + 15], bf16
+    float m[NT][2], l[NT][2], qs[NT][2];     // of heads 2 t4, 2 t4 + 1 of each 8 columns; qs: score scale, log2 domain
+    float acc[kMmas][NT][4];                 // [i][.][e]: head 2 t4 + (e & 1), element kOwn gq + 2 i + (e >> 1)
+    uint32_t qf[kMmas][NT][2];
 
     static __device__ __forceinline__ void load_raw(QRaw &raw, const __nv_bfloat16 *q_group, int g, int lane) {
         const int gq = lane >> 2, t4 = lane & 3;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int hl = nt * 8 + gq;
-            const __nv_bfloat16 *row = q_group + (size_t)(hl < g ? hl : 0) * D + 4 * t4;
+            const uint4 *row = reinterpret_cast<const uint4 *>(q_group + (size_t)(hl < g ? hl : 0) * D + 16 * t4);
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                raw[c][nt] = hl < g ? __ldg(reinterpret_cast<const uint2 *>(row + 16 * c)) : make_uint2(0u, 0u);
+            for (int j = 0; j < kParts; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    raw[j][i][nt] = hl < g ? __ldg(row + 8 * j + i) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
 
@@ -226,30 +237,31 @@ struct WarpAttnE4m3 {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             float top = 0.f;
+            auto each = [&](auto f) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const uint32_t w[2] = {raw[c][nt].x, raw[c][nt].y};
+                for (int j = 0; j < kParts; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float a = fabsf(__uint_as_float(w[i] << 16)), b = fabsf(__uint_as_float(w[i] & 0xffff0000u));
-                    top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
-                }
-            }
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w[4] = {raw[j][i][nt].x, raw[j][i][nt].y, raw[j][i][nt].z, raw[j][i][nt].w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // elements 64 j + 16 t4 + 8 i + 2 k, + 1
+                            f(4 * j + 2 * i + (k >> 1), k & 1, __uint_as_float(w[k] << 16),
+                              __uint_as_float(w[k] & 0xffff0000u));
+                    }
+            };
+            each([&](int, int, float a, float b) {
+                a = fabsf(a), b = fabsf(b);
+                top = fmaxf(top, fmaxf(a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f));
+            });
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // exponent of the scale, kept where both it and its reciprocal are normal numbers
             const int e = top > 0.f ? max(-100, min(113, (int)(__float_as_uint(top) >> 23) - 127 - 13)) : 0;
             const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                const uint32_t w[2] = {raw[c][nt].x, raw[c][nt].y};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const __half2 h = __floats2half2_rn(__uint_as_float(w[i] << 16) * inv,
-                                                        __uint_as_float(w[i] & 0xffff0000u) * inv);
-                    qf[c][nt][i] = *reinterpret_cast<const uint32_t *>(&h);
-                }
-            }
+            each([&](int mma, int r, float a, float b) {
+                const __half2 h = __floats2half2_rn(a * inv, b * inv);
+                qf[mma][nt][r] = *reinterpret_cast<const uint32_t *>(&h);
+            });
             const float sc = __uint_as_float((uint32_t)(127 + e) << 23) * scale_log2;  // of head gq
             qs[nt][0] = __shfl_sync(0xffffffffu, sc, 8 * t4);
             qs[nt][1] = __shfl_sync(0xffffffffu, sc, 8 * t4 + 4);
@@ -262,89 +274,132 @@ struct WarpAttnE4m3 {
             m[nt][0] = m[nt][1] = -INFINITY;
             l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
+            for (int i = 0; i < kMmas; ++i)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[c][nt][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
         }
     }
 
-    // One staged block. Rows below lo are not tokens (the tile was loaded lo rows early and they are
-    // zeros); kb, vb: scale bytes of this lane's two token rows gq and gq + 8.
-    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, const uint32_t (&kb)[2], const uint32_t (&vb)[2],
-                                          int lo, int lane) {
-        const int gq = lane >> 2, mi = lane >> 3, r8 = lane & 7;
-        const int row = r8 + (mi & 1) * 8;  // of this lane's ldmatrix addresses, K and V alike
-        float sc[NT][4], sb[NT][4];
+    // NB staged blocks of one unit: one softmax update, and enough independent MMAs to keep the
+    // tensor pipe fed from three warps a scheduler. Rows of the last block from `valid` on are not
+    // tokens. tile: shared address of each block's K tile, its V tile one tile further.
+    template <int NB>
+    __device__ __forceinline__ void blocks(const uint32_t (&tile)[NB], int valid, int lane) {
+        constexpr int kTile = PKV_E4M3_TILE_BYTES(D);
+        const int gq = lane >> 2, t4 = lane & 3;
+        float sc[NB][NT][4], sb[NB][NT][4];
+        uint32_t kb[NB][2], vb[NB][2];  // scale bytes of this lane's two token rows gq and gq + 8
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t at = tile[b] + kBlock * D + gq;
+            kb[b][0] = ld_shared_u8(at), kb[b][1] = ld_shared_u8(at + 8);
+            vb[b][0] = ld_shared_u8(at + kTile), vb[b][1] = ld_shared_u8(at + kTile + 8);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[nt][e] = sb[nt][e] = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < kChunks; c += 2) {
-            uint32_t k[4];
-            ldsm_x4(at(sk, row, c + (mi >> 1)), k);
-            const uint32_t a0[4] = {cvt_f16x2_e4m3x2(k[0]), cvt_f16x2_e4m3x2(k[1]), cvt_f16x2_e4m3x2(k[0] >> 16),
-                                    cvt_f16x2_e4m3x2(k[1] >> 16)};
-            const uint32_t a1[4] = {cvt_f16x2_e4m3x2(k[2]), cvt_f16x2_e4m3x2(k[3]), cvt_f16x2_e4m3x2(k[2] >> 16),
-                                    cvt_f16x2_e4m3x2(k[3] >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_f16_16816(sc[nt], a0, qf[c][nt][0], qf[c][nt][1]);
-                mma_f16_16816(sb[nt], a1, qf[c + 1][nt][0], qf[c + 1][nt][1]);
-            }
+                for (int e = 0; e < 4; ++e) sc[b][nt][e] = sb[b][nt][e] = 0.f;
         }
-        const bool v0 = gq >= lo, v1 = gq + 8 >= lo;
-        const float k0 = e8m0_value(kb[0]), k1 = e8m0_value(kb[1]);
-        const float ev0 = (float)((int)vb[0] - 127), ev1 = (float)((int)vb[1] - 127);
-        uint32_t p0[NT], p1[NT];
+#pragma unroll
+        for (int j = 0; j < kParts; ++j)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t k0[4], k1[4];
+                const uint32_t at = tile[b] + gq * D + 64 * j + 16 * t4;
+                ld_shared_v4(at, k0);
+                ld_shared_v4(at + 8 * D, k1);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t a[4] = {cvt_f16x2_e4m3x2(k0[w]), cvt_f16x2_e4m3x2(k1[w]),
+                                           cvt_f16x2_e4m3x2(k0[w] >> 16), cvt_f16x2_e4m3x2(k1[w] >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_f16_16816(w & 1 ? sb[b][nt] : sc[b][nt], a, qf[4 * j + w][nt][0], qf[4 * j + w][nt][1]);
+                }
+            }
+        float kv[NB][2], ev[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                kv[b][i] = e8m0_value(kb[b][i]);
+                ev[b][i] = __uint_as_float(0x4b000000u | vb[b][i]) - (8388608.f + 127.f);  // byte - 127
+            }
+        uint32_t p0[NB][NT], p1[NB][NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float x[4], y[4];
+            float x[NB][4], y[NB][4], mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool ok = e < 2 ? v0 : v1;
-                x[e] = ok ? (sc[nt][e] + sb[nt][e]) * (e < 2 ? k0 : k1) * qs[nt][e & 1] : -INFINITY;
-                y[e] = ok ? x[e] + (e < 2 ? ev0 : ev1) : -INFINITY;
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[b][e] = (sc[b][nt][e] + sb[b][nt][e]) * kv[b][e >> 1] * qs[nt][e & 1];
+                    y[b][e] = x[b][e] + ev[b][e >> 1];
+                    if (b == NB - 1 && gq + 8 * (e >> 1) >= valid) x[b][e] = y[b][e] = -INFINITY;
+                }
+                mx0 = max3f(mx0, y[b][0], y[b][2]);
+                mx1 = max3f(mx1, y[b][1], y[b][3]);
             }
-            float mx0 = fmaxf(y[0], y[2]), mx1 = fmaxf(y[1], y[3]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
             }
-            const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);  // finite: a block holds a token
-            const float al0 = ex2_approx(m[nt][0] - mn0), al1 = ex2_approx(m[nt][1] - mn1);
-            m[nt][0] = mn0;
-            m[nt][1] = mn1;
-            l[nt][0] = l[nt][0] * al0 + (ex2_approx(x[0] - mn0) + ex2_approx(x[2] - mn0));
-            l[nt][1] = l[nt][1] * al1 + (ex2_approx(x[1] - mn1) + ex2_approx(x[3] - mn1));
-            const __half2 w0 = __floats2half2_rn(ex2_approx(y[0] - mn0), ex2_approx(y[1] - mn1));
-            const __half2 w1 = __floats2half2_rn(ex2_approx(y[2] - mn0), ex2_approx(y[3] - mn1));
+            // finite: a block holds a token
+            const bool up = mx0 > m[nt][0] || mx1 > m[nt][1];
+            if (__any_sync(0xffffffffu, up)) {  // (most blocks move no maximum)
+                const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);
+                const float al0 = ex2_approx(m[nt][0] - mn0), al1 = ex2_approx(m[nt][1] - mn1);
+                m[nt][0] = mn0;
+                m[nt][1] = mn1;
+                l[nt][0] *= al0;
+                l[nt][1] *= al1;
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-                acc[c][nt][0] *= al0;
-                acc[c][nt][1] *= al1;
-                acc[c][nt][2] *= al0;
-                acc[c][nt][3] *= al1;
+                for (int i = 0; i < kMmas; ++i) {
+                    acc[i][nt][0] *= al0;
+                    acc[i][nt][1] *= al1;
+                    acc[i][nt][2] *= al0;
+                    acc[i][nt][3] *= al1;
+                }
             }
-            p0[nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&w0));
-            p1[nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&w1));
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                l[nt][0] += ex2_approx(x[b][0] - m[nt][0]) + ex2_approx(x[b][2] - m[nt][0]);
+                l[nt][1] += ex2_approx(x[b][1] - m[nt][1]) + ex2_approx(x[b][3] - m[nt][1]);
+                const __half2 w0 = __floats2half2_rn(ex2_approx(y[b][0] - m[nt][0]), ex2_approx(y[b][1] - m[nt][1]));
+                const __half2 w1 = __floats2half2_rn(ex2_approx(y[b][2] - m[nt][0]), ex2_approx(y[b][3] - m[nt][1]));
+                p0[b][nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&w0));
+                p1[b][nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&w1));
+            }
         }
 #pragma unroll
-        for (int c = 0; c < kChunks; c += 2) {
-            uint32_t v[4];
-            ldsm_x4_trans(at(sv, row, c + (mi >> 1)), v);
+        for (int b = 0; b < NB; ++b) {
+            constexpr int kWords = kOwn / 4;
+            uint32_t v[4][kWords];  // tokens 2 t4, + 1, + 8, + 9
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = __byte_perm(v[i], 0u, 0x3120);  // (t, d) (t + 1, d) | (t, d + 1) (t + 1, d + 1)
-            const uint32_t a0[4] = {cvt_f16x2_e4m3x2(v[0]), cvt_f16x2_e4m3x2(v[0] >> 16), cvt_f16x2_e4m3x2(v[1]),
-                                    cvt_f16x2_e4m3x2(v[1] >> 16)};
-            const uint32_t a1[4] = {cvt_f16x2_e4m3x2(v[2]), cvt_f16x2_e4m3x2(v[2] >> 16), cvt_f16x2_e4m3x2(v[3]),
-                                    cvt_f16x2_e4m3x2(v[3] >> 16)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                mma_f16_16816(acc[c][nt], a0, p0[nt], p1[nt]);
-                mma_f16_16816(acc[c + 1][nt], a1, p0[nt], p1[nt]);
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t at = tile[b] + kTile + (2 * t4 + (r & 1) + 8 * (r >> 1)) * D + kOwn * gq;
+                if constexpr (kWords == 4) ld_shared_v4(at, v[r]);
+                else ld_shared_v2(at, v[r]);
             }
+            if (b == NB - 1 && valid < kBlock) {  // what is not a token may hold anything: no weight undoes a NaN
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (2 * t4 + (r & 1) + 8 * (r >> 1) >= valid) {
+#pragma unroll
+                        for (int w = 0; w < kWords; ++w) v[r][w] = 0u;
+                    }
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t lo = __byte_perm(v[0][w], v[1][w], e ? 0x7362 : 0x5140);
+                    const uint32_t hi = __byte_perm(v[2][w], v[3][w], e ? 0x7362 : 0x5140);
+                    const uint32_t a[4] = {cvt_f16x2_e4m3x2(lo), cvt_f16x2_e4m3x2(lo >> 16), cvt_f16x2_e4m3x2(hi),
+                                           cvt_f16x2_e4m3x2(hi >> 16)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_f16_16816(acc[2 * w + e][nt], a, p0[b][nt], p1[b][nt]);
+                }
         }
     }
 
@@ -370,10 +425,14 @@ struct WarpAttnE4m3 {
                 if (head >= g) continue;
                 const float inv = 1.f / l[nt][e];
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    OutT *o = rows + (size_t)head * D + 16 * c + 2 * gq;
-                    o[0] = to_out<OutT>(acc[c][nt][e] * inv);
-                    o[1] = to_out<OutT>(acc[c][nt][e + 2] * inv);
+                for (int i = 0; i < kMmas; i += 4) {
+                    float o[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = acc[i + k][nt][e] * inv;
+                        o[2 * k + 1] = acc[i + k][nt][e + 2] * inv;
+                    }
+                    store8(rows + (size_t)head * D + kOwn * gq + 2 * i, o);
                 }
             }
     }
@@ -391,22 +450,23 @@ struct WarpAttnE4m3 {
                     row[1] = l[nt][e];
                 }
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c)
-                    *reinterpret_cast<float2 *>(row + 2 + 16 * c + 2 * gq) = make_float2(acc[c][nt][e], acc[c][nt][e + 2]);
+                for (int i = 0; i < kMmas; ++i)
+                    *reinterpret_cast<float2 *>(row + 2 + kOwn * gq + 2 * i) =
+                        make_float2(acc[i][nt][e], acc[i][nt][e + 2]);
             }
     }
 };
 
 template <int D, int NS, int NW>
 struct E4m3Cfg {
-    static constexpr int kTile = kBlock * D;  // codes of one (block, head) tile
+    static constexpr int kTile = PKV_E4M3_TILE_BYTES(D);
     static constexpr int kStage = 2 * kTile;  // K, then V
     static constexpr int kThreads = NW * 32;
-    static constexpr int kScaleOff = NW * NS * kStage;               // [NW][NS] x (16 K, 16 V scale bytes)
-    static constexpr int kBarOff = kScaleOff + NW * NS * 2 * kBlock;
+    static constexpr int kBarOff = NW * NS * kStage;
     static constexpr int kPrefixOff = kBarOff + NW * NS * 8;
-    static constexpr size_t smem_bytes(int num_seqs) { return kPrefixOff + (size_t)(num_seqs + 1) * 4 + 1024; }
-    static_assert((NS & (NS - 1)) == 0 && NS <= 32, "stage index and bad-block bits");
+    static constexpr size_t smem_bytes(int num_seqs) { return kPrefixOff + (size_t)(num_seqs + 1) * 4; }
+    static_assert((NS & (NS - 1)) == 0, "stage index");
+    static_assert(kStage % 16 == 0, "bulk copies start on 16 bytes");
 };
 
 // A unit cut by the end of worker w's range, begun in it: its segments (0: none) and first output row.
@@ -416,21 +476,17 @@ struct E4m3Cut {
 
 template <int D, int NT, int NS, int NW, typename OutT>
 __global__ void __launch_bounds__(NW * 32, 1)
-    decode_e4m3_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                       const DecodeParams p, E4m3Cut *cuts, const int whole_units) {
+    decode_e4m3_kernel(const DecodeParams p, E4m3Cut *cuts, const int whole_units) {
     using C = E4m3Cfg<D, NS, NW>;
     using WA = WarpAttnE4m3<D, NT>;
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ __align__(16) uint8_t base[];
     __shared__ int warp_total[NW];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = p.num_seqs, Hkv = p.num_kv_heads, g = p.group;
-    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(base + C::kBarOff) + warp * NS;
     int *prefix = reinterpret_cast<int *>(base + C::kPrefixOff);
     OutT *out = static_cast<OutT *>(p.out);
     if (tid == 0) {
-        prefetch_tensormap(&tmk);
-        prefetch_tensormap(&tmv);
         for (int i = 0; i < NW * NS; ++i) mbar_init(full + i, 1);
         mbar_fence_init();
     }
@@ -502,16 +558,16 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
 
     // Block ids of 32 positions (lane i: the i-th from the cursor), gathered a batch ahead of use,
-    // each with 16 * kv head + the rows its tile is loaded early.
+    // each with its kv head.
     struct Batch {
-        int pb, hs;
+        int pb, h;
     };
     auto batch_of = [&](Cursor b, int count) -> Batch {
         Batch r{0, 0};
         if (lane < count) {
             cursor_advance(b, lane, prefix, Hkv);
             r.pb = __ldg(p.block_tables + (size_t)b.s * p.max_blocks_per_seq + b.j);
-            r.hs = b.h * 16 + ((b.j == b.n - 1) ? kBlock * b.n - seq_len(p, b.s, false) : 0);
+            r.h = b.h;
         }
         return r;
     };
@@ -522,10 +578,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
         nxt = batch_of(bnext, min(32, cnt - 32));
     }
     uint8_t *ring = base + warp * NS * C::kStage;
-    uint8_t *scales = base + C::kScaleOff + warp * NS * 2 * kBlock;
     const uint64_t policy = l2_evict_first();
     int issued = 0;
-    uint32_t bad = 0;  // bit of a stage whose block id is out of range: it reads as zeros
     auto issue = [&]() {
         if (issued > 0 && (issued & 31) == 0) {
             cur = nxt;
@@ -535,21 +589,27 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
         }
         const int pb = __shfl_sync(0xffffffffu, cur.pb, issued & 31);
-        const int hs = __shfl_sync(0xffffffffu, cur.hs, issued & 31);
+        const int h = __shfl_sync(0xffffffffu, cur.h, issued & 31);
         const int st = issued & (NS - 1);
-        const bool ok = pb >= 0 && pb < p.num_blocks;
-        bad = (bad & ~(1u << st)) | ((ok ? 0u : 1u) << st);
-        if (lane == 0) {
-            if (!ok) raise_error(PKV_DEVERR_BLOCK_ID);
-            const int z = ok ? pb * Hkv + (hs >> 4) : -1, y = -(hs & 15);
-            mbar_arrive_expect_tx(&full[st], C::kStage + (ok ? 2 * kBlock : 0));
-            tma_load_3d_hint(ring + st * C::kStage, &tmk, 0, y, z, &full[st], policy);
-            tma_load_3d_hint(ring + st * C::kStage + C::kTile, &tmv, 0, y, z, &full[st], policy);
-            if (ok) {
-                const size_t tail = (size_t)z * PKV_E4M3_TILE_BYTES(D) + kBlock * D;
-                bulk_load(scales + st * 2 * kBlock, static_cast<const uint8_t *>(p.k_cache) + tail, kBlock, &full[st]);
-                bulk_load(scales + st * 2 * kBlock + kBlock, static_cast<const uint8_t *>(p.v_cache) + tail, kBlock,
-                          &full[st]);
+        uint8_t *stage = ring + st * C::kStage;
+        if (pb >= 0 && pb < p.num_blocks) {
+            if (lane == 0) {
+                const size_t from = ((size_t)pb * Hkv + h) * C::kTile;
+                mbar_arrive_expect_tx(&full[st], C::kStage);
+                bulk_load_hint(stage, static_cast<const uint8_t *>(p.k_cache) + from, C::kTile, &full[st], policy);
+                bulk_load_hint(stage + C::kTile, static_cast<const uint8_t *>(p.v_cache) + from, C::kTile, &full[st],
+                               policy);
+            }
+        } else {  // a bad block id reads as zeros (scale 1)
+            for (int i = lane; i < C::kStage / 16; i += 32) {
+                const uint32_t w = i % (C::kTile / 16) == D ? 0x7f7f7f7fu : 0u;
+                reinterpret_cast<uint4 *>(stage)[i] = make_uint4(w, w, w, w);
+            }
+            fence_proxy_async_smem();  // these writes before the copy that refills the stage
+            __syncwarp();
+            if (lane == 0) {
+                raise_error(PKV_DEVERR_BLOCK_ID);
+                mbar_arrive(&full[st]);
             }
         }
         ++issued;
@@ -567,29 +627,43 @@ __global__ void __launch_bounds__(NW * 32, 1)
     E4m3Cut cut{0, 0};
     int i = 0;
     bool waited = true;
-    for (; i < cnt; ++i) {
-        const int st = i & (NS - 1);
-        const bool unit_end = c.j == c.n - 1;
+    // NB blocks from position i on, all of one unit
+    auto step = [&](auto nb_tag, int valid) -> bool {
+        constexpr int NB = decltype(nb_tag)::value;
+        uint32_t tile[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int st = (i + b) & (NS - 1);
+            if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ((i + b) / NS) & 1))) return false;
+            tile[b] = smem_u32(ring + st * C::kStage);
+        }
+        wa.template blocks<NB>(tile, valid, lane);
+        __syncwarp();  // every lane's reads of the stages are done before their refill
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+            if (issued < cnt) issue();
+        return true;
+    };
+    while (true) {
+        const bool two = i + 1 < cnt && c.j + 1 < c.n;
+        const int last_j = two ? c.j + 1 : c.j, last_i = two ? i + 1 : i;
+        const bool unit_end = last_j == c.n - 1;
         Cursor cn = c;
         int len_next = 0;
-        if (unit_end && i != cnt - 1) {  // the next unit's query and length, in flight while this block computes
+        if (unit_end && last_i != cnt - 1) {  // the next unit's query and length, in flight while these blocks compute
+            cn.j = last_j;
             cursor_advance(cn, 1, prefix, Hkv);
             WA::load_raw(raw, qbase + ((size_t)cn.s * p.num_q_heads + (size_t)cn.h * g) * D, g, lane);
             len_next = seq_len(p, cn.s, false);
         }
-        if (!(waited = __all_sync(0xffffffffu, mbar_wait(&full[st], (i / NS) & 1)))) break;
-        const int lo = unit_end ? kBlock * c.n - len : 0;
-        const uint8_t *sb = scales + st * 2 * kBlock;
-        const int r0 = max((lane >> 2) - lo, 0), r1 = max((lane >> 2) + 8 - lo, 0);
-        const bool isbad = (bad >> st) & 1;
-        const uint32_t kb[2] = {isbad ? 127u : sb[r0], isbad ? 127u : sb[r1]};
-        const uint32_t vb[2] = {isbad ? 127u : sb[kBlock + r0], isbad ? 127u : sb[kBlock + r1]};
-        const uint32_t sk = smem_u32(ring + st * C::kStage);
-        wa.block(sk, sk + C::kTile, kb, vb, lo, lane);
-        __syncwarp();  // every lane's reads of the stage are done before its refill
-        if (issued < cnt) issue();
+        const int valid = unit_end ? len - kBlock * (c.n - 1) : kBlock;  // tokens of the last of these blocks
+        waited = two ? step(IntConst<2>{}, valid) : step(IntConst<1>{}, valid);
+        if (!waited) break;
+        i = last_i;
+        c.j = last_j;
         if (!unit_end && i != cnt - 1) {
             ++c.j;
+            ++i;
             continue;
         }
         // ---- the segment ends here ----
@@ -607,6 +681,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             }
         }
         if (i == cnt - 1) break;
+        ++i;
         c = cn;
         seg_j0 = 0;
         len = len_next;
@@ -616,7 +691,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (!waited) {
         // a copy never landed: the output is unspecified; wait (bounded) for the others before leaving
         if (lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
-        for (++i; i < issued; ++i) mbar_wait(&full[i & (NS - 1)], (i / NS) & 1);
+        for (; i < issued; ++i) mbar_wait(&full[i & (NS - 1)], (i / NS) & 1);
         cut.segments = 0;
     }
     if (cuts && lane == 0) cuts[w] = cut;

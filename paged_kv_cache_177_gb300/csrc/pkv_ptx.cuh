@@ -91,22 +91,14 @@ __device__ __forceinline__ void tma_load_4d_hint(void *smem_dst, const CUtensorM
         : "memory");
 }
 
-// 3-D tiled bulk tensor load with an L2 cache policy (coordinates as for tma_load_4d).
-__device__ __forceinline__ void tma_load_3d_hint(void *smem_dst, const CUtensorMap *map, int x, int y, int z,
-                                                 uint64_t *bar, uint64_t policy) {
+// Untiled bulk copy global -> shared with an L2 cache policy: both addresses 16-byte aligned, bytes a
+// multiple of 16; completion counted in bytes on `bar`.
+__device__ __forceinline__ void bulk_load_hint(void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar,
+                                               uint64_t policy) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, "
-        "{%2, %3, %4}], [%5], %6;" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-        : "memory");
-}
-
-// Untiled bulk copy global -> shared: both addresses 16-byte aligned, bytes a multiple of 16.
-__device__ __forceinline__ void bulk_load(void *smem_dst, const void *src, uint32_t bytes, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-            smem_u32(smem_dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar))
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], "
+        "%4;" ::"r"(smem_u32(smem_dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
 
@@ -358,6 +350,12 @@ __device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t (&r)[4]) {
 }
 __device__ __forceinline__ void ld_shared_v2(uint32_t addr, uint32_t (&r)[2]) {
     asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr));
+    return r;
 }
 
 // The two bf16 of a 32-bit word as a packed fp32 pair (element at the lower

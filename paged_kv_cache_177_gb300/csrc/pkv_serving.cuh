@@ -82,26 +82,8 @@ constexpr int kE4m3Warps = PKV_E4M3_WARPS;
 // their outputs itself, so no merge is launched.
 bool e4m3_whole_units(int max_context_len) { return max_context_len <= 256; }
 
-// 3-D view of an e4m3 cache: x = code within a row, y = slot (16, so rows before the tile read as
-// zeros), z = (block * Hkv + head) tile; the scale bytes behind the rows are left out. The box is the
-// tile's codes, under the swizzle of a row's width.
-int encode_e4m3_map(CUtensorMap *map, const void *cache, int num_blocks, int num_kv_heads, int head_dim) {
-    auto fn = encode_fn();
-    if (!fn) return PKV_ERR_CUDA;
-    cuuint64_t dims[3] = {(cuuint64_t)head_dim, 16, (cuuint64_t)num_blocks * num_kv_heads};
-    cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)PKV_E4M3_TILE_BYTES(head_dim)};
-    cuuint32_t box[3] = {(cuuint32_t)head_dim, 16, 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
-}
-
 template <int D, int NT, typename OutT>
-int launch_decode_e4m3_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, pkv::DecodeParams &p, void *workspace,
-                             cudaStream_t st) {
+int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t st) {
     // two column tiles need 168 registers and more: eight warps, which have them
     constexpr int NS = PKV_E4M3_STAGES, NW = NT == 2 ? 8 : kE4m3Warps;
     using C = pkv::E4m3Cfg<D, NS, NW>;
@@ -125,7 +107,7 @@ int launch_decode_e4m3_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, pkv
         cuts = reinterpret_cast<pkv::E4m3Cut *>(static_cast<char *>(workspace) + kCounterBytes);
         p.partials = reinterpret_cast<float *>(cuts + (size_t)kPersistMaxCtas * NW);
     }
-    kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(tmk, tmv, p, cuts, whole ? 1 : 0);
+    kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(p, cuts, whole ? 1 : 0);
     const int rc = check_launch();
     if (rc != PKV_OK || whole) return rc;
     return launch_pdl(pkv::e4m3_merge_kernel<D, OutT>, dim3(grid * NW), dim3(256), 0, st, static_cast<OutT *>(p.out),
@@ -133,13 +115,12 @@ int launch_decode_e4m3_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, pkv
 }
 
 template <typename OutT>
-int launch_decode_e4m3(const CUtensorMap &tmk, const CUtensorMap &tmv, pkv::DecodeParams &p, int head_dim,
-                       void *workspace, cudaStream_t st) {
+int launch_decode_e4m3(pkv::DecodeParams &p, int head_dim, void *workspace, cudaStream_t st) {
     if (head_dim == 128)
-        return p.group <= 8 ? launch_decode_e4m3_shape<128, 1, OutT>(tmk, tmv, p, workspace, st)
-                            : launch_decode_e4m3_shape<128, 2, OutT>(tmk, tmv, p, workspace, st);
-    return p.group <= 8 ? launch_decode_e4m3_shape<64, 1, OutT>(tmk, tmv, p, workspace, st)
-                        : launch_decode_e4m3_shape<64, 2, OutT>(tmk, tmv, p, workspace, st);
+        return p.group <= 8 ? launch_decode_e4m3_shape<128, 1, OutT>(p, workspace, st)
+                            : launch_decode_e4m3_shape<128, 2, OutT>(p, workspace, st);
+    return p.group <= 8 ? launch_decode_e4m3_shape<64, 1, OutT>(p, workspace, st)
+                        : launch_decode_e4m3_shape<64, 2, OutT>(p, workspace, st);
 }
 
 template <typename T, int D>
@@ -219,9 +200,6 @@ int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, c
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
     const size_t need = pkv_e4m3_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
-    alignas(64) CUtensorMap tmk, tmv;
-    if ((rc = encode_e4m3_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
-    if ((rc = encode_e4m3_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // the kernel keeps the batch's block counts in shared memory: larger batches go in slices
     for (int s0 = 0; s0 < num_seqs; s0 += kPersistMaxSeqs) {
@@ -232,8 +210,8 @@ int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, c
         ps.block_tables = block_tables + (size_t)s0 * max_blocks_per_seq;
         ps.context_lens = context_lens + s0;
         ps.num_seqs = num_seqs - s0 < kPersistMaxSeqs ? num_seqs - s0 : kPersistMaxSeqs;
-        rc = dtype == PKV_BF16 ? launch_decode_e4m3<__nv_bfloat16>(tmk, tmv, ps, head_dim, workspace, st)
-                               : launch_decode_e4m3<float>(tmk, tmv, ps, head_dim, workspace, st);
+        rc = dtype == PKV_BF16 ? launch_decode_e4m3<__nv_bfloat16>(ps, head_dim, workspace, st)
+                               : launch_decode_e4m3<float>(ps, head_dim, workspace, st);
         if (rc != PKV_OK) return rc;
     }
     return PKV_OK;
