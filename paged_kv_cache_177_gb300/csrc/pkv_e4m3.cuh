@@ -469,14 +469,15 @@ struct E4m3Cfg {
     static_assert(kStage % 16 == 0, "bulk copies start on 16 bytes");
 };
 
-// A unit cut by the end of worker w's range, begun in it: its segments (0: none) and first output row.
+// A unit cut by the end of the range of the worker that began it: its segments (0: not cut), that worker,
+// and its first output row. One record a unit where units are fewer than workers, else one a worker.
 struct E4m3Cut {
-    int segments, row;
+    int segments, worker, row, pad;
 };
 
 template <int D, int NT, int NS, int NW, typename OutT>
 __global__ void __launch_bounds__(NW * 32, 1)
-    decode_e4m3_kernel(const DecodeParams p, E4m3Cut *cuts, const int whole_units) {
+    decode_e4m3_kernel(const DecodeParams p, E4m3Cut *cuts, const int whole_units, const int cuts_by_unit) {
     using C = E4m3Cfg<D, NS, NW>;
     using WA = WarpAttnE4m3<D, NT>;
     extern __shared__ __align__(16) uint8_t base[];
@@ -522,13 +523,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
         if (prefix[s + 1] == prefix[s]) {
             OutT *o = out + (size_t)s * p.num_q_heads * D;
             for (int i = tid; i < p.num_q_heads * D; i += C::kThreads) o[i] = to_out<OutT>(0.f);
+            if (cuts_by_unit)
+                for (int h = tid; h < Hkv; h += C::kThreads) cuts[s * Hkv + h].segments = 0;
         }
 
-    // this worker's range of positions: an equal share, or (short contexts) a share of whole units
+    // this worker's range of positions: an equal share, of no less than its ring holds, or (short contexts) a share of whole units
     const long long T = (long long)Hkv * prefix[S];
     const int all = gridDim.x * NW, w = blockIdx.x * NW + warp;
     const long long U = (long long)S * Hkv;
-    const int W = (int)min((long long)all, whole_units ? U : max(1LL, T / 2));
+    const int W = (int)min((long long)all, whole_units ? U : max(1LL, T / NS));
     long long start = 0, end = 0;
     if (w < W) {
         auto unit_begin = [&](long long u) {
@@ -540,7 +543,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     const int cnt = (int)(end - start);
     if (cnt <= 0) {
-        if (cuts && lane == 0) cuts[w].segments = 0;
+        if (cuts && !cuts_by_unit && lane == 0) cuts[w].segments = 0;
         return;
     }
     Cursor c;
@@ -624,7 +627,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     WA::load_raw(raw, qbase + ((size_t)c.s * p.num_q_heads + (size_t)c.h * g) * D, g, lane);
     wa.set_q(raw, p.scale_log2, lane);
     wa.reset();
-    E4m3Cut cut{0, 0};
+    E4m3Cut cut{0, w, 0, 0};
     int i = 0;
     bool waited = true;
     // NB blocks from position i on, all of one unit
@@ -680,6 +683,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 cut.row = (int)orow;
             }
         }
+        if (cuts_by_unit && seg_j0 == 0 && lane == 0) cuts[c.s * Hkv + c.h] = cut;
         if (i == cnt - 1) break;
         ++i;
         c = cn;
@@ -693,82 +697,59 @@ __global__ void __launch_bounds__(NW * 32, 1)
         if (lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
         for (; i < issued; ++i) mbar_wait(&full[i & (NS - 1)], (i / NS) & 1);
         cut.segments = 0;
+        if (cuts_by_unit && seg_j0 == 0 && lane == 0) cuts[c.s * Hkv + c.h] = cut;
     }
-    if (cuts && lane == 0) cuts[w] = cut;
+    if (cuts && !cuts_by_unit && lane == 0) cuts[w] = cut;
 }
 
-// Merges the states of every cut unit: one CTA per worker that began one. Up to 64 segments a warp
-// takes whole heads (the segments' loads overlap); more are shared among the warps head by head.
+// Merges the states of every cut unit, one CTA per (record, query head of the group): its warps share
+// the segments, eight in flight each, and join through shared memory.
+constexpr int kE4m3MergeWarps = 4;
 template <int D, typename OutT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kE4m3MergeWarps * 32)
     e4m3_merge_kernel(OutT *out, const float *__restrict__ partials, const E4m3Cut *__restrict__ cuts, int g) {
-    constexpr int PER = D / 32;
-    __shared__ float part[8][2 + D];
-    const int w1 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int PER = D / 32, NW = kE4m3MergeWarps;
+    __shared__ float part[NW][2 + D];
+    const int head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const E4m3Cut cut = cuts[w1];
+    const E4m3Cut cut = cuts[blockIdx.x];
     const int nseg = cut.segments;
     if (nseg <= 0) return;
-    auto row_of = [&](int k, int head) {
-        return partials + ((size_t)(2 * (w1 + k) + (k == 0 ? 1 : 0)) * g + head) * (2 + D);
+    auto row_of = [&](int k) {  // the first segment ends its worker's range, the others begin theirs
+        return partials + ((size_t)(2 * (cut.worker + k) + (k == 0 ? 1 : 0)) * g + head) * (2 + D);
     };
-    // segments first, first + step, ...: their max, weight sum and weighted outputs
-    auto gather = [&](int head, int first, int step, float &M, float &L, float (&acc)[PER]) {
-        M = -INFINITY;
-        for (int k = first + lane * step; k < nseg; k += 32 * step) M = fmaxf(M, row_of(k, head)[0]);
+    float M = -INFINITY, L = 0.f, acc[PER];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        L = 0.f;
+    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+    const int w_used = min(NW, nseg);
+    for (int k = warp + lane * NW; k < nseg; k += 32 * NW) M = fmaxf(M, row_of(k)[0]);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll 4
-        for (int k = first; k < nseg; k += step) {
-            const float *r = row_of(k, head);
-            const float f = ex2_approx(r[0] - M);
-            L = fmaf(r[1], f, L);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 8
+    for (int k = warp; k < nseg; k += NW) {
+        const float *r = row_of(k);
+        const float f = ex2_approx(r[0] - M);
+        L = fmaf(r[1], f, L);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = fmaf(r[2 + lane + 32 * i], f, acc[i]);
-        }
-    };
-    float M, L, acc[PER];
-    if (nseg <= 64) {
-        for (int head = warp; head < g; head += 8) {
-            gather(head, 0, 1, M, L, acc);
-            const float inv = 1.f / L;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                out[(size_t)(cut.row + head) * D + lane + 32 * i] = to_out<OutT>(acc[i] * inv);
-        }
-        return;
+        for (int i = 0; i < PER; ++i) acc[i] = fmaf(r[2 + lane + 32 * i], f, acc[i]);
     }
-    for (int head = 0; head < g; ++head) {
-        gather(head, warp, 8, M, L, acc);
-        if (lane == 0) {
-            part[warp][0] = M;
-            part[warp][1] = L;
+    if (lane == 0) {
+        part[warp][0] = M;
+        part[warp][1] = L;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) part[warp][2 + lane + 32 * i] = acc[i];
+    __syncthreads();
+    for (int d = threadIdx.x; d < D; d += NW * 32) {
+        float top = -INFINITY;
+        for (int v = 0; v < w_used; ++v) top = fmaxf(top, part[v][0]);
+        float sum = 0.f, o = 0.f;
+        for (int v = 0; v < w_used; ++v) {
+            const float f = ex2_approx(part[v][0] - top);
+            sum = fmaf(part[v][1], f, sum);
+            o = fmaf(part[v][2 + d], f, o);
         }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) part[warp][2 + lane + 32 * i] = acc[i];
-        __syncthreads();
-        if (warp == 0) {
-#pragma unroll
-            for (int v = 0; v < 8; ++v) M = fmaxf(M, part[v][0]);
-            L = 0.f;
-#pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-#pragma unroll
-            for (int v = 0; v < 8; ++v) {
-                const float f = ex2_approx(part[v][0] - M);
-                L = fmaf(part[v][1], f, L);
-#pragma unroll
-                for (int i = 0; i < PER; ++i) acc[i] = fmaf(part[v][2 + lane + 32 * i], f, acc[i]);
-            }
-            const float inv = 1.f / L;
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                out[(size_t)(cut.row + head) * D + lane + 32 * i] = to_out<OutT>(acc[i] * inv);
-        }
-        __syncthreads();
+        out[(size_t)(cut.row + head) * D + d] = to_out<OutT>(o / sum);
     }
 }
 

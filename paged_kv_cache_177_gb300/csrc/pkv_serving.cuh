@@ -107,10 +107,13 @@ int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t
         cuts = reinterpret_cast<pkv::E4m3Cut *>(static_cast<char *>(workspace) + kCounterBytes);
         p.partials = reinterpret_cast<float *>(cuts + (size_t)kPersistMaxCtas * NW);
     }
-    kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(p, cuts, whole ? 1 : 0);
+    const long long units = (long long)p.num_seqs * p.num_kv_heads;
+    const bool by_unit = !whole && units <= grid * NW;
+    kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(p, cuts, whole ? 1 : 0, by_unit ? 1 : 0);
     const int rc = check_launch();
     if (rc != PKV_OK || whole) return rc;
-    return launch_pdl(pkv::e4m3_merge_kernel<D, OutT>, dim3(grid * NW), dim3(256), 0, st, static_cast<OutT *>(p.out),
+    return launch_pdl(pkv::e4m3_merge_kernel<D, OutT>, dim3(by_unit ? (unsigned)units : grid * NW, p.group),
+                      dim3(pkv::kE4m3MergeWarps * 32), 0, st, static_cast<OutT *>(p.out),
                       static_cast<const float *>(p.partials), static_cast<const pkv::E4m3Cut *>(cuts), p.group);
 }
 
