@@ -475,7 +475,7 @@ struct E4m3Cut {
     int segments, worker, row, pad;
 };
 
-template <int D, int NT, int NS, int NW, typename OutT>
+template <int D, int NT, int NB, int NS, int NW, typename OutT>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_e4m3_kernel(const DecodeParams p, E4m3Cut *cuts, const int whole_units, const int cuts_by_unit) {
     using C = E4m3Cfg<D, NS, NW>;
@@ -630,25 +630,25 @@ __global__ void __launch_bounds__(NW * 32, 1)
     E4m3Cut cut{0, w, 0, 0};
     int i = 0;
     bool waited = true;
-    // NB blocks from position i on, all of one unit
+    // N blocks from position i on, all of one unit
     auto step = [&](auto nb_tag, int valid) -> bool {
-        constexpr int NB = decltype(nb_tag)::value;
-        uint32_t tile[NB];
+        constexpr int N = decltype(nb_tag)::value;
+        uint32_t tile[N];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int b = 0; b < N; ++b) {
             const int st = (i + b) & (NS - 1);
             if (!__all_sync(0xffffffffu, mbar_wait(&full[st], ((i + b) / NS) & 1))) return false;
             tile[b] = smem_u32(ring + st * C::kStage);
         }
-        wa.template blocks<NB>(tile, valid, lane);
+        wa.template blocks<N>(tile, valid, lane);
         __syncwarp();  // every lane's reads of the stages are done before their refill
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < N; ++b)
             if (issued < cnt) issue();
         return true;
     };
     while (true) {
-        const bool two = i + 1 < cnt && c.j + 1 < c.n;
+        const bool two = NB == 2 && i + 1 < cnt && c.j + 1 < c.n;
         const int last_j = two ? c.j + 1 : c.j, last_i = two ? i + 1 : i;
         const bool unit_end = last_j == c.n - 1;
         Cursor cn = c;
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
             len_next = seq_len(p, cn.s, false);
         }
         const int valid = unit_end ? len - kBlock * (c.n - 1) : kBlock;  // tokens of the last of these blocks
-        waited = two ? step(IntConst<2>{}, valid) : step(IntConst<1>{}, valid);
+        waited = two ? step(IntConst<NB>{}, valid) : step(IntConst<1>{}, valid);
         if (!waited) break;
         i = last_i;
         c.j = last_j;
@@ -703,35 +703,53 @@ __global__ void __launch_bounds__(NW * 32, 1)
 }
 
 // Merges the states of every cut unit, one CTA per (record, query head of the group): its warps share
-// the segments, eight in flight each, and join through shared memory.
-constexpr int kE4m3MergeWarps = 4;
-template <int D, typename OutT>
-__global__ void __launch_bounds__(kE4m3MergeWarps * 32)
+// the segments, eight at a time with all their loads in flight, and join through shared memory. Bound
+// by those loads' latency: many units' few segments take four warps, few units' many sixteen.
+template <int D, int NW, typename OutT>
+__global__ void __launch_bounds__(NW * 32)
     e4m3_merge_kernel(OutT *out, const float *__restrict__ partials, const E4m3Cut *__restrict__ cuts, int g) {
-    constexpr int PER = D / 32, NW = kE4m3MergeWarps;
+    constexpr int PER = D / 32, NB = 8;
     __shared__ float part[NW][2 + D];
     const int head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const E4m3Cut cut = cuts[blockIdx.x];
     const int nseg = cut.segments;
     if (nseg <= 0) return;
-    auto row_of = [&](int k) {  // the first segment ends its worker's range, the others begin theirs
-        return partials + ((size_t)(2 * (cut.worker + k) + (k == 0 ? 1 : 0)) * g + head) * (2 + D);
-    };
     float M = -INFINITY, L = 0.f, acc[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    const int w_used = min(NW, nseg);
-    for (int k = warp + lane * NW; k < nseg; k += 32 * NW) M = fmaxf(M, row_of(k)[0]);
+    for (int k0 = warp; k0 < nseg; k0 += NW * NB) {
+        float m[NB], l[NB], o[NB][PER];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll 8
-    for (int k = warp; k < nseg; k += NW) {
-        const float *r = row_of(k);
-        const float f = ex2_approx(r[0] - M);
-        L = fmaf(r[1], f, L);
+        for (int b = 0; b < NB; ++b) {
+            const int k = k0 + b * NW;
+            m[b] = -INFINITY;
+            l[b] = 0.f;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] = fmaf(r[2 + lane + 32 * i], f, acc[i]);
+            for (int i = 0; i < PER; ++i) o[b][i] = 0.f;
+            if (k < nseg) {  // the first segment ends its worker's range, the others begin theirs
+                const float *r = partials + ((size_t)(2 * (cut.worker + k) + (k == 0 ? 1 : 0)) * g + head) * (2 + D);
+                m[b] = __ldcg(r);
+                l[b] = __ldcg(r + 1);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) o[b][i] = __ldcg(r + 2 + lane + 32 * i);
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) top = fmaxf(top, m[b]);
+        const float al = ex2_approx(M - top);
+        M = top;
+        L *= al;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) acc[i] *= al;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const float f = ex2_approx(m[b] - top);
+            L = fmaf(l[b], f, L);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] = fmaf(o[b][i], f, acc[i]);
+        }
     }
     if (lane == 0) {
         part[warp][0] = M;
@@ -740,11 +758,12 @@ __global__ void __launch_bounds__(kE4m3MergeWarps * 32)
 #pragma unroll
     for (int i = 0; i < PER; ++i) part[warp][2 + lane + 32 * i] = acc[i];
     __syncthreads();
+    const int used = min(NW, nseg);  // (the other warps saw no segment)
     for (int d = threadIdx.x; d < D; d += NW * 32) {
         float top = -INFINITY;
-        for (int v = 0; v < w_used; ++v) top = fmaxf(top, part[v][0]);
+        for (int v = 0; v < used; ++v) top = fmaxf(top, part[v][0]);
         float sum = 0.f, o = 0.f;
-        for (int v = 0; v < w_used; ++v) {
+        for (int v = 0; v < used; ++v) {
             const float f = ex2_approx(part[v][0] - top);
             sum = fmaf(part[v][1], f, sum);
             o = fmaf(part[v][2 + d], f, o);

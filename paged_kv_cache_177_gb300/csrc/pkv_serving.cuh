@@ -76,7 +76,14 @@ int launch_dequantize(void *dk, void *dv, int dst_nb, const void *sk, const void
 #ifndef PKV_E4M3_STAGES
 #define PKV_E4M3_STAGES 4
 #endif
+#ifndef PKV_E4M3_WARPS2
+#define PKV_E4M3_WARPS2 8
+#endif
+#ifndef PKV_E4M3_NB2
+#define PKV_E4M3_NB2 1
+#endif
 constexpr int kE4m3Warps = PKV_E4M3_WARPS;
+constexpr int kE4m3MaxSeqs = 4096;  // sequences of one launch: their block counts lie in shared memory
 
 // Contexts this short are not cut: a worker takes whole (sequence, kv head) units and writes
 // their outputs itself, so no merge is launched.
@@ -84,17 +91,22 @@ bool e4m3_whole_units(int max_context_len) { return max_context_len <= 256; }
 
 template <int D, int NT, typename OutT>
 int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t st) {
-    // two column tiles need 168 registers and more: eight warps, which have them
-    constexpr int NS = PKV_E4M3_STAGES, NW = NT == 2 ? 8 : kE4m3Warps;
+    // Two column tiles need more than the 168 registers that twelve warps leave: eight warps. The ring is
+    // 16 KB a warp. At head_dim 128 a step takes one block, whose stage is refilled at once (32K-128K
+    // contexts: 234 us, and 249 us with two blocks a step, whose stages wait for each other); at 64 a
+    // step of two blocks hides its latencies better than it costs.
+    constexpr int NW = NT == 2 ? PKV_E4M3_WARPS2 : kE4m3Warps;
+    constexpr int NS = D == 128 ? PKV_E4M3_STAGES : 2 * PKV_E4M3_STAGES;
+    constexpr int NB = D == 128 ? (NT == 2 ? PKV_E4M3_NB2 : 1) : 2;
     using C = pkv::E4m3Cfg<D, NS, NW>;
-    static_assert(C::smem_bytes(kPersistMaxSeqs) + 64 <= kSmemLimit, "shared memory");
-    auto kern = pkv::decode_e4m3_kernel<D, NT, NS, NW, OutT>;
+    static_assert(C::smem_bytes(kE4m3MaxSeqs) + 64 <= kSmemLimit, "shared memory");
+    auto kern = pkv::decode_e4m3_kernel<D, NT, NB, NS, NW, OutT>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     if (configured_device != dev) {
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)C::smem_bytes(kPersistMaxSeqs)) != cudaSuccess)
+                                 (int)C::smem_bytes(kE4m3MaxSeqs)) != cudaSuccess)
             return PKV_ERR_CUDA;
         configured_device = dev;
     }
@@ -112,9 +124,13 @@ int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t
     kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(p, cuts, whole ? 1 : 0, by_unit ? 1 : 0);
     const int rc = check_launch();
     if (rc != PKV_OK || whole) return rc;
-    return launch_pdl(pkv::e4m3_merge_kernel<D, OutT>, dim3(by_unit ? (unsigned)units : grid * NW, p.group),
-                      dim3(pkv::kE4m3MergeWarps * 32), 0, st, static_cast<OutT *>(p.out),
-                      static_cast<const float *>(p.partials), static_cast<const pkv::E4m3Cut *>(cuts), p.group);
+    const dim3 records(by_unit ? (unsigned)units : grid * NW, p.group);
+    auto merge = [&](auto kernel, int warps) {
+        return launch_pdl(kernel, records, dim3(warps * 32), 0, st, static_cast<OutT *>(p.out),
+                          static_cast<const float *>(p.partials), static_cast<const pkv::E4m3Cut *>(cuts), p.group);
+    };
+    return by_unit && 8 * units <= grid * NW ? merge(pkv::e4m3_merge_kernel<D, 16, OutT>, 16)
+                                             : merge(pkv::e4m3_merge_kernel<D, 4, OutT>, 4);
 }
 
 template <typename OutT>
@@ -205,14 +221,14 @@ int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, c
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     // the kernel keeps the batch's block counts in shared memory: larger batches go in slices
-    for (int s0 = 0; s0 < num_seqs; s0 += kPersistMaxSeqs) {
+    for (int s0 = 0; s0 < num_seqs; s0 += kE4m3MaxSeqs) {
         pkv::DecodeParams ps = p;
         const size_t row = (size_t)s0 * num_q_heads * head_dim;
         ps.out = static_cast<char *>(out) + row * (dtype == PKV_BF16 ? 2 : 4);
         ps.q = static_cast<const char *>(q) + row * 2;
         ps.block_tables = block_tables + (size_t)s0 * max_blocks_per_seq;
         ps.context_lens = context_lens + s0;
-        ps.num_seqs = num_seqs - s0 < kPersistMaxSeqs ? num_seqs - s0 : kPersistMaxSeqs;
+        ps.num_seqs = num_seqs - s0 < kE4m3MaxSeqs ? num_seqs - s0 : kE4m3MaxSeqs;
         rc = dtype == PKV_BF16 ? launch_decode_e4m3<__nv_bfloat16>(ps, head_dim, workspace, st)
                                : launch_decode_e4m3<float>(ps, head_dim, workspace, st);
         if (rc != PKV_OK) return rc;
