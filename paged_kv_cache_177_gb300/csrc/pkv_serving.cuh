@@ -142,6 +142,50 @@ int launch_decode_e4m3(pkv::DecodeParams &p, int head_dim, void *workspace, cuda
                         : launch_decode_e4m3_shape<64, 2, OutT>(p, workspace, st);
 }
 
+// Trees: contexts of at most four chunks of 128 keys are not cut, so no merge is launched.
+bool tree_whole_units(int max_context_len) { return max_context_len <= 512; }
+
+// Two row tiles to a unit where one does not hold the largest tree's rows.
+bool tree_pair(int g, int max_query_len) { return max_query_len > 128 / g; }
+
+template <int D, bool kPair>
+int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::TreeParams &tp,
+                void *workspace, cudaStream_t st) {
+    using C = pkv::TreeCfg<D, kPair>;
+    static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
+    auto kern = pkv::tree_attention_kernel<D, kPair>;
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    if (configured_device != dev) {
+        // the register split draws on the registers the CTA is launched with
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+        if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + 256 * C::kHighRegs) return PKV_ERR_UNSUPPORTED;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured_device = dev;
+    }
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    const int grid = sms < kPersistMaxCtas ? sms : kPersistMaxCtas, g = tp.d.group, tile_tokens = 128 / g;
+    const bool whole = tree_whole_units(tp.d.max_context_len);
+    pkv::TreeCut *cuts = nullptr;
+    float *partials = nullptr;
+    if (!whole) {
+        cuts = reinterpret_cast<pkv::TreeCut *>(static_cast<char *>(workspace) + kCounterBytes);
+        partials = reinterpret_cast<float *>(cuts + kPersistMaxCtas);
+    }
+    kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, tp, partials, cuts, tile_tokens);
+    const int rc = check_launch();
+    if (rc != PKV_OK || whole) return rc;
+    const int per_set = C::kTiles * tile_tokens;
+    const int rows = (tp.max_query_len < per_set ? tp.max_query_len : per_set) * g;  // of the largest unit
+    return launch_pdl(pkv::tree_merge_kernel<D>, dim3(grid, (rows + 7) / 8), dim3(256), 0, st,
+                      static_cast<__nv_bfloat16 *>(tp.d.out), static_cast<const float *>(partials),
+                      static_cast<const pkv::TreeCut *>(cuts), C::kUnitRows, g, tp.d.num_q_heads, tile_tokens);
+}
+
 template <typename T, int D>
 int launch_rope(const pkv::RopeParams &p, bool interleaved, bool e4m3, cudaStream_t st) {
     auto kern = interleaved ? (e4m3 ? pkv::qk_norm_rope_append_kernel<T, D, true, true>
@@ -287,8 +331,11 @@ int tree_masks(int64_t *tree_mask, const int32_t *parents, const int32_t *query_
 
 size_t pkv_tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_query_len,
                                 int max_context_len) {
-    (void)num_seqs, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)max_query_len, (void)max_context_len;
-    return 0;
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_query_len <= 0 ||
+        num_q_heads % num_kv_heads != 0 || tree_whole_units(max_context_len))
+        return 0;
+    const size_t rows = tree_pair(num_q_heads / num_kv_heads, max_query_len) ? 256 : 128;
+    return kCounterBytes + kPersistMaxCtas * (sizeof(pkv::TreeCut) + 2 * rows * (2 + (size_t)head_dim) * sizeof(float));
 }
 
 int paged_tree_attention(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -318,10 +365,18 @@ int paged_tree_attention(void *out, const void *q, const void *k_cache, const vo
     tp.mask_words = mask_words;
     tp.num_queries = num_queries;
     tp.max_query_len = max_query_len;
-    const dim3 grid((unsigned)(((long long)max_query_len * num_q_heads + 3) / 4), num_seqs);
-    auto kern = head_dim == 128 ? pkv::tree_attention_kernel<128> : pkv::tree_attention_kernel<64>;
-    kern<<<grid, 128, 0, static_cast<cudaStream_t>(stream)>>>(tp);
-    return check_launch();
+    const int g = tp.d.group, tile_tokens = 128 / g;
+    alignas(64) CUtensorMap tmq, tmk, tmv;
+    if ((rc = encode_q_map(&tmq, q, num_queries, num_q_heads, head_dim, g, tile_tokens)) != PKV_OK) return rc;
+    if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim, true)) != PKV_OK) return rc;
+    if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool pair = tree_pair(g, max_query_len);
+    if (head_dim == 128)
+        return pair ? launch_tree<128, true>(tmq, tmk, tmv, tp, workspace, st)
+                    : launch_tree<128, false>(tmq, tmk, tmv, tp, workspace, st);
+    return pair ? launch_tree<64, true>(tmq, tmk, tmv, tp, workspace, st)
+                : launch_tree<64, false>(tmq, tmk, tmv, tp, workspace, st);
 }
 
 int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layers, const int32_t *block_tables,

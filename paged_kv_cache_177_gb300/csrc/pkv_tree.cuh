@@ -3,7 +3,7 @@
 // accepted path's keys and values to consecutive positions.
 #pragma once
 
-#include "pkv_kernels.cuh"
+#include "pkv_prefill_tc.cuh"
 
 namespace pkv {
 
@@ -61,77 +61,759 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 }
 
 // =====================================================================================
-// Attention, one warp per (row, query head): 32 tokens at a time, a lane scores one of them.
+// Attention on the 5th-generation tensor cores (tcgen05).
+//
+// Rows are (draft, query head of the kv head's group) pairs, 128 to an MMA tile (128 / g drafts), keys
+// are taken 128 at a time (8 cache blocks, a chunk). All (sequence, kv head, row set) units' chunks form
+// one line of T positions, cut into equal ranges, one per CTA (one CTA per SM), so every SM
+// streams the same bytes whatever the lengths; a unit cut by a range's end leaves one state per
+// segment -- row max (log2 domain), sum and unnormalised output, fp32 -- that tree_merge_kernel
+// joins. Contexts of a few chunks are not cut: a CTA then takes whole units.
+//
+// The work of a drafts' batch is to read the context once: 4 D bytes of K and V a token and
+// kv head, against 4 D flops per row, so up to about 256 rows HBM bounds it, and the roles below are
+// there to keep 64 to 190 KB of copies in flight per SM:
+//   warp 0, one thread   TMA: a unit's Q rows; per chunk 16 K boxes and 8 V boxes into the rings
+//   warp 1, one thread   MMA: S = Q K^T (128 x 128, fp32 in tensor memory); O += P V with P from tensor memory
+//   warps 2-3            the values of the drafts: a row that does not see a draft must not meet its
+//                        NaN (0 * NaN is NaN), so non-finite elements there are zeroed before P V
+//   warps 4-7, 8-11      softmax, one thread per row (tensor-memory lane): two sides
+// The two sides are two row tiles of a unit (kPair, units of more than 128 rows), or take turns at the
+// chunks of one tile, each with its own S, O and running max; their two states are joined, half
+// of the columns each, when the segment ends. Either way one side's softmax runs while the tensor
+// cores work for the other.
+//
+// A row's max moves only when it grows by more than 8 (log2), as in the prefill kernels. Weights enter P V
+// as two bf16 values, the rounded weight and its remainder (16 significant bits): the second product
+// is tensor time that waits for HBM anyway, and a row's error stays at its output's rounding.
+//
+// Every wait is bounded; on a timeout the role records PKV_DEVERR_TIMEOUT, waits (bounded) for its own
+// copies and MMAs in flight, and the CTA frees its tensor memory and exits.
 // =====================================================================================
-template <int D>
-__global__ void __launch_bounds__(128) tree_attention_kernel(const TreeParams tp) {
-    constexpr int PER = D / 32;
+template <int D, bool kPair>
+struct TreeCfg {
+    static constexpr int kRows = 128, kSides = 2;
+    static constexpr int kTiles = kPair ? 2 : 1;           // row tiles of a unit
+    static constexpr int kUnitRows = kTiles * kRows;
+    static constexpr int kKeys = 128, kChunkBlocks = kKeys / kBlock;
+    static constexpr int kHalves = D / 64;
+    static constexpr int kHalfRows = 128 * 128;            // bytes of 128 rows of 128 bytes
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kStage = kKeys * D * 2;           // one chunk of K (or of V)
+    static constexpr int kBlockBytes = kBlock * D * 2;
+    static constexpr int kStages = D == 128 ? (kPair ? 2 : 3) : 4;
+    static constexpr int kKOff = kTiles * kQBytes;
+    static constexpr int kVOff = kKOff + kStages * kStage;
+    static constexpr int kBarOff = kVOff + kStages * kStage;
+    static constexpr int kBarBytes = 512;
+    static constexpr int kXchOff = kBarOff + kBarBytes;    // [2 sides][128 rows] (max, sum)
+    static constexpr int kSmem = kXchOff + (kPair ? 0 : kSides * kRows * 8);
+    static constexpr int kThreads = 384;
+    static constexpr int kLowRegs = 72, kHighRegs = 208;   // setmaxnreg split, launched at 168
+    static_assert(128 * kLowRegs + 256 * kHighRegs <= kThreads * 168, "register split");
+    static constexpr uint32_t kTmemCols = 512, kSideCols = 256, kOCol = 128;
+};
+
+struct TreeBars {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
+    uint64_t v_clean[4];                       // per stage: its drafts' values are finite
+    uint64_t s_full[2], p_full[2], o_done[2];  // per side
+    uint64_t x_full[2], x_done[2];             // per side: its state is in shared memory; it has read both O
+    uint64_t drain;
+    uint32_t tmem_base;
+    int any_bad;                                // a draft's value was not finite
+    int start_seq;                              // where this CTA's range begins: sequence ...
+    long long start_in;                         // ... position within the sequence, ...
+    long long total;                            // and the line's length
+    long long warp_sum[12];
+};
+static_assert(sizeof(TreeBars) <= 512, "barrier area");
+
+// A unit cut by the end of a worker's range: its segments (0: not cut), and where its rows go.
+struct TreeCut {
+    int segments, q_row, drafts, head;  // first query row of the unit, its drafts, first query head
+};
+
+// A worker's way along the line: one segment (a unit's chunks c0 .. c1 - 1) at a time.
+template <int D, bool kPair>
+struct TreeWalk {
+    using C = TreeCfg<D, kPair>;
+    int s, unit, units;       // sequence, unit within it (kv head major, then row set), its units
+    int len, q0, n, chunks, sets;
+    int c0, c1;
+    long long pos, left;      // position of the segment's first chunk (or unit), positions left with it
+
+    __device__ __forceinline__ static long long weigh(const TreeParams &tp, int s, int per_set, bool whole, bool flag,
+                                                int &len, int &q0, int &n) {
+        len = seq_len(tp.d, s, flag);
+        if (!tree_rows(tp.query_start, s, len, tp.max_query_len, tp.num_queries, q0, n)) {
+            if (flag) raise_error(PKV_DEVERR_LENGTH);
+            n = 0;
+        }
+        const int sets = (n + per_set - 1) / per_set;
+        return (long long)sets * tp.d.num_kv_heads * (whole ? 1 : (len + C::kKeys - 1) / C::kKeys);
+    }
+    __device__ __forceinline__ void enter(const TreeParams &tp, int per_set) {  // the sequence s
+        weigh(tp, s, per_set, false, false, len, q0, n);
+        sets = (n + per_set - 1) / per_set;
+        units = sets * tp.d.num_kv_heads;
+        chunks = (len + C::kKeys - 1) / C::kKeys;
+    }
+    __device__ __forceinline__ void segment(bool whole) {
+        c1 = whole ? chunks : (int)min((long long)chunks, c0 + left);
+    }
+    // Moves to the next segment; false at the end of the range.
+    __device__ __forceinline__ bool next(const TreeParams &tp, int per_set, bool whole) {
+        const int took = whole ? 1 : c1 - c0;
+        pos += took;
+        left -= took;
+        if (left <= 0) return false;
+        c0 = 0;
+        if (++unit == units) {
+            unit = 0;
+            do {
+                ++s;
+                enter(tp, per_set);
+            } while (units == 0);
+        }
+        segment(whole);
+        return true;
+    }
+    __device__ __forceinline__ int head() const { return unit / sets; }
+    __device__ __forceinline__ int first_draft(int per_set) const { return (unit % sets) * per_set; }
+};
+
+// Bits e = 0 .. 15: whether a row sees position pos + e. Positions before `base` are context; bit j of the row's
+// mask words is draft j = position base + j.
+__device__ __forceinline__ uint32_t tree_bits16(const int64_t *words, int pos, int base, int n) {
+    const int d = pos - base;
+    if (d + 15 < 0) return 0xffffu;
+    const int j0 = max(d, 0);             // first draft wanted
+    if (j0 >= n) return d < 0 ? (1u << -d) - 1u : 0u;
+    const int w = j0 >> 6, sh = j0 & 63;
+    unsigned long long v = (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w) >> sh;
+    if (sh > 48 && (w + 1) * 64 < n)
+        v |= (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w + 1) << (64 - sh);
+    const int room = n - j0;
+    uint32_t bits = (uint32_t)v & 0xffffu;
+    if (room < 16) bits &= (1u << room) - 1u;
+    if (d < 0) bits = (bits << -d) | ((1u << -d) - 1u);
+    return bits & 0xffffu;
+}
+
+template <int D, bool kPair>
+__global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
+    tree_attention_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                          const __grid_constant__ CUtensorMap tmv, const TreeParams tp, float *partials,
+                          TreeCut *cuts, const int tile_tokens) {
+    using C = TreeCfg<D, kPair>;
+    constexpr int NS = C::kStages;
     const DecodeParams &p = tp.d;
-    __shared__ float qs[4][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.y;
-    const int len = seq_len(p, s, blockIdx.x == 0 && threadIdx.x == 0);
-    int q0, n;
-    if (!tree_rows(tp.query_start, s, len, tp.max_query_len, tp.num_queries, q0, n)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) raise_error(PKV_DEVERR_LENGTH);
+    extern __shared__ __align__(1024) uint8_t base[];  // (three stages leave no room to align it by hand)
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = p.group, per_set = C::kTiles * tile_tokens;
+    const bool whole = cuts == nullptr;
+    if (smem_u32(base) & 1023u) {  // the swizzle's atoms would not be where the descriptors say
+        if (tid == 0) raise_error(PKV_DEVERR_TIMEOUT);
         return;
     }
-    const int item = blockIdx.x * 4 + warp;
-    const int i = item / p.num_q_heads, hq = item - i * p.num_q_heads;
-    if (i >= n) return;
-    const int h = hq / p.group;
-    const size_t row = (size_t)(q0 + i) * p.num_q_heads + hq;
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.q) + row * D;
-    for (int d = lane; d < D; d += 32) qs[warp][d] = __bfloat162float(q[d]) * p.scale_log2;
-    __syncwarp();
-    const __nv_bfloat16 *kc = static_cast<const __nv_bfloat16 *>(p.k_cache);
-    const __nv_bfloat16 *vc = static_cast<const __nv_bfloat16 *>(p.v_cache);
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-    const int64_t *words = tp.mask + (size_t)(q0 + i) * tp.mask_words;
-    const int base = len - n;
-    float m = -INFINITY, l = 0.f, acc[PER];
+    TreeBars &b = *reinterpret_cast<TreeBars *>(base + C::kBarOff);
+    if (tid == 0) {
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+        mbar_init(&b.q_full, 1);
+        mbar_init(&b.q_empty, 1);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&b.k_full[i], 1);
+            mbar_init(&b.k_empty[i], 1);
+            mbar_init(&b.v_full[i], 1);
+            mbar_init(&b.v_empty[i], 1);
+            mbar_init(&b.v_clean[i], 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.s_full[i], 1);
+            mbar_init(&b.p_full[i], 4);
+            mbar_init(&b.o_done[i], 1);
+            mbar_init(&b.x_full[i], 4);
+            mbar_init(&b.x_done[i], 4);
+        }
+        mbar_init(&b.drain, 1);
+        b.any_bad = 0;
+        b.start_seq = -1;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&b.tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+
+    // ---- this CTA's range of the line: a scan of the sequences' weights ----
+    {
+        const int S = p.num_seqs, per = (S + C::kThreads - 1) / C::kThreads;
+        const int s_lo = min(S, tid * per), s_hi = min(S, s_lo + per);
+        int len, q0, n;
+        long long local = 0;
+        for (int s = s_lo; s < s_hi; ++s)
+            local += TreeWalk<D, kPair>::weigh(tp, s, per_set, whole, blockIdx.x == 0, len, q0, n);
+        long long incl = local;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int t0 = 0; t0 < len; t0 += 32) {
-        const int t = t0 + lane, j = t - base;
-        const bool see = t < len && (j < 0 || ((__ldg(words + j / 64) >> (j % 64)) & 1) != 0);
-        int pb = -1;
-        if (see) {
-            pb = __ldg(table + t / kBlock);
-            if (pb < 0 || pb >= p.num_blocks) {
-                raise_error(PKV_DEVERR_BLOCK_ID);
-                pb = -1;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) b.warp_sum[warp] = incl;
+        __syncthreads();
+        long long before = incl - local, total = 0;
+        for (int w = 0; w < C::kThreads / 32; ++w) {
+            if (w < warp) before += b.warp_sum[w];
+            total += b.warp_sum[w];
+        }
+        // workers: no more than the line has (cut units: pairs of) positions
+        const int W = (int)min((long long)gridDim.x, whole ? total : max(1LL, total / 2));
+        const long long start = W > 0 ? total * blockIdx.x / W : 0;
+        if ((int)blockIdx.x < W && start >= before && start < before + local) {
+            long long at = before;
+            for (int s = s_lo; s < s_hi; ++s) {
+                const long long wt = TreeWalk<D, kPair>::weigh(tp, s, per_set, whole, false, len, q0, n);
+                if (start < at + wt) {
+                    b.start_seq = s;
+                    b.start_in = start - at;
+                    break;
+                }
+                at += wt;
             }
         }
-        float x = see ? 0.f : -INFINITY;
-        if (pb >= 0) {
-            const __nv_bfloat16 *kr = kc + (((size_t)pb * p.num_kv_heads + h) * kBlock + (t & 15)) * D;
-            for (int d = 0; d < D; ++d) x = fmaf(__bfloat162float(kr[d]), qs[warp][d], x);
-        }
-        float mx = x;
+        if (tid == 0) b.total = total;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();  // the merge may be set up; it waits for the states
+    const uint32_t tmem = b.tmem_base;
+    const long long T = b.total;
+    const int W = (int)min((long long)gridDim.x, whole ? T : max(1LL, T / 2)), w = blockIdx.x;
+    if (w >= W || T == 0) {
+        if (cuts && tid == 0) cuts[w].segments = 0;
+        __syncthreads();
+        if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+        return;
+    }
+    TreeWalk<D, kPair> at;
+    at.pos = T * w / W;
+    at.left = T * (w + 1) / W - at.pos;
+    at.s = b.start_seq;
+    at.enter(tp, per_set);
+    at.unit = (int)(whole ? b.start_in : b.start_in / at.chunks);
+    at.c0 = whole ? 0 : (int)(b.start_in - (long long)at.unit * at.chunks);
+    at.segment(whole);
+    const uint32_t q_s = smem_u32(base), k_s = smem_u32(base + C::kKOff), v_s = smem_u32(base + C::kVOff);
+
+    if (warp < 4) {
+        setmaxnreg_dec<C::kLowRegs>();
+        if (warp == 0) {
+            // ------------------------------ TMA producer ------------------------------
+            if (lane == 0) {
+                bool ok = true;
+                int seg = 0, r = 0;         // segments, ring position
+                int have_k = 0, have_v = 0; // chunks issued
+                const uint64_t policy = l2_evict_first();
+                do {
+                    const int h = at.head();
+                    const int nblk = (at.len + kBlock - 1) / kBlock, last_valid = at.len - (nblk - 1) * kBlock;
+                    const int32_t *table = p.block_tables + (size_t)at.s * p.max_blocks_per_seq;
+                    for (int j = at.c0; j < at.c1 && ok; ++j, ++r) {
+                        const int st = r % NS;
+                        // the chunk's tiles (-1: past the sequence or a bad id, reads as zeros) and first slots
+                        int z[C::kChunkBlocks], y[C::kChunkBlocks];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-        const float al = exp2f(m - ms), w = exp2f(x - ms);
-        m = mn;
-        l = l * al + w;
+                        for (int bi = 0; bi < C::kChunkBlocks; ++bi) {
+                            const int blk = j * C::kChunkBlocks + bi;
+                            z[bi] = blk < nblk ? __ldg(table + blk) : -1;
+                        }
+                        if (r >= NS && !(ok = mbar_wait(&b.k_empty[st], (r / NS - 1) & 1))) break;
+#pragma unroll
+                        for (int bi = 0; bi < C::kChunkBlocks; ++bi) {
+                            const int blk = j * C::kChunkBlocks + bi;
+                            y[bi] = blk == nblk - 1 ? last_valid - kBlock : 0;
+                            if (blk < nblk) {
+                                if (z[bi] < 0 || z[bi] >= p.num_blocks) {
+                                    raise_error(PKV_DEVERR_BLOCK_ID);
+                                    z[bi] = -1;
+                                } else {
+                                    z[bi] = z[bi] * p.num_kv_heads + h;
+                                }
+                            }
+                        }
+                        // K as [half][128 keys][64]
+                        mbar_arrive_expect_tx(&b.k_full[st], C::kStage);
+#pragma unroll
+                        for (int bi = 0; bi < C::kChunkBlocks; ++bi)
+#pragma unroll
+                            for (int u = 0; u < C::kHalves; ++u)
+                                tma_load_4d_hint(base + C::kKOff + st * C::kStage + u * C::kHalfRows + bi * (kBlock * 128),
+                                                 &tmk, 0, y[bi], u, z[bi], &b.k_full[st], policy);
+                        have_k = r + 1;
+                        if (r >= NS && !(ok = mbar_wait(&b.v_empty[st], (r / NS - 1) & 1))) break;
+                        // V as [block][half][16 keys][64]
+                        mbar_arrive_expect_tx(&b.v_full[st], C::kStage);
+#pragma unroll
+                        for (int bi = 0; bi < C::kChunkBlocks; ++bi)
+                            tma_load_4d_hint(base + C::kVOff + st * C::kStage + bi * C::kBlockBytes, &tmv, 0, y[bi], 0,
+                                             z[bi], &b.v_full[st], policy);
+                        have_v = r + 1;
+                        if (j == at.c0) {  // behind the first chunk's keys, so that these need not wait for the last S
+                            if (seg > 0 && !(ok = mbar_wait(&b.q_empty, (seg - 1) & 1))) break;
+                            const int t0 = at.first_draft(per_set);
+                            const int tiles = kPair && t0 + tile_tokens < at.n ? 2 : 1;
+                            mbar_arrive_expect_tx(&b.q_full, tiles * C::kHalves * 128 * g * tile_tokens);
+                            for (int t = 0; t < tiles; ++t)
+                                for (int u = 0; u < C::kHalves; ++u)
+                                    tma_load_4d(base + t * C::kQBytes + u * C::kHalfRows, &tmq, 0, u, h * g,
+                                                at.q0 + t0 + t * tile_tokens, &b.q_full);
+                            ++seg;
+                        }
+                    }
+                } while (ok && at.next(tp, per_set, whole));
+                if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+                // no copy may land after the CTA is gone
+                for (int i = max(0, have_k - NS); i < have_k; ++i) mbar_wait(&b.k_full[i % NS], (i / NS) & 1);
+                for (int i = max(0, have_v - NS); i < have_v; ++i) mbar_wait(&b.v_full[i % NS], (i / NS) & 1);
+                if (seg > 0) mbar_wait(&b.q_full, (seg - 1) & 1);
+            }
+        } else if (warp == 1) {
+            // ------------------------------ MMA issuer ------------------------------
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16_f32(C::kRows, C::kKeys, false, false);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(C::kRows, D, false, true);
+                bool ok = true;
+                int seg = 0, r0 = 0, pcount[2] = {0, 0};
+                auto issue_s = [&](int side, int r) {
+                    const uint32_t qt = q_s + (kPair ? side * C::kQBytes : 0);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (kk >> 2) * C::kHalfRows + (kk & 3) * 32;
+                        umma_bf16(tmem + side * C::kSideCols, smem_desc_sw128(qt + off, 16, 1024),
+                                  smem_desc_sw128(k_s + (r % NS) * C::kStage + off, 16, 1024), idesc_s, kk > 0);
+                    }
+                };
+                auto issue_pv = [&](int side, int r, bool first) {
+#pragma unroll
+                    for (int kk = 0; kk < C::kChunkBlocks; ++kk) {
+                        const uint64_t vd =
+                            smem_desc_sw128(v_s + (r % NS) * C::kStage + kk * C::kBlockBytes, kBlock * 128, 1024);
+                        const uint32_t pa = tmem + side * C::kSideCols + (kk >> 1) * 32 + (kk & 1) * 8;
+                        umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa, vd, idesc_o, !first || kk > 0);
+                        umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa + 16, vd, idesc_o, true);
+                    }
+                };
+                auto wait_k = [&](int r) { return mbar_wait(&b.k_full[r % NS], (r / NS) & 1); };
+                do {
+                    const int nc = at.c1 - at.c0;
+                    const int tiles = kPair && at.first_draft(per_set) + tile_tokens < at.n ? 2 : 1;
+                    if (!(ok = mbar_wait(&b.q_full, seg & 1))) break;
+                    auto values_ready = [&](int k) {
+                        const int st = (r0 + k) % NS;
+                        return mbar_wait(&b.v_full[st], ((r0 + k) / NS) & 1) &&
+                               mbar_wait(&b.v_clean[st], ((r0 + k) / NS) & 1);
+                    };
+                    auto weights_ready = [&](int side) {
+                        const bool good = mbar_wait(&b.p_full[side], pcount[side]++ & 1);
+                        tc_fence_after();
+                        return good;
+                    };
+                    if constexpr (kPair) {
+                        if (!(ok = wait_k(r0))) break;
+                        tc_fence_after();
+                        for (int t = 0; t < tiles; ++t) {
+                            issue_s(t, r0);
+                            umma_commit(&b.s_full[t]);
+                        }
+                        umma_commit(&b.k_empty[r0 % NS]);
+                        for (int k = 0; k < nc && ok; ++k) {
+                            ok = values_ready(k) && (k + 1 == nc || wait_k(r0 + k + 1));
+                            for (int t = 0; t < tiles && ok; ++t) {
+                                if (!(ok = weights_ready(t))) break;
+                                issue_pv(t, r0 + k, k == 0);
+                                if (k + 1 < nc) {
+                                    issue_s(t, r0 + k + 1);
+                                    umma_commit(&b.s_full[t]);
+                                } else {
+                                    umma_commit(&b.o_done[t]);
+                                }
+                            }
+                            if (!ok) break;
+                            umma_commit(&b.v_empty[(r0 + k) % NS]);
+                            if (k + 1 < nc) umma_commit(&b.k_empty[(r0 + k + 1) % NS]);
+                            if (k + 2 >= nc && k + 1 < nc) umma_commit(&b.q_empty);
+                            if (nc == 1) umma_commit(&b.q_empty);
+                        }
+                    } else {
+                        // S of chunk k + 1 goes to the other side before P V of chunk k
+                        auto scores = [&](int k) {
+                            if (!wait_k(r0 + k)) return false;
+                            tc_fence_after();
+                            issue_s(k & 1, r0 + k);
+                            umma_commit(&b.s_full[k & 1]);
+                            umma_commit(&b.k_empty[(r0 + k) % NS]);
+                            if (k == nc - 1) umma_commit(&b.q_empty);
+                            return true;
+                        };
+                        ok = scores(0);
+                        for (int k = 0; k < nc && ok; ++k) {
+                            if (k + 1 < nc && !(ok = scores(k + 1))) break;
+                            if (!(ok = values_ready(k) && weights_ready(k & 1))) break;
+                            issue_pv(k & 1, r0 + k, k < 2);
+                            umma_commit(&b.v_empty[(r0 + k) % NS]);
+                            if (k + 2 >= nc) umma_commit(&b.o_done[k & 1]);
+                        }
+                    }
+                    r0 += nc;
+                    ++seg;
+                } while (ok && at.next(tp, per_set, whole));
+                if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+                umma_commit(&b.drain);  // every MMA has finished before the tensor memory is released
+                mbar_wait(&b.drain, 0);
+            }
+            __syncwarp();
+        } else {
+            // ------------------------------ the drafts' values ------------------------------
+            bool ok = true;
+            int r0 = 0;
+            do {
+                const int nc = at.c1 - at.c0, ctx = at.len - at.n;
+                const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
+                // every chunk is waited for and passed on, drafts or not, so that no stage's phase runs
+                // away from this role's count
+                for (int k = 0; k < nc && ok; ++k) {
+                    const int st = (r0 + k) % NS;
+                    if (!(ok = warp_wait(&b.v_full[st], ((r0 + k) / NS) & 1))) break;
+                    const int blk0 = (at.c0 + k) * C::kChunkBlocks;
+                    const int b_lo = max(0, ctx / kBlock - blk0), b_hi = min(C::kChunkBlocks, nblk - blk0);
+                    uint8_t *vst = base + C::kVOff + st * C::kStage;
+                    for (int i = b_lo * (C::kBlockBytes / 16) + (tid - 64); i < b_hi * (C::kBlockBytes / 16); i += 64) {
+                        const uint4 v = reinterpret_cast<const uint4 *>(vst)[i];
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            bad |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+                        if (bad) {
+                            const int blk = blk0 + i / (C::kBlockBytes / 16), row = (i >> 3) & 15;
+                            const int pos = blk * kBlock + row - (blk == nblk - 1 ? lo : 0);
+                            if (pos >= ctx) {
+                                reinterpret_cast<uint4 *>(vst)[i] = make_uint4(0u, 0u, 0u, 0u);
+                                *reinterpret_cast<volatile int *>(&b.any_bad) = 1;
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.v_clean[st]);
+                }
+                r0 += nc;
+            } while (ok && at.next(tp, per_set, whole));
+            if (!ok && lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
+        }
+    } else {
+        setmaxnreg_inc<C::kHighRegs>();
+        // ------------------------------ softmax ------------------------------
+        const int side = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_cols = tmem + ((uint32_t)(quad * 32) << 16);
+        const uint32_t cols = lane_cols + side * C::kSideCols;
+        // scores stay raw: x * sl is the log2-domain score, the sign is folded in; a scale of 0 becomes one that
+        // leaves every score 0, so that a masked -inf stays -inf
+        const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
+        const float sgn = p.scale_log2 < 0.f ? -1.f : 1.f;
+        const bool no_scale = p.scale_log2 == 0.f;
+        float2 *xch = reinterpret_cast<float2 *>(base + C::kXchOff);
+        bool ok = true;
+        int scount = 0, ocount[2] = {0, 0}, seg = 0;
+        TreeCut cut{0, 0, 0, 0};
+        do {
+            const int nc = at.c1 - at.c0, h = at.head();
+            const int tok0 = at.first_draft(per_set) + (kPair ? side * tile_tokens : 0);
+            const int rows = max(0, min(at.n - tok0, tile_tokens)) * g;
+            const bool row_ok = row < rows;
+            const int draft = tok0 + row / g;
+            const int64_t *words = tp.mask + (size_t)(at.q0 + (row_ok ? draft : 0)) * tp.mask_words;
+            const int ctx = at.len - at.n;
+            const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
+            const bool warp_rows = quad * 32 < rows;   // a warp without rows only keeps the barriers' count
+            float m = -INFINITY, l = 0.f;
+            const int k_step = kPair ? 1 : 2, k_first = kPair ? 0 : side;
+            const bool active = !kPair || rows > 0;    // (the MMA thread leaves an empty second tile out)
+            for (int k = k_first; active && k < nc; k += k_step) {
+                if (!(ok = warp_wait(&b.s_full[side], scount++ & 1))) break;
+                if (warp_rows) {
+                    tc_fence_after();
+                    const int j = at.c0 + k;
+                    float x[4][32];  // the whole row of S in registers
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld32(cols + q * 32, x[q]);
+                    tmem_wait_ld();
+                    if (sgn < 0.f || no_scale) {
+                        const float f = no_scale ? 0.f : -1.f;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[q][e] *= f;
+                    }
+                    // only chunks that hold drafts or the sequence's end need masks
+                    if ((j + 1) * C::kKeys > ctx || (j + 1) * C::kChunkBlocks >= nblk) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t see = 0;
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int blk = j * C::kChunkBlocks + 2 * q + i;
+                                uint32_t bits = 0;
+                                if (blk < nblk) {
+                                    const int shift = blk == nblk - 1 ? lo : 0;  // (loaded that many rows early)
+                                    bits = tree_bits16(words, blk * kBlock - shift, ctx, at.n) & (0xffffu << shift);
+                                }
+                                see |= (bits & 0xffffu) << (16 * i);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[q][e] = (see >> e) & 1u ? x[q][e] : -INFINITY;
+                        }
+                    }
+                    float mxs[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mxs[i] = -INFINITY;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            mxs[(e >> 1) & 7] = max3f(mxs[(e >> 1) & 7], x[q][e], x[q][e + 1]);
+                    const float mx = fmaxf(max3f(max3f(mxs[0], mxs[1], mxs[2]), mxs[3], mxs[4]),
+                                           max3f(mxs[5], mxs[6], mxs[7]));
+                    const float m_new = fmaxf(m, mx * sl);
+                    const bool move = m_new > m + 8.f;
+                    const float m_use = move ? m_new : m;
+                    const float ms = m_use == -INFINITY ? 0.f : m_use;
+                    const float alpha = ex2_approx(m - ms);
+                    // this side's O is quiescent: P V of its previous chunk ran before this S
+                    if (k >= k_step && __any_sync(0xffffffffu, move && m != -INFINITY)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tmem_ld32(cols + C::kOCol + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tmem_st32(cols + C::kOCol + c * 32, o);
+                        }
+                    }
+                    m = m_use;
+                    // P over each quarter's score columns: keys 32 q + 2 i, + 1 at column 32 q + i, remainders at + 16
+                    const uint64_t sl2 = pack_f2(sl, sl), nms2 = pack_f2(-ms, -ms);
+                    uint64_t rss[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t hi[16], rem[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float a0, a1;
+                            unpack_f2(fma_f2(pack_f2(x[q][2 * i], x[q][2 * i + 1]), sl2, nms2), a0, a1);
+                            const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+                            rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
+                            const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
+                            hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
+                            const float2 fh = __bfloat1622float2(ph);
+                            const __nv_bfloat162 pl = __floats2bfloat162_rn(e0 - fh.x, e1 - fh.y);
+                            rem[i] = *reinterpret_cast<const uint32_t *>(&pl);
+                        }
+                        tmem_st16(cols + q * 32, hi);
+                        tmem_st16(cols + q * 32 + 16, rem);
+                    }
+                    tmem_wait_st();
+                    float rs[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) unpack_f2(rss[i], rs[2 * i], rs[2 * i + 1]);
+                    l = l * alpha + (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.p_full[side]);
+            }
+            // ---- the segment ends here ----
+            const bool used[2] = {true, nc > 1};       // (two sides on one tile: chunks in turn)
+            const bool uncut = at.c0 == 0 && at.c1 == at.chunks;
+            if (ok) {
+                if constexpr (kPair) {
+                    if (active) ok = warp_wait(&b.o_done[side], ocount[side]++ & 1);
+                } else {
+                    xch[side * C::kRows + row] = make_float2(m, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.x_full[side]);
+                    ok = warp_wait(&b.x_full[side ^ 1], seg & 1);
+                    for (int t = 0; t < 2; ++t)
+                        if (ok && used[t]) ok = warp_wait(&b.o_done[t], ocount[t]++ & 1);
+                }
+            }
+            if (ok && warp_rows) {
+                tc_fence_after();
+                float f[2] = {1.f, 0.f}, M = m, L = l;
+                if constexpr (!kPair) {
+                    const float2 other = xch[(side ^ 1) * C::kRows + row];
+                    M = fmaxf(m, other.x);
+                    const float ms = M == -INFINITY ? 0.f : M;
+                    f[side] = ex2_approx(m - ms);
+                    f[side ^ 1] = ex2_approx(other.x - ms);
+                    L = l * f[side] + other.y * f[side ^ 1];
+                }
+                // a value that was not finite was zeroed: the rows that see its draft get NaN instead
+                bool poison = false;
+                if (row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0) {
+                    for (int jd = 0; jd < at.n && !poison; ++jd) {
+                        if (!((__ldg(words + jd / 64) >> (jd % 64)) & 1)) continue;
+                        const int ps = ctx + jd;
+                        const int pb = __ldg(p.block_tables + (size_t)at.s * p.max_blocks_per_seq + ps / kBlock);
+                        if (pb < 0 || pb >= p.num_blocks) continue;
+                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                                 (((size_t)pb * p.num_kv_heads + h) * kBlock + ps % kBlock) * D;
+                        for (int d = 0; d < D; ++d) poison |= !(fabsf(__bfloat162float(v[d])) < INFINITY);
+                    }
+                }
+                const float inv = !uncut ? 1.f : L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // (NaN stays)
+                constexpr int kMine = kPair ? D : D / 2;   // columns this side writes
+                const int d0 = kPair ? 0 : side * kMine;
+                const int unit_row = kPair ? side * C::kRows + row : row;
+                float *slot = partials + (size_t)(2 * w + (at.c0 == 0 ? 1 : 0)) * C::kUnitRows * (2 + D);
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                                     ((size_t)(at.q0 + (row_ok ? draft : 0)) * p.num_q_heads + h * g + row % g) * D + d0;
+                if (!uncut && d0 == 0 && row_ok)
+                    *reinterpret_cast<float2 *>(slot + 2 * unit_row) = make_float2(M, L);
+                float *po = slot + 2 * C::kUnitRows + (size_t)unit_row * D + d0;
+#pragma unroll
+                for (int c = 0; c < kMine / 32; ++c) {
+                    float o[32];
+                    if constexpr (kPair) {
+                        tmem_ld32(cols + C::kOCol + c * 32, o);
+                        tmem_wait_ld();
+                    } else {
+                        float o1[32];
+                        tmem_ld32(lane_cols + C::kOCol + d0 + c * 32, o);
+                        if (used[1]) tmem_ld32(lane_cols + C::kSideCols + C::kOCol + d0 + c * 32, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            o[e] *= f[0];
+                            if (used[1]) o[e] = fmaf(o1[e], f[1], o[e]);
+                        }
+                    }
+                    if (poison) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(0x7fc00000u);
+                    }
+                    if (row_ok && uncut) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[q * 8 + 2 * e] * inv,
+                                                                                o[q * 8 + 2 * e + 1] * inv);
+                                v[e] = *reinterpret_cast<const uint32_t *>(&v2);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + c * 32 + q * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    } else if (row_ok) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            *reinterpret_cast<float4 *>(po + c * 32 + 4 * q) =
+                                make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                }
+                tc_fence_before();
+            }
+            if (!uncut && at.c0 == 0) {  // begun here, ends further on (a worker cuts at most one unit so)
+                const long long x0 = at.pos;
+                cut.segments = (int)(((x0 + at.chunks) * W - 1) / T) - w + 1;
+                cut.q_row = at.q0 + at.first_draft(per_set);
+                cut.drafts = min(per_set, at.n - at.first_draft(per_set));
+                cut.head = h * g;
+            }
+            if constexpr (!kPair) {
+                // the next segment's first P lets the MMA overwrite O: not before both sides have read it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.x_done[side]);
+                if (ok) ok = warp_wait(&b.x_done[side ^ 1], seg & 1);
+            }
+            ++seg;
+        } while (ok && at.next(tp, per_set, whole));
+        if (!ok) {
+            if (lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
+            cut.segments = 0;
+        }
+        if (cuts && tid == 128) cuts[w] = cut;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+// Joins the states of every cut unit: a warp per row, four segments' loads in flight.
+template <int D>
+__global__ void __launch_bounds__(256)
+    tree_merge_kernel(__nv_bfloat16 *out, const float *__restrict__ partials, const TreeCut *__restrict__ cuts,
+                      int unit_rows, int g, int num_q_heads, int tile_tokens) {
+    constexpr int PER = D / 32, NB = 4;
+    const int w1 = blockIdx.x, lane = threadIdx.x & 31;
+    const int i = blockIdx.y * 8 + (threadIdx.x >> 5);  // (draft, head) of the unit
+    pdl_wait();
+    const TreeCut cut = cuts[w1];
+    if (cut.segments <= 0 || i >= cut.drafts * g) return;
+    const int draft = i / g, hg = i - draft * g;
+    const int row = (draft / tile_tokens) * 128 + (draft % tile_tokens) * g + hg;
+    float M = -INFINITY, L = 0.f, acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int k0 = 0; k0 < cut.segments; k0 += NB) {
+        float m[NB], l[NB], o[NB][PER];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int k = k0 + b;
+            m[b] = -INFINITY;
+            l[b] = 0.f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) o[b][e] = 0.f;
+            if (k < cut.segments) {  // the first segment ends its worker's range, the others begin theirs
+                const float *slot = partials + (size_t)(2 * (w1 + k) + (k == 0 ? 1 : 0)) * unit_rows * (2 + D);
+                m[b] = __ldcg(slot + 2 * row);
+                l[b] = __ldcg(slot + 2 * row + 1);
+#pragma unroll
+                for (int e = 0; e < PER; ++e) o[b][e] = __ldcg(slot + 2 * unit_rows + (size_t)row * D + lane + 32 * e);
+            }
+        }
+        float top = M;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) top = fmaxf(top, m[b]);
+        const float ms = top == -INFINITY ? 0.f : top;  // (rows that have seen nothing yet)
+        const float al = ex2_approx(M - ms);
+        M = top;
+        L *= al;
 #pragma unroll
         for (int e = 0; e < PER; ++e) acc[e] *= al;
-        for (int u = 0; u < min(32, len - t0); ++u) {
-            const int b = __shfl_sync(0xffffffffu, pb, u);
-            const float wu = __shfl_sync(0xffffffffu, w, u);
-            if (b < 0) continue;
-            const __nv_bfloat16 *vr = vc + (((size_t)b * p.num_kv_heads + h) * kBlock + ((t0 + u) & 15)) * D;
 #pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(__bfloat162float(vr[lane + 32 * e]), wu, acc[e]);
+        for (int b = 0; b < NB; ++b) {
+            const float f = ex2_approx(m[b] - ms);
+            L = fmaf(l[b], f, L);
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(o[b][e], f, acc[e]);
         }
     }
+    const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
+    __nv_bfloat16 *dst = out + ((size_t)(cut.q_row + draft) * num_q_heads + cut.head + hg) * D;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.out) + row * D;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int e = 0; e < PER; ++e) out[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+    for (int e = 0; e < PER; ++e) dst[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
 }
 
 // =====================================================================================
