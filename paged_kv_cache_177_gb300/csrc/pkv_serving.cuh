@@ -150,7 +150,7 @@ bool tree_pair(int g, int max_query_len) { return max_query_len > 128 / g; }
 
 template <int D, bool kPair>
 int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::TreeParams &tp,
-                void *workspace, cudaStream_t st) {
+                int q_tokens, void *workspace, cudaStream_t st) {
     using C = pkv::TreeCfg<D, kPair>;
     static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
     auto kern = pkv::tree_attention_kernel<D, kPair>;
@@ -176,7 +176,7 @@ int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMa
         cuts = reinterpret_cast<pkv::TreeCut *>(static_cast<char *>(workspace) + kCounterBytes);
         partials = reinterpret_cast<float *>(cuts + kPersistMaxCtas);
     }
-    kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, tp, partials, cuts, tile_tokens);
+    kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, tp, partials, cuts, tile_tokens, q_tokens);
     const int rc = check_launch();
     if (rc != PKV_OK || whole) return rc;
     const int per_set = C::kTiles * tile_tokens;
@@ -367,16 +367,17 @@ int paged_tree_attention(void *out, const void *q, const void *k_cache, const vo
     tp.max_query_len = max_query_len;
     const int g = tp.d.group, tile_tokens = 128 / g;
     alignas(64) CUtensorMap tmq, tmk, tmv;
-    if ((rc = encode_q_map(&tmq, q, num_queries, num_q_heads, head_dim, g, tile_tokens)) != PKV_OK) return rc;
+    const int q_tokens = max_query_len < tile_tokens ? max_query_len : tile_tokens;  // loaded of a tile's drafts
+    if ((rc = encode_q_map(&tmq, q, num_queries, num_q_heads, head_dim, g, q_tokens)) != PKV_OK) return rc;
     if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim, true)) != PKV_OK) return rc;
     if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool pair = tree_pair(g, max_query_len);
     if (head_dim == 128)
-        return pair ? launch_tree<128, true>(tmq, tmk, tmv, tp, workspace, st)
-                    : launch_tree<128, false>(tmq, tmk, tmv, tp, workspace, st);
-    return pair ? launch_tree<64, true>(tmq, tmk, tmv, tp, workspace, st)
-                : launch_tree<64, false>(tmq, tmk, tmv, tp, workspace, st);
+        return pair ? launch_tree<128, true>(tmq, tmk, tmv, tp, q_tokens, workspace, st)
+                    : launch_tree<128, false>(tmq, tmk, tmv, tp, q_tokens, workspace, st);
+    return pair ? launch_tree<64, true>(tmq, tmk, tmv, tp, q_tokens, workspace, st)
+                : launch_tree<64, false>(tmq, tmk, tmv, tp, q_tokens, workspace, st);
 }
 
 int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layers, const int32_t *block_tables,

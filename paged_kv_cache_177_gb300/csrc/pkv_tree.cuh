@@ -73,9 +73,10 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 // The work of a drafts' batch is to read the context once: 4 D bytes of K and V a token and
 // kv head, against 4 D flops per row, so up to about 256 rows HBM bounds it, and the roles below are
 // there to keep 64 to 190 KB of copies in flight per SM:
-//   warp 0, one thread   TMA: a unit's Q rows; per chunk 16 K boxes and 8 V boxes into the rings
+//   warps 0 and 2, one   TMA: a unit's Q rows and the K chunks; the V chunks (two threads, so that neither
+//   thread each          ring waits for the other's stages)
 //   warp 1, one thread   MMA: S = Q K^T (128 x 128, fp32 in tensor memory); O += P V with P from tensor memory
-//   warps 2-3            the values of the drafts: a row that does not see a draft must not meet its
+//   warp 3               the values of the drafts: a row that does not see a draft must not meet its
 //                        NaN (0 * NaN is NaN), so non-finite elements there are zeroed before P V
 //   warps 4-7, 8-11      softmax, one thread per row (tensor-memory lane): two sides
 // The two sides are two row tiles of a unit (kPair, units of more than 128 rows), or take turns at the
@@ -83,9 +84,11 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 // of the columns each, when the segment ends. Either way one side's softmax runs while the tensor
 // cores work for the other.
 //
-// A row's max moves only when it grows by more than 8 (log2), as in the prefill kernels. Weights enter P V
-// as two bf16 values, the rounded weight and its remainder (16 significant bits): the second product
-// is tensor time that waits for HBM anyway, and a row's error stays at its output's rounding.
+// A row's max moves only when it grows by more than 8 (log2), as in the prefill kernels, and as there the
+// weights of a sequence's first 128 positions enter P V as two bf16 values, the rounded weight and
+// its remainder (16 significant bits): a row of few keys would carry the full rounding of its weights.
+// Over more keys the roundings average out, to about the output's own (the remainder on every chunk took
+// 574 us on eight contexts of 32K-128K, 428 us without).
 //
 // Every wait is bounded; on a timeout the role records PKV_DEVERR_TIMEOUT, waits (bounded) for its own
 // copies and MMAs in flight, and the CTA frees its tensor memory and exits.
@@ -109,7 +112,7 @@ struct TreeCfg {
     static constexpr int kXchOff = kBarOff + kBarBytes;    // [2 sides][128 rows] (max, sum)
     static constexpr int kSmem = kXchOff + (kPair ? 0 : kSides * kRows * 8);
     static constexpr int kThreads = 384;
-    static constexpr int kLowRegs = 72, kHighRegs = 208;   // setmaxnreg split, launched at 168
+    static constexpr int kLowRegs = 104, kHighRegs = 200;   // setmaxnreg split, launched at 168
     static_assert(128 * kLowRegs + 256 * kHighRegs <= kThreads * 168, "register split");
     static constexpr uint32_t kTmemCols = 512, kSideCols = 256, kOCol = 128;
 };
@@ -185,14 +188,15 @@ struct TreeWalk {
 };
 
 // Bits e = 0 .. 15: whether a row sees position pos + e. Positions before `base` are context; bit j of the row's
-// mask words is draft j = position base + j.
-__device__ __forceinline__ uint32_t tree_bits16(const int64_t *words, int pos, int base, int n) {
+// mask words (word0: the first) is draft j = position base + j.
+__device__ __forceinline__ uint32_t tree_bits16(const int64_t *words, unsigned long long word0, int pos, int base, int n) {
     const int d = pos - base;
     if (d + 15 < 0) return 0xffffu;
     const int j0 = max(d, 0);             // first draft wanted
     if (j0 >= n) return d < 0 ? (1u << -d) - 1u : 0u;
     const int w = j0 >> 6, sh = j0 & 63;
-    unsigned long long v = (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w) >> sh;
+    unsigned long long v =
+        (w == 0 ? word0 : (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w)) >> sh;
     if (sh > 48 && (w + 1) * 64 < n)
         v |= (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w + 1) << (64 - sh);
     const int room = n - j0;
@@ -202,11 +206,80 @@ __device__ __forceinline__ uint32_t tree_bits16(const int64_t *words, int pos, i
     return bits & 0xffffu;
 }
 
+// One thread's copies: the K chunks of the worker's range and each unit's Q rows, or the V chunks.
+template <int D, bool kPair, bool kKeysAndQ>
+__device__ __forceinline__ void tree_produce(const CUtensorMap &tm, const CUtensorMap &tmq, const TreeParams &tp,
+                                             TreeWalk<D, kPair> at, uint8_t *base, TreeBars &b, int per_set,
+                                             int tile_tokens, int q_tokens, bool whole) {
+    using C = TreeCfg<D, kPair>;
+    constexpr int NS = C::kStages, CB = C::kChunkBlocks;
+    const DecodeParams &p = tp.d;
+    uint64_t *full = kKeysAndQ ? b.k_full : b.v_full, *empty = kKeysAndQ ? b.k_empty : b.v_empty;
+    uint8_t *ring = base + (kKeysAndQ ? C::kKOff : C::kVOff);
+    const uint64_t policy = l2_evict_first();
+    bool ok = true;
+    int seg = 0, r = 0;  // segments, ring position
+    do {
+        const int h = at.head();
+        const int nblk = (at.len + kBlock - 1) / kBlock, last_valid = at.len - (nblk - 1) * kBlock;
+        const int32_t *table = p.block_tables + (size_t)at.s * p.max_blocks_per_seq;
+        int id[CB], ahead[CB];  // the chunk's block ids (-1 past the sequence), and the next chunk's
+        auto ids = [&](int j, int (&out)[CB]) {
+#pragma unroll
+            for (int i = 0; i < CB; ++i) out[i] = j * CB + i < nblk ? __ldg(table + j * CB + i) : -1;
+        };
+        ids(at.c0, ahead);
+        for (int j = at.c0; j < at.c1 && ok; ++j, ++r) {
+            const int st = r % NS;
+#pragma unroll
+            for (int i = 0; i < CB; ++i) id[i] = ahead[i];
+            if (j + 1 < at.c1) ids(j + 1, ahead);
+            if (r >= NS && !(ok = mbar_wait(&empty[st], (r / NS - 1) & 1))) break;
+            mbar_arrive_expect_tx(&full[st], C::kStage);
+#pragma unroll
+            for (int i = 0; i < CB; ++i) {
+                const int blk = j * CB + i, y = blk == nblk - 1 ? last_valid - kBlock : 0;
+                int z = -1;  // outside the tensor: reads as zeros
+                if (blk < nblk) {
+                    if (id[i] < 0 || id[i] >= p.num_blocks) raise_error(PKV_DEVERR_BLOCK_ID);
+                    else z = id[i] * p.num_kv_heads + h;
+                }
+                if constexpr (kKeysAndQ) {  // [half][128 keys][64]
+#pragma unroll
+                    for (int u = 0; u < C::kHalves; ++u)
+                        tma_load_4d_hint(ring + st * C::kStage + u * C::kHalfRows + i * (kBlock * 128), &tm, 0, y, u, z,
+                                         &full[st], policy);
+                } else {                    // [block][half][16 keys][64]
+                    tma_load_4d_hint(ring + st * C::kStage + i * C::kBlockBytes, &tm, 0, y, 0, z, &full[st], policy);
+                }
+            }
+            if (kKeysAndQ && j == at.c0) {  // behind the first chunk's keys, which need not wait for the last S
+                if (seg > 0 && !(ok = mbar_wait(&b.q_empty, (seg - 1) & 1))) {
+                    ++r;
+                    break;
+                }
+                const int t0 = at.first_draft(per_set);
+                const int tiles = kPair && t0 + tile_tokens < at.n ? 2 : 1;
+                mbar_arrive_expect_tx(&b.q_full, tiles * C::kHalves * 128 * p.group * q_tokens);
+                for (int t = 0; t < tiles; ++t)
+                    for (int u = 0; u < C::kHalves; ++u)
+                        tma_load_4d(base + t * C::kQBytes + u * C::kHalfRows, &tmq, 0, u, h * p.group,
+                                    at.q0 + t0 + t * tile_tokens, &b.q_full);
+                ++seg;
+            }
+        }
+    } while (ok && at.next(tp, per_set, whole));
+    if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+    // no copy may land after the CTA is gone
+    for (int i = max(0, r - NS); i < r; ++i) mbar_wait(&full[i % NS], (i / NS) & 1);
+    if (seg > 0) mbar_wait(&b.q_full, (seg - 1) & 1);
+}
+
 template <int D, bool kPair>
 __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const TreeParams tp, float *partials,
-                          TreeCut *cuts, const int tile_tokens) {
+                          TreeCut *cuts, const int tile_tokens, const int q_tokens) {
     using C = TreeCfg<D, kPair>;
     constexpr int NS = C::kStages;
     const DecodeParams &p = tp.d;
@@ -230,7 +303,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             mbar_init(&b.k_empty[i], 1);
             mbar_init(&b.v_full[i], 1);
             mbar_init(&b.v_empty[i], 1);
-            mbar_init(&b.v_clean[i], 2);
+            mbar_init(&b.v_clean[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&b.s_full[i], 1);
@@ -313,82 +386,16 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     if (warp < 4) {
         setmaxnreg_dec<C::kLowRegs>();
         if (warp == 0) {
-            // ------------------------------ TMA producer ------------------------------
-            if (lane == 0) {
-                bool ok = true;
-                int seg = 0, r = 0;         // segments, ring position
-                int have_k = 0, have_v = 0; // chunks issued
-                const uint64_t policy = l2_evict_first();
-                do {
-                    const int h = at.head();
-                    const int nblk = (at.len + kBlock - 1) / kBlock, last_valid = at.len - (nblk - 1) * kBlock;
-                    const int32_t *table = p.block_tables + (size_t)at.s * p.max_blocks_per_seq;
-                    for (int j = at.c0; j < at.c1 && ok; ++j, ++r) {
-                        const int st = r % NS;
-                        // the chunk's tiles (-1: past the sequence or a bad id, reads as zeros) and first slots
-                        int z[C::kChunkBlocks], y[C::kChunkBlocks];
-#pragma unroll
-                        for (int bi = 0; bi < C::kChunkBlocks; ++bi) {
-                            const int blk = j * C::kChunkBlocks + bi;
-                            z[bi] = blk < nblk ? __ldg(table + blk) : -1;
-                        }
-                        if (r >= NS && !(ok = mbar_wait(&b.k_empty[st], (r / NS - 1) & 1))) break;
-#pragma unroll
-                        for (int bi = 0; bi < C::kChunkBlocks; ++bi) {
-                            const int blk = j * C::kChunkBlocks + bi;
-                            y[bi] = blk == nblk - 1 ? last_valid - kBlock : 0;
-                            if (blk < nblk) {
-                                if (z[bi] < 0 || z[bi] >= p.num_blocks) {
-                                    raise_error(PKV_DEVERR_BLOCK_ID);
-                                    z[bi] = -1;
-                                } else {
-                                    z[bi] = z[bi] * p.num_kv_heads + h;
-                                }
-                            }
-                        }
-                        // K as [half][128 keys][64]
-                        mbar_arrive_expect_tx(&b.k_full[st], C::kStage);
-#pragma unroll
-                        for (int bi = 0; bi < C::kChunkBlocks; ++bi)
-#pragma unroll
-                            for (int u = 0; u < C::kHalves; ++u)
-                                tma_load_4d_hint(base + C::kKOff + st * C::kStage + u * C::kHalfRows + bi * (kBlock * 128),
-                                                 &tmk, 0, y[bi], u, z[bi], &b.k_full[st], policy);
-                        have_k = r + 1;
-                        if (r >= NS && !(ok = mbar_wait(&b.v_empty[st], (r / NS - 1) & 1))) break;
-                        // V as [block][half][16 keys][64]
-                        mbar_arrive_expect_tx(&b.v_full[st], C::kStage);
-#pragma unroll
-                        for (int bi = 0; bi < C::kChunkBlocks; ++bi)
-                            tma_load_4d_hint(base + C::kVOff + st * C::kStage + bi * C::kBlockBytes, &tmv, 0, y[bi], 0,
-                                             z[bi], &b.v_full[st], policy);
-                        have_v = r + 1;
-                        if (j == at.c0) {  // behind the first chunk's keys, so that these need not wait for the last S
-                            if (seg > 0 && !(ok = mbar_wait(&b.q_empty, (seg - 1) & 1))) break;
-                            const int t0 = at.first_draft(per_set);
-                            const int tiles = kPair && t0 + tile_tokens < at.n ? 2 : 1;
-                            mbar_arrive_expect_tx(&b.q_full, tiles * C::kHalves * 128 * g * tile_tokens);
-                            for (int t = 0; t < tiles; ++t)
-                                for (int u = 0; u < C::kHalves; ++u)
-                                    tma_load_4d(base + t * C::kQBytes + u * C::kHalfRows, &tmq, 0, u, h * g,
-                                                at.q0 + t0 + t * tile_tokens, &b.q_full);
-                            ++seg;
-                        }
-                    }
-                } while (ok && at.next(tp, per_set, whole));
-                if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
-                // no copy may land after the CTA is gone
-                for (int i = max(0, have_k - NS); i < have_k; ++i) mbar_wait(&b.k_full[i % NS], (i / NS) & 1);
-                for (int i = max(0, have_v - NS); i < have_v; ++i) mbar_wait(&b.v_full[i % NS], (i / NS) & 1);
-                if (seg > 0) mbar_wait(&b.q_full, (seg - 1) & 1);
-            }
+            // ------------------------------ TMA: Q and K ------------------------------
+            if (lane == 0) tree_produce<D, kPair, true>(tmk, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole);
         } else if (warp == 1) {
             // ------------------------------ MMA issuer ------------------------------
             if (lane == 0) {
                 constexpr uint32_t idesc_s = idesc_bf16_f32(C::kRows, C::kKeys, false, false);
                 constexpr uint32_t idesc_o = idesc_bf16_f32(C::kRows, D, false, true);
                 bool ok = true;
-                int seg = 0, r0 = 0, pcount[2] = {0, 0};
+                int seg = 0, r0 = 0;
+                uint32_t p_parity = 0;  // bit of a side
                 auto issue_s = [&](int side, int r) {
                     const uint32_t qt = q_s + (kPair ? side * C::kQBytes : 0);
 #pragma unroll
@@ -398,14 +405,15 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                                   smem_desc_sw128(k_s + (r % NS) * C::kStage + off, 16, 1024), idesc_s, kk > 0);
                     }
                 };
-                auto issue_pv = [&](int side, int r, bool first) {
+                auto issue_pv = [&](int side, int r, bool first, bool split) {
 #pragma unroll
                     for (int kk = 0; kk < C::kChunkBlocks; ++kk) {
                         const uint64_t vd =
                             smem_desc_sw128(v_s + (r % NS) * C::kStage + kk * C::kBlockBytes, kBlock * 128, 1024);
                         const uint32_t pa = tmem + side * C::kSideCols + (kk >> 1) * 32 + (kk & 1) * 8;
                         umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa, vd, idesc_o, !first || kk > 0);
-                        umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa + 16, vd, idesc_o, true);
+                        if (split)
+                            umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa + 16, vd, idesc_o, true);
                     }
                 };
                 auto wait_k = [&](int r) { return mbar_wait(&b.k_full[r % NS], (r / NS) & 1); };
@@ -419,7 +427,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                                mbar_wait(&b.v_clean[st], ((r0 + k) / NS) & 1);
                     };
                     auto weights_ready = [&](int side) {
-                        const bool good = mbar_wait(&b.p_full[side], pcount[side]++ & 1);
+                        const bool good = mbar_wait(&b.p_full[side], (p_parity >> side) & 1);
+                        p_parity ^= 1u << side;
                         tc_fence_after();
                         return good;
                     };
@@ -435,7 +444,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             ok = values_ready(k) && (k + 1 == nc || wait_k(r0 + k + 1));
                             for (int t = 0; t < tiles && ok; ++t) {
                                 if (!(ok = weights_ready(t))) break;
-                                issue_pv(t, r0 + k, k == 0);
+                                issue_pv(t, r0 + k, k == 0, at.c0 + k == 0);
                                 if (k + 1 < nc) {
                                     issue_s(t, r0 + k + 1);
                                     umma_commit(&b.s_full[t]);
@@ -460,11 +469,12 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             if (k == nc - 1) umma_commit(&b.q_empty);
                             return true;
                         };
-                        ok = scores(0);
-                        for (int k = 0; k < nc && ok; ++k) {
+#pragma unroll 1
+                        for (int k = -1; k < nc && ok; ++k) {
                             if (k + 1 < nc && !(ok = scores(k + 1))) break;
+                            if (k < 0) continue;
                             if (!(ok = values_ready(k) && weights_ready(k & 1))) break;
-                            issue_pv(k & 1, r0 + k, k < 2);
+                            issue_pv(k & 1, r0 + k, k < 2, at.c0 + k == 0);
                             umma_commit(&b.v_empty[(r0 + k) % NS]);
                             if (k + 2 >= nc) umma_commit(&b.o_done[k & 1]);
                         }
@@ -477,6 +487,9 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 mbar_wait(&b.drain, 0);
             }
             __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------ TMA: V ------------------------------
+            if (lane == 0) tree_produce<D, kPair, false>(tmv, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole);
         } else {
             // ------------------------------ the drafts' values ------------------------------
             bool ok = true;
@@ -492,7 +505,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     const int blk0 = (at.c0 + k) * C::kChunkBlocks;
                     const int b_lo = max(0, ctx / kBlock - blk0), b_hi = min(C::kChunkBlocks, nblk - blk0);
                     uint8_t *vst = base + C::kVOff + st * C::kStage;
-                    for (int i = b_lo * (C::kBlockBytes / 16) + (tid - 64); i < b_hi * (C::kBlockBytes / 16); i += 64) {
+                    for (int i = b_lo * (C::kBlockBytes / 16) + lane; i < b_hi * (C::kBlockBytes / 16); i += 32) {
                         const uint4 v = reinterpret_cast<const uint4 *>(vst)[i];
                         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
                         bool bad = false;
@@ -525,11 +538,10 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         // scores stay raw: x * sl is the log2-domain score, the sign is folded in; a scale of 0 becomes one that
         // leaves every score 0, so that a masked -inf stays -inf
         const float sl = fmaxf(fabsf(p.scale_log2), 1e-30f);
-        const float sgn = p.scale_log2 < 0.f ? -1.f : 1.f;
-        const bool no_scale = p.scale_log2 == 0.f;
         float2 *xch = reinterpret_cast<float2 *>(base + C::kXchOff);
         bool ok = true;
-        int scount = 0, ocount[2] = {0, 0}, seg = 0;
+        int scount = 0, seg = 0;
+        uint32_t o_parity = 0;  // bit of a side
         TreeCut cut{0, 0, 0, 0};
         do {
             const int nc = at.c1 - at.c0, h = at.head();
@@ -538,6 +550,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             const bool row_ok = row < rows;
             const int draft = tok0 + row / g;
             const int64_t *words = tp.mask + (size_t)(at.q0 + (row_ok ? draft : 0)) * tp.mask_words;
+            const unsigned long long word0 = (unsigned long long)__ldg(reinterpret_cast<const long long *>(words));
             const int ctx = at.len - at.n;
             const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
             const bool warp_rows = quad * 32 < rows;   // a warp without rows only keeps the barriers' count
@@ -549,110 +562,159 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 if (warp_rows) {
                     tc_fence_after();
                     const int j = at.c0 + k;
-                    float x[4][32];  // the whole row of S in registers
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) tmem_ld32(cols + q * 32, x[q]);
-                    tmem_wait_ld();
-                    if (sgn < 0.f || no_scale) {
-                        const float f = no_scale ? 0.f : -1.f;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[q][e] *= f;
-                    }
                     // only chunks that hold drafts or the sequence's end need masks
-                    if ((j + 1) * C::kKeys > ctx || (j + 1) * C::kChunkBlocks >= nblk) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t see = 0;
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int blk = j * C::kChunkBlocks + 2 * q + i;
-                                uint32_t bits = 0;
-                                if (blk < nblk) {
-                                    const int shift = blk == nblk - 1 ? lo : 0;  // (loaded that many rows early)
-                                    bits = tree_bits16(words, blk * kBlock - shift, ctx, at.n) & (0xffffu << shift);
-                                }
-                                see |= (bits & 0xffffu) << (16 * i);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) x[q][e] = (see >> e) & 1u ? x[q][e] : -INFINITY;
-                        }
-                    }
-                    float mxs[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mxs[i] = -INFINITY;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2)
-                            mxs[(e >> 1) & 7] = max3f(mxs[(e >> 1) & 7], x[q][e], x[q][e + 1]);
-                    const float mx = fmaxf(max3f(max3f(mxs[0], mxs[1], mxs[2]), mxs[3], mxs[4]),
-                                           max3f(mxs[5], mxs[6], mxs[7]));
-                    const float m_new = fmaxf(m, mx * sl);
-                    const bool move = m_new > m + 8.f;
-                    const float m_use = move ? m_new : m;
-                    const float ms = m_use == -INFINITY ? 0.f : m_use;
-                    const float alpha = ex2_approx(m - ms);
-                    // this side's O is quiescent: P V of its previous chunk ran before this S
-                    if (k >= k_step && __any_sync(0xffffffffu, move && m != -INFINITY)) {
+                    const bool masked = (j + 1) * C::kKeys > ctx || (j + 1) * C::kChunkBlocks >= nblk;
+                    // The row of S is read twice, for the max and for the weights, in rolled loops over parts of it:
+                    // one warp a scheduler and side runs this code, and unrolled over the row it outgrew
+                    // the instruction cache (a third of the warps' cycles waited for instructions).
+                    // (1) the new reference max and the rescale of this side's O where it moved
+                    auto move_max = [&](float mx) {
+                        const float m_new = fmaxf(m, mx * sl);
+                        const bool move = m_new > m + 8.f;
+                        const float m_use = move ? m_new : m;
+                        const float ms = m_use == -INFINITY ? 0.f : m_use;
+                        const float alpha = ex2_approx(m - ms);
+                        // O is quiescent: P V of this side's previous chunk ran before this S
+                        if (k >= k_step && __any_sync(0xffffffffu, move && m != -INFINITY)) {
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            float o[32];
-                            tmem_ld32(cols + C::kOCol + c * 32, o);
-                            tmem_wait_ld();
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                tmem_ld32(cols + C::kOCol + c * 32, o);
+                                tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                            tmem_st32(cols + C::kOCol + c * 32, o);
+                                for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                                tmem_st32(cols + C::kOCol + c * 32, o);
+                            }
                         }
-                    }
-                    m = m_use;
-                    // P over each quarter's score columns: keys 32 q + 2 i, + 1 at column 32 q + i, remainders at + 16
-                    const uint64_t sl2 = pack_f2(sl, sl), nms2 = pack_f2(-ms, -ms);
-                    uint64_t rss[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t hi[16], rem[16];
+                        m = m_use;
+                        l *= alpha;
+                        return ms;
+                    };
+                    // (2) 32 weights: P over their own score columns (keys 2 i, + 1 at column i), remainders at + 16
+                    auto weights = [&](const float (&x)[32], uint32_t at_col, uint64_t sl2, uint64_t nms2,
+                                       uint64_t (&rss)[4], bool split) {
+                        uint32_t hi[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             float a0, a1;
-                            unpack_f2(fma_f2(pack_f2(x[q][2 * i], x[q][2 * i + 1]), sl2, nms2), a0, a1);
+                            unpack_f2(fma_f2(pack_f2(x[2 * i], x[2 * i + 1]), sl2, nms2), a0, a1);
                             const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
                             rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
                             const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
                             hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
-                            const float2 fh = __bfloat1622float2(ph);
-                            const __nv_bfloat162 pl = __floats2bfloat162_rn(e0 - fh.x, e1 - fh.y);
-                            rem[i] = *reinterpret_cast<const uint32_t *>(&pl);
                         }
-                        tmem_st16(cols + q * 32, hi);
-                        tmem_st16(cols + q * 32 + 16, rem);
+                        tmem_st16(at_col, hi);
+                        if (split) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                float a0, a1;
+                                unpack_f2(fma_f2(pack_f2(x[2 * i], x[2 * i + 1]), sl2, nms2), a0, a1);
+                                const __nv_bfloat162 pl =
+                                    __floats2bfloat162_rn(ex2_approx(a0) - __uint_as_float(hi[i] << 16),
+                                                          ex2_approx(a1) - __uint_as_float(hi[i] & 0xffff0000u));
+                                hi[i] = *reinterpret_cast<const uint32_t *>(&pl);
+                            }
+                            tmem_st16(at_col + 16, hi);
+                        }
+                    };
+                    uint64_t rss[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
+                    if (!masked && j != 0 && p.scale_log2 > 0.f) {
+                        float x[2][32], mx = -INFINITY;
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            tmem_ld32(cols + half * 64, x[0]);
+                            tmem_ld32(cols + half * 64 + 32, x[1]);
+                            tmem_wait_ld();
+                            float mxs[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2)
+                                    mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], x[q][e], x[q][e + 1]);
+                            mx = fmaxf(max3f(mxs[0], mxs[1], mxs[2]), mxs[3]);
+                        }
+                        const float ms = move_max(mx);
+                        const uint64_t sl2 = pack_f2(sl, sl), nms2 = pack_f2(-ms, -ms);
+#pragma unroll 1
+                        for (int half = 0; half < 2; ++half) {
+                            tmem_ld32(cols + half * 64, x[0]);
+                            tmem_ld32(cols + half * 64 + 32, x[1]);
+                            tmem_wait_ld();
+                            weights(x[0], cols + half * 64, sl2, nms2, rss, false);
+                            weights(x[1], cols + half * 64 + 32, sl2, nms2, rss, false);
+                        }
+                    } else {
+                        // chunks with masks, a sequence's first chunk (whose remainders the MMA thread uses), and
+                        // scales that are not positive: a quarter of the row at a time
+                        const float f = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
+                        float x[32], mx = -INFINITY, ms = 0.f;
+#pragma unroll 1
+                        for (int step = 0; step < 8; ++step) {
+                            const int q = step & 3;
+                            tmem_ld32(cols + q * 32, x);
+                            tmem_wait_ld();
+                            if (f != 1.f) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] *= f;
+                            }
+                            // the quarter's two blocks: which of their columns this row sees
+                            const int blk = j * C::kChunkBlocks + 2 * q;
+                            if ((blk + 2) * kBlock > ctx || blk + 2 >= nblk) {
+                                uint32_t see = 0;
+#pragma unroll 1
+                                for (int i = 0; i < 2 && blk + i < nblk; ++i) {
+                                    const int shift = blk + i == nblk - 1 ? lo : 0;  // (loaded that many rows early)
+                                    const uint32_t bits =
+                                        tree_bits16(words, word0, (blk + i) * kBlock - shift, ctx, at.n);
+                                    see |= (bits & (0xffffu << shift) & 0xffffu) << (16 * i);
+                                }
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = see & (1u << e) ? x[e] : -INFINITY;
+                            }
+                            if (step < 4) {
+                                float mxs[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2)
+                                    mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], x[e], x[e + 1]);
+                                mx = fmaxf(max3f(mxs[0], mxs[1], mxs[2]), mxs[3]);
+                                if (step == 3) ms = move_max(mx);
+                            } else {
+                                weights(x, cols + q * 32, pack_f2(sl, sl), pack_f2(-ms, -ms), rss, j == 0);
+                            }
+                        }
                     }
                     tmem_wait_st();
                     float rs[8];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) unpack_f2(rss[i], rs[2 * i], rs[2 * i + 1]);
-                    l = l * alpha + (((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7])));
+                    l += ((rs[0] + rs[1]) + (rs[2] + rs[3])) + ((rs[4] + rs[5]) + (rs[6] + rs[7]));
                     tc_fence_before();
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p_full[side]);
             }
             // ---- the segment ends here ----
-            const bool used[2] = {true, nc > 1};       // (two sides on one tile: chunks in turn)
+            const bool both = nc > 1;                  // (two sides on one tile take its chunks in turn)
             const bool uncut = at.c0 == 0 && at.c1 == at.chunks;
             if (ok) {
                 if constexpr (kPair) {
-                    if (active) ok = warp_wait(&b.o_done[side], ocount[side]++ & 1);
+                    if (active) {
+                        ok = warp_wait(&b.o_done[side], o_parity & 1);
+                        o_parity ^= 1;
+                    }
                 } else {
                     xch[side * C::kRows + row] = make_float2(m, l);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&b.x_full[side]);
                     ok = warp_wait(&b.x_full[side ^ 1], seg & 1);
+#pragma unroll
                     for (int t = 0; t < 2; ++t)
-                        if (ok && used[t]) ok = warp_wait(&b.o_done[t], ocount[t]++ & 1);
+                        if (ok && (t == 0 || both)) {
+                            ok = warp_wait(&b.o_done[t], (o_parity >> t) & 1);
+                            o_parity ^= 1u << t;
+                        }
                 }
             }
             if (ok && warp_rows) {
@@ -689,7 +751,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 if (!uncut && d0 == 0 && row_ok)
                     *reinterpret_cast<float2 *>(slot + 2 * unit_row) = make_float2(M, L);
                 float *po = slot + 2 * C::kUnitRows + (size_t)unit_row * D + d0;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kMine / 32; ++c) {
                     float o[32];
                     if constexpr (kPair) {
@@ -698,12 +760,12 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     } else {
                         float o1[32];
                         tmem_ld32(lane_cols + C::kOCol + d0 + c * 32, o);
-                        if (used[1]) tmem_ld32(lane_cols + C::kSideCols + C::kOCol + d0 + c * 32, o1);
+                        if (both) tmem_ld32(lane_cols + C::kSideCols + C::kOCol + d0 + c * 32, o1);
                         tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
                             o[e] *= f[0];
-                            if (used[1]) o[e] = fmaf(o1[e], f[1], o[e]);
+                            if (both) o[e] = fmaf(o1[e], f[1], o[e]);
                         }
                     }
                     if (poison) {
