@@ -73,8 +73,8 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 // The work of a drafts' batch is to read the context once: 4 D bytes of K and V a token and
 // kv head, against 4 D flops per row, so up to about 256 rows HBM bounds it, and the roles below are
 // there to keep 64 to 190 KB of copies in flight per SM:
-//   warps 0 and 2, one   TMA: a unit's Q rows and the K chunks; the V chunks (two threads, so that neither
-//   thread each          ring waits for the other's stages)
+//   warps 0 and 2        TMA: a unit's Q rows and the K chunks; the V chunks (two warps, so that neither
+//                        ring waits for the other's stages)
 //   warp 1, one thread   MMA: S = Q K^T (128 x 128, fp32 in tensor memory); O += P V with P from tensor memory
 //   warp 3               the values of the drafts: a row that does not see a draft must not meet its
 //                        NaN (0 * NaN is NaN), so non-finite elements there are zeroed before P V
@@ -85,10 +85,10 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 // cores work for the other.
 //
 // A row's max moves only when it grows by more than 8 (log2), as in the prefill kernels, and as there the
-// weights of a sequence's first 128 positions enter P V as two bf16 values, the rounded weight and
-// its remainder (16 significant bits): a row of few keys would carry the full rounding of its weights.
-// Over more keys the roundings average out, to about the output's own (the remainder on every chunk took
-// 574 us on eight contexts of 32K-128K, 428 us without).
+// weights of rows that may see few keys enter P V as two bf16 values, the rounded weight and its
+// remainder (16 significant bits): such a row would carry the full rounding of its weights. Over more
+// keys the roundings average out, to about the output's own (the remainder on every chunk took 574 us on
+// eight contexts of 32K-128K, 428 us without).
 //
 // Every wait is bounded; on a timeout the role records PKV_DEVERR_TIMEOUT, waits (bounded) for its own
 // copies and MMAs in flight, and the CTA frees its tensor memory and exits.
@@ -138,6 +138,9 @@ struct TreeCut {
     int segments, q_row, drafts, head;  // first query row of the unit, its drafts, first query head
 };
 
+// Whether a unit's first chunk gives its weights' remainders too: where a row may see fewer than 64 keys.
+__device__ __forceinline__ bool tree_split(int ctx) { return ctx < kPrefillSplitPositions; }
+
 // A worker's way along the line: one segment (a unit's chunks c0 .. c1 - 1) at a time.
 template <int D, bool kPair>
 struct TreeWalk {
@@ -183,34 +186,48 @@ struct TreeWalk {
         segment(whole);
         return true;
     }
-    __device__ __forceinline__ int head() const { return unit / sets; }
-    __device__ __forceinline__ int first_draft(int per_set) const { return (unit % sets) * per_set; }
+    // (one tile's worth of rows holds every tree where units are single tiles: one set)
+    __device__ __forceinline__ int head() const { return kPair ? unit / sets : unit; }
+    __device__ __forceinline__ int first_draft(int per_set) const { return kPair ? (unit % sets) * per_set : 0; }
 };
 
-// Bits e = 0 .. 15: whether a row sees position pos + e. Positions before `base` are context; bit j of the row's
-// mask words (word0: the first) is draft j = position base + j.
-__device__ __forceinline__ uint32_t tree_bits16(const int64_t *words, unsigned long long word0, int pos, int base, int n) {
-    const int d = pos - base;
-    if (d + 15 < 0) return 0xffffu;
-    const int j0 = max(d, 0);             // first draft wanted
-    if (j0 >= n) return d < 0 ? (1u << -d) - 1u : 0u;
-    const int w = j0 >> 6, sh = j0 & 63;
-    unsigned long long v =
-        (w == 0 ? word0 : (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w)) >> sh;
-    if (sh > 48 && (w + 1) * 64 < n)
-        v |= (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w + 1) << (64 - sh);
-    const int room = n - j0;
-    uint32_t bits = (uint32_t)v & 0xffffu;
-    if (room < 16) bits &= (1u << room) - 1u;
-    if (d < 0) bits = (bits << -d) | ((1u << -d) - 1u);
-    return bits & 0xffffu;
+// Bits e = 0 .. 63: whether a row sees position pos + e. Positions before ctx are context; bit j of the row's
+// mask words (word0: the first) is draft j < n = position ctx + j.
+__device__ __forceinline__ unsigned long long tree_visible(const int64_t *words, unsigned long long word0, int pos,
+                                                           int ctx, int n) {
+    const int d = pos - ctx;
+    if (d <= -64) return ~0ull;
+    const int j0 = max(d, 0);  // first draft wanted
+    unsigned long long v = 0;
+    if (j0 < n) {
+        auto word = [&](int w) {
+            return w == 0 ? word0 : (unsigned long long)__ldg(reinterpret_cast<const long long *>(words) + w);
+        };
+        const int w = j0 >> 6, sh = j0 & 63;
+        v = word(w) >> sh;
+        if (sh > 0 && (w + 1) * 64 < n) v |= word(w + 1) << (64 - sh);
+        if (n - j0 < 64) v &= (1ull << (n - j0)) - 1ull;
+    }
+    return d < 0 ? (v << -d) | ((1ull << -d) - 1ull) : v;
 }
 
-// One thread's copies: the K chunks of the worker's range and each unit's Q rows, or the V chunks.
+// The same for the 64 score columns of blocks blk .. blk + 3: the sequence's last block was loaded lo rows early, so
+// its token t is column lo + t; columns of later blocks hold nothing.
+__device__ __forceinline__ unsigned long long tree_columns(unsigned long long visible, int blk, int nblk, int lo) {
+    const int last = nblk - 1 - blk;
+    if (last >= 4) return visible;
+    if (last < 0) return 0ull;
+    const unsigned long long before = visible & ((1ull << (16 * last)) - 1ull);
+    const unsigned long long tokens = (visible >> (16 * last)) & ((1ull << (kBlock - lo)) - 1ull);
+    return before | (tokens << (16 * last + lo));
+}
+
+// One warp's copies, issued by its first lane: the K chunks of the worker's range and each unit's Q rows, or the V
+// chunks. Lane i < 8 holds the id of a chunk's i-th block, and the next chunk's ahead of use.
 template <int D, bool kPair, bool kKeysAndQ>
 __device__ __forceinline__ void tree_produce(const CUtensorMap &tm, const CUtensorMap &tmq, const TreeParams &tp,
                                              TreeWalk<D, kPair> at, uint8_t *base, TreeBars &b, int per_set,
-                                             int tile_tokens, int q_tokens, bool whole) {
+                                             int tile_tokens, int q_tokens, bool whole, int lane) {
     using C = TreeCfg<D, kPair>;
     constexpr int NS = C::kStages, CB = C::kChunkBlocks;
     const DecodeParams &p = tp.d;
@@ -223,53 +240,56 @@ __device__ __forceinline__ void tree_produce(const CUtensorMap &tm, const CUtens
         const int h = at.head();
         const int nblk = (at.len + kBlock - 1) / kBlock, last_valid = at.len - (nblk - 1) * kBlock;
         const int32_t *table = p.block_tables + (size_t)at.s * p.max_blocks_per_seq;
-        int id[CB], ahead[CB];  // the chunk's block ids (-1 past the sequence), and the next chunk's
-        auto ids = [&](int j, int (&out)[CB]) {
-#pragma unroll
-            for (int i = 0; i < CB; ++i) out[i] = j * CB + i < nblk ? __ldg(table + j * CB + i) : -1;
-        };
-        ids(at.c0, ahead);
-        for (int j = at.c0; j < at.c1 && ok; ++j, ++r) {
-            const int st = r % NS;
-#pragma unroll
-            for (int i = 0; i < CB; ++i) id[i] = ahead[i];
-            if (j + 1 < at.c1) ids(j + 1, ahead);
-            if (r >= NS && !(ok = mbar_wait(&empty[st], (r / NS - 1) & 1))) break;
-            mbar_arrive_expect_tx(&full[st], C::kStage);
-#pragma unroll
+        auto id_of = [&](int j) { return lane < CB && j * CB + lane < nblk ? __ldg(table + j * CB + lane) : -1; };
+        int ahead = id_of(at.c0);
+        for (int j = at.c0; j < at.c1; ++j, ++r) {
+            const int st = r % NS, blk = j * CB + lane;
+            const int id = ahead;
+            if (j + 1 < at.c1) ahead = id_of(j + 1);
+            // this lane's block: its tile (outside the tensor, reading as zeros, past the sequence and for a bad
+            // id) and its first slot
+            int z = -1;
+            const int y = blk == nblk - 1 ? last_valid - kBlock : 0;
+            if (lane < CB && blk < nblk) {
+                if (id < 0 || id >= p.num_blocks) raise_error(PKV_DEVERR_BLOCK_ID);
+                else z = id * p.num_kv_heads + h;
+            }
+            if (r >= NS && !(ok = warp_wait(&empty[st], (r / NS - 1) & 1))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&full[st], C::kStage);
+            uint8_t *dst = ring + st * C::kStage;
+#pragma unroll 1
             for (int i = 0; i < CB; ++i) {
-                const int blk = j * CB + i, y = blk == nblk - 1 ? last_valid - kBlock : 0;
-                int z = -1;  // outside the tensor: reads as zeros
-                if (blk < nblk) {
-                    if (id[i] < 0 || id[i] >= p.num_blocks) raise_error(PKV_DEVERR_BLOCK_ID);
-                    else z = id[i] * p.num_kv_heads + h;
-                }
-                if constexpr (kKeysAndQ) {  // [half][128 keys][64]
+                const int zi = __shfl_sync(0xffffffffu, z, i), yi = __shfl_sync(0xffffffffu, y, i);
+                if (lane == 0) {
+                    if constexpr (kKeysAndQ) {  // [half][128 keys][64]
 #pragma unroll
-                    for (int u = 0; u < C::kHalves; ++u)
-                        tma_load_4d_hint(ring + st * C::kStage + u * C::kHalfRows + i * (kBlock * 128), &tm, 0, y, u, z,
-                                         &full[st], policy);
-                } else {                    // [block][half][16 keys][64]
-                    tma_load_4d_hint(ring + st * C::kStage + i * C::kBlockBytes, &tm, 0, y, 0, z, &full[st], policy);
+                        for (int u = 0; u < C::kHalves; ++u)
+                            tma_load_4d_hint(dst + u * C::kHalfRows, &tm, 0, yi, u, zi, &full[st], policy);
+                    } else {                    // [block][half][16 keys][64]
+                        tma_load_4d_hint(dst, &tm, 0, yi, 0, zi, &full[st], policy);
+                    }
                 }
+                dst += kKeysAndQ ? kBlock * 128 : C::kBlockBytes;
             }
             if (kKeysAndQ && j == at.c0) {  // behind the first chunk's keys, which need not wait for the last S
-                if (seg > 0 && !(ok = mbar_wait(&b.q_empty, (seg - 1) & 1))) {
+                if (seg > 0 && !(ok = warp_wait(&b.q_empty, (seg - 1) & 1))) {
                     ++r;
                     break;
                 }
-                const int t0 = at.first_draft(per_set);
-                const int tiles = kPair && t0 + tile_tokens < at.n ? 2 : 1;
-                mbar_arrive_expect_tx(&b.q_full, tiles * C::kHalves * 128 * p.group * q_tokens);
-                for (int t = 0; t < tiles; ++t)
-                    for (int u = 0; u < C::kHalves; ++u)
-                        tma_load_4d(base + t * C::kQBytes + u * C::kHalfRows, &tmq, 0, u, h * p.group,
-                                    at.q0 + t0 + t * tile_tokens, &b.q_full);
+                if (lane == 0) {
+                    const int t0 = at.first_draft(per_set);
+                    const int tiles = kPair && t0 + tile_tokens < at.n ? 2 : 1;
+                    mbar_arrive_expect_tx(&b.q_full, tiles * C::kHalves * 128 * p.group * q_tokens);
+#pragma unroll 1
+                    for (int t = 0; t < tiles * C::kHalves; ++t)
+                        tma_load_4d(base + (t / C::kHalves) * C::kQBytes + (t % C::kHalves) * C::kHalfRows, &tmq, 0,
+                                    t % C::kHalves, h * p.group, at.q0 + t0 + (t / C::kHalves) * tile_tokens, &b.q_full);
+                }
                 ++seg;
             }
         }
     } while (ok && at.next(tp, per_set, whole));
-    if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+    if (!ok && lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
     // no copy may land after the CTA is gone
     for (int i = max(0, r - NS); i < r; ++i) mbar_wait(&full[i % NS], (i / NS) & 1);
     if (seg > 0) mbar_wait(&b.q_full, (seg - 1) & 1);
@@ -283,10 +303,11 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     using C = TreeCfg<D, kPair>;
     constexpr int NS = C::kStages;
     const DecodeParams &p = tp.d;
-    extern __shared__ __align__(1024) uint8_t base[];  // (three stages leave no room to align it by hand)
+    extern __shared__ __align__(1024) uint8_t tree_smem[];  // (three stages leave no room to align it by hand)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = p.group, per_set = C::kTiles * tile_tokens;
     const bool whole = cuts == nullptr;
+    uint8_t *const base = tree_smem;
     if (smem_u32(base) & 1023u) {  // the swizzle's atoms would not be where the descriptors say
         if (tid == 0) raise_error(PKV_DEVERR_TIMEOUT);
         return;
@@ -387,7 +408,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         setmaxnreg_dec<C::kLowRegs>();
         if (warp == 0) {
             // ------------------------------ TMA: Q and K ------------------------------
-            if (lane == 0) tree_produce<D, kPair, true>(tmk, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole);
+            tree_produce<D, kPair, true>(tmk, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole, lane);
         } else if (warp == 1) {
             // ------------------------------ MMA issuer ------------------------------
             if (lane == 0) {
@@ -398,7 +419,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 uint32_t p_parity = 0;  // bit of a side
                 auto issue_s = [&](int side, int r) {
                     const uint32_t qt = q_s + (kPair ? side * C::kQBytes : 0);
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::kHalfRows + (kk & 3) * 32;
                         umma_bf16(tmem + side * C::kSideCols, smem_desc_sw128(qt + off, 16, 1024),
@@ -406,7 +427,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     }
                 };
                 auto issue_pv = [&](int side, int r, bool first, bool split) {
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 0; kk < C::kChunkBlocks; ++kk) {
                         const uint64_t vd =
                             smem_desc_sw128(v_s + (r % NS) * C::kStage + kk * C::kBlockBytes, kBlock * 128, 1024);
@@ -444,7 +465,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             ok = values_ready(k) && (k + 1 == nc || wait_k(r0 + k + 1));
                             for (int t = 0; t < tiles && ok; ++t) {
                                 if (!(ok = weights_ready(t))) break;
-                                issue_pv(t, r0 + k, k == 0, at.c0 + k == 0);
+                                issue_pv(t, r0 + k, k == 0, at.c0 + k == 0 && tree_split(at.len - at.n));
                                 if (k + 1 < nc) {
                                     issue_s(t, r0 + k + 1);
                                     umma_commit(&b.s_full[t]);
@@ -474,7 +495,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             if (k + 1 < nc && !(ok = scores(k + 1))) break;
                             if (k < 0) continue;
                             if (!(ok = values_ready(k) && weights_ready(k & 1))) break;
-                            issue_pv(k & 1, r0 + k, k < 2, at.c0 + k == 0);
+                            issue_pv(k & 1, r0 + k, k < 2, at.c0 + k == 0 && tree_split(at.len - at.n));
                             umma_commit(&b.v_empty[(r0 + k) % NS]);
                             if (k + 2 >= nc) umma_commit(&b.o_done[k & 1]);
                         }
@@ -489,7 +510,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ------------------------------ TMA: V ------------------------------
-            if (lane == 0) tree_produce<D, kPair, false>(tmv, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole);
+            tree_produce<D, kPair, false>(tmv, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole, lane);
         } else {
             // ------------------------------ the drafts' values ------------------------------
             bool ok = true;
@@ -533,6 +554,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         setmaxnreg_inc<C::kHighRegs>();
         // ------------------------------ softmax ------------------------------
         const int side = (warp - 4) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const int row_draft = row / g, row_head = row - row_draft * g;
         const uint32_t lane_cols = tmem + ((uint32_t)(quad * 32) << 16);
         const uint32_t cols = lane_cols + side * C::kSideCols;
         // scores stay raw: x * sl is the log2-domain score, the sign is folded in; a scale of 0 becomes one that
@@ -548,7 +570,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             const int tok0 = at.first_draft(per_set) + (kPair ? side * tile_tokens : 0);
             const int rows = max(0, min(at.n - tok0, tile_tokens)) * g;
             const bool row_ok = row < rows;
-            const int draft = tok0 + row / g;
+            const int draft = tok0 + row_draft;
             const int64_t *words = tp.mask + (size_t)(at.q0 + (row_ok ? draft : 0)) * tp.mask_words;
             const unsigned long long word0 = (unsigned long long)__ldg(reinterpret_cast<const long long *>(words));
             const int ctx = at.len - at.n;
@@ -564,124 +586,116 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     const int j = at.c0 + k;
                     // only chunks that hold drafts or the sequence's end need masks
                     const bool masked = (j + 1) * C::kKeys > ctx || (j + 1) * C::kChunkBlocks >= nblk;
-                    // The row of S is read twice, for the max and for the weights, in rolled loops over parts of it:
-                    // one warp a scheduler and side runs this code, and unrolled over the row it outgrew
-                    // the instruction cache (a third of the warps' cycles waited for instructions).
-                    // (1) the new reference max and the rescale of this side's O where it moved
-                    auto move_max = [&](float mx) {
-                        const float m_new = fmaxf(m, mx * sl);
-                        const bool move = m_new > m + 8.f;
-                        const float m_use = move ? m_new : m;
-                        const float ms = m_use == -INFINITY ? 0.f : m_use;
-                        const float alpha = ex2_approx(m - ms);
-                        // O is quiescent: P V of this side's previous chunk ran before this S
-                        if (k >= k_step && __any_sync(0xffffffffu, move && m != -INFINITY)) {
-#pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float o[32];
-                                tmem_ld32(cols + C::kOCol + c * 32, o);
-                                tmem_wait_ld();
+                    // The row of S is read twice, for the max and for the weights, in short rolled loops, and what
+                    // only some chunks need stands apart: one warp a scheduler and side runs this code, and
+                    // its time follows the instructions that must be fetched (unrolled over the row, with
+                    // the masks in line, a chunk took 5000 cycles, a third of them without an instruction;
+                    // so it takes 2000).
+                    if (__builtin_expect(masked || p.scale_log2 <= 0.f, 0)) {
+                        // S rewritten: the sign of the scale folded in, -inf where the row does not see
+                        const float f = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
+                        unsigned long long see[2] = {~0ull, ~0ull};
+                        if (masked) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                                tmem_st32(cols + C::kOCol + c * 32, o);
+                            for (int i = 0; i < 2; ++i) {
+                                const int blk = j * C::kChunkBlocks + 4 * i;
+                                see[i] = tree_columns(tree_visible(words, word0, blk * kBlock, ctx, at.n), blk, nblk, lo);
                             }
                         }
-                        m = m_use;
-                        l *= alpha;
-                        return ms;
-                    };
-                    // (2) 32 weights: P over their own score columns (keys 2 i, + 1 at column i), remainders at + 16
-                    auto weights = [&](const float (&x)[32], uint32_t at_col, uint64_t sl2, uint64_t nms2,
-                                       uint64_t (&rss)[4], bool split) {
-                        uint32_t hi[16];
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t bits = (uint32_t)((q & 2 ? see[1] : see[0]) >> (q & 1 ? 32 : 0));
+                            if (!__any_sync(0xffffffffu, bits != ~0u || f != 1.f)) continue;
+                            float x[32];
+                            tmem_ld32(cols + q * 32, x);
+                            tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float a0, a1;
-                            unpack_f2(fma_f2(pack_f2(x[2 * i], x[2 * i + 1]), sl2, nms2), a0, a1);
-                            const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
-                            rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
-                            const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
-                            hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
+                            for (int e = 0; e < 32; ++e) x[e] = bits & (1u << e) ? x[e] * f : -INFINITY;
+                            tmem_st32(cols + q * 32, x);
                         }
-                        tmem_st16(at_col, hi);
-                        if (split) {
+                        tmem_wait_st();
+                    }
+                    float mx = -INFINITY;
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        float x[2][32];
+                        tmem_ld32(cols + half * 64, x[0]);
+                        tmem_ld32(cols + half * 64 + 32, x[1]);
+                        tmem_wait_ld();
+                        float mxs[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], x[q][e], x[q][e + 1]);
+                        mx = fmaxf(max3f(mxs[0], mxs[1], mxs[2]), mxs[3]);
+                    }
+                    const float m_new = fmaxf(m, mx * sl);
+                    const bool move = m_new > m + 8.f;
+                    const float m_use = move ? m_new : m;
+                    const float ms = m_use == -INFINITY ? 0.f : m_use;
+                    const float alpha = ex2_approx(m - ms);
+                    // O is quiescent: P V of this side's previous chunk ran before this S
+                    if (__builtin_expect(k >= k_step && __any_sync(0xffffffffu, move && m != -INFINITY), 0)) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            float o[32];
+                            tmem_ld32(cols + C::kOCol + c * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                            tmem_st32(cols + C::kOCol + c * 32, o);
+                        }
+                    }
+                    m = m_use;
+                    l *= alpha;
+                    // P over each quarter's score columns: keys 32 q + 2 i, + 1 at column 32 q + i, remainders at + 16
+                    const uint64_t sl2 = pack_f2(sl, sl), nms2 = pack_f2(-ms, -ms);
+                    uint64_t rss[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
+                    if (__builtin_expect(j == 0 && tree_split(ctx), 0)) {
+#pragma unroll 1
+                        for (int q = 0; q < 4; ++q) {
+                            float x[32];
+                            uint32_t hi[16], rem[16];
+                            tmem_ld32(cols + q * 32, x);
+                            tmem_wait_ld();
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 float a0, a1;
                                 unpack_f2(fma_f2(pack_f2(x[2 * i], x[2 * i + 1]), sl2, nms2), a0, a1);
-                                const __nv_bfloat162 pl =
-                                    __floats2bfloat162_rn(ex2_approx(a0) - __uint_as_float(hi[i] << 16),
-                                                          ex2_approx(a1) - __uint_as_float(hi[i] & 0xffff0000u));
-                                hi[i] = *reinterpret_cast<const uint32_t *>(&pl);
+                                const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+                                rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
+                                const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
+                                hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
+                                const __nv_bfloat162 pl = __floats2bfloat162_rn(e0 - __uint_as_float(hi[i] << 16),
+                                                                                e1 - __uint_as_float(hi[i] & 0xffff0000u));
+                                rem[i] = *reinterpret_cast<const uint32_t *>(&pl);
                             }
-                            tmem_st16(at_col + 16, hi);
-                        }
-                    };
-                    uint64_t rss[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
-                    if (!masked && j != 0 && p.scale_log2 > 0.f) {
-                        float x[2][32], mx = -INFINITY;
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            tmem_ld32(cols + half * 64, x[0]);
-                            tmem_ld32(cols + half * 64 + 32, x[1]);
-                            tmem_wait_ld();
-                            float mxs[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2)
-                                    mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], x[q][e], x[q][e + 1]);
-                            mx = fmaxf(max3f(mxs[0], mxs[1], mxs[2]), mxs[3]);
-                        }
-                        const float ms = move_max(mx);
-                        const uint64_t sl2 = pack_f2(sl, sl), nms2 = pack_f2(-ms, -ms);
-#pragma unroll 1
-                        for (int half = 0; half < 2; ++half) {
-                            tmem_ld32(cols + half * 64, x[0]);
-                            tmem_ld32(cols + half * 64 + 32, x[1]);
-                            tmem_wait_ld();
-                            weights(x[0], cols + half * 64, sl2, nms2, rss, false);
-                            weights(x[1], cols + half * 64 + 32, sl2, nms2, rss, false);
+                            tmem_st16(cols + q * 32, hi);
+                            tmem_st16(cols + q * 32 + 16, rem);
                         }
                     } else {
-                        // chunks with masks, a sequence's first chunk (whose remainders the MMA thread uses), and
-                        // scales that are not positive: a quarter of the row at a time
-                        const float f = p.scale_log2 > 0.f ? 1.f : p.scale_log2 < 0.f ? -1.f : 0.f;
-                        float x[32], mx = -INFINITY, ms = 0.f;
 #pragma unroll 1
-                        for (int step = 0; step < 8; ++step) {
-                            const int q = step & 3;
-                            tmem_ld32(cols + q * 32, x);
+                        for (int half = 0; half < 2; ++half) {
+                            float x[2][32];
+                            tmem_ld32(cols + half * 64, x[0]);
+                            tmem_ld32(cols + half * 64 + 32, x[1]);
                             tmem_wait_ld();
-                            if (f != 1.f) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] *= f;
-                            }
-                            // the quarter's two blocks: which of their columns this row sees
-                            const int blk = j * C::kChunkBlocks + 2 * q;
-                            if ((blk + 2) * kBlock > ctx || blk + 2 >= nblk) {
-                                uint32_t see = 0;
-#pragma unroll 1
-                                for (int i = 0; i < 2 && blk + i < nblk; ++i) {
-                                    const int shift = blk + i == nblk - 1 ? lo : 0;  // (loaded that many rows early)
-                                    const uint32_t bits =
-                                        tree_bits16(words, word0, (blk + i) * kBlock - shift, ctx, at.n);
-                                    see |= (bits & (0xffffu << shift) & 0xffffu) << (16 * i);
+                            for (int q = 0; q < 2; ++q) {
+                                uint32_t hi[16];
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    float a0, a1;
+                                    unpack_f2(fma_f2(pack_f2(x[q][2 * i], x[q][2 * i + 1]), sl2, nms2), a0, a1);
+                                    const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
+                                    rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
+                                    const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
+                                    hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
                                 }
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) x[e] = see & (1u << e) ? x[e] : -INFINITY;
-                            }
-                            if (step < 4) {
-                                float mxs[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2)
-                                    mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], x[e], x[e + 1]);
-                                mx = fmaxf(max3f(mxs[0], mxs[1], mxs[2]), mxs[3]);
-                                if (step == 3) ms = move_max(mx);
-                            } else {
-                                weights(x, cols + q * 32, pack_f2(sl, sl), pack_f2(-ms, -ms), rss, j == 0);
+                                tmem_st16(cols + half * 64 + q * 32, hi);
                             }
                         }
                     }
@@ -730,7 +744,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 }
                 // a value that was not finite was zeroed: the rows that see its draft get NaN instead
                 bool poison = false;
-                if (row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0) {
+                if (__builtin_expect(row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0, 0)) {
                     for (int jd = 0; jd < at.n && !poison; ++jd) {
                         if (!((__ldg(words + jd / 64) >> (jd % 64)) & 1)) continue;
                         const int ps = ctx + jd;
@@ -742,52 +756,48 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     }
                 }
                 const float inv = !uncut ? 1.f : L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // (NaN stays)
+                f[0] *= inv;
+                f[1] *= inv;
                 constexpr int kMine = kPair ? D : D / 2;   // columns this side writes
                 const int d0 = kPair ? 0 : side * kMine;
                 const int unit_row = kPair ? side * C::kRows + row : row;
                 float *slot = partials + (size_t)(2 * w + (at.c0 == 0 ? 1 : 0)) * C::kUnitRows * (2 + D);
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                                     ((size_t)(at.q0 + (row_ok ? draft : 0)) * p.num_q_heads + h * g + row % g) * D + d0;
+                                     ((size_t)(at.q0 + (row_ok ? draft : 0)) * p.num_q_heads + h * g + row_head) * D + d0;
                 if (!uncut && d0 == 0 && row_ok)
                     *reinterpret_cast<float2 *>(slot + 2 * unit_row) = make_float2(M, L);
                 float *po = slot + 2 * C::kUnitRows + (size_t)unit_row * D + d0;
+                const uint64_t g0 = pack_f2(f[0], f[0]), g1 = pack_f2(f[1], f[1]), zero = pack_f2(0.f, 0.f);
+                const uint32_t col0 = (kPair ? cols : lane_cols) + C::kOCol + d0;
 #pragma unroll 1
-                for (int c = 0; c < kMine / 32; ++c) {
-                    float o[32];
-                    if constexpr (kPair) {
-                        tmem_ld32(cols + C::kOCol + c * 32, o);
-                        tmem_wait_ld();
-                    } else {
-                        float o1[32];
-                        tmem_ld32(lane_cols + C::kOCol + d0 + c * 32, o);
-                        if (both) tmem_ld32(lane_cols + C::kSideCols + C::kOCol + d0 + c * 32, o1);
-                        tmem_wait_ld();
+                for (int c = 0; c < kMine; c += 16) {
+                    float o[16], o1[16];
+                    tmem_ld16(col0 + c, o);
+                    if (!kPair && both) tmem_ld16(col0 + C::kSideCols + c, o1);
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            o[e] *= f[0];
-                            if (both) o[e] = fmaf(o1[e], f[1], o[e]);
-                        }
+                    for (int e = 0; e < 16; e += 2) {
+                        uint64_t v = fma_f2(pack_f2(o[e], o[e + 1]), g0, zero);
+                        if (!kPair && both) v = fma_f2(pack_f2(o1[e], o1[e + 1]), g1, v);
+                        unpack_f2(v, o[e], o[e + 1]);
                     }
-                    if (poison) {
+                    if (__builtin_expect(poison, 0)) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(0x7fc00000u);
+                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(0x7fc00000u);
                     }
                     if (row_ok && uncut) {
+                        uint32_t v[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[q * 8 + 2 * e] * inv,
-                                                                                o[q * 8 + 2 * e + 1] * inv);
-                                v[e] = *reinterpret_cast<const uint32_t *>(&v2);
-                            }
-                            *reinterpret_cast<uint4 *>(dst + c * 32 + q * 8) = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int e = 0; e < 8; ++e) {
+                            const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+                            v[e] = *reinterpret_cast<const uint32_t *>(&v2);
                         }
+                        reinterpret_cast<uint4 *>(dst + c)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<uint4 *>(dst + c)[1] = make_uint4(v[4], v[5], v[6], v[7]);
                     } else if (row_ok) {
 #pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            *reinterpret_cast<float4 *>(po + c * 32 + 4 * q) =
+                        for (int q = 0; q < 4; ++q)
+                            *reinterpret_cast<float4 *>(po + c + 4 * q) =
                                 make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                     }
                 }
