@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 uint32_t p_parity = 0;  // bit of a side
                 auto issue_s = [&](int side, int r) {
                     const uint32_t qt = q_s + (kPair ? side * C::kQBytes : 0);
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::kHalfRows + (kk & 3) * 32;
                         umma_bf16(tmem + side * C::kSideCols, smem_desc_sw128(qt + off, 16, 1024),
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     }
                 };
                 auto issue_pv = [&](int side, int r, bool first, bool split) {
-#pragma unroll 1
+#pragma unroll
                     for (int kk = 0; kk < C::kChunkBlocks; ++kk) {
                         const uint64_t vd =
                             smem_desc_sw128(v_s + (r % NS) * C::kStage + kk * C::kBlockBytes, kBlock * 128, 1024);
