@@ -141,6 +141,18 @@ struct TreeCut {
 // Whether a unit's first chunk gives its weights' remainders too: where a row may see fewer than 64 keys.
 __device__ __forceinline__ bool tree_split(int ctx) { return ctx < kPrefillSplitPositions; }
 
+// The line that is cut into the workers' ranges: every unit takes kTreeUnitCost positions for its start and end (Q, a
+// masked chunk, the join of the sides, the output: about as long as that many chunks), then one per chunk.
+// A worker does the chunks whose positions lie in its range; where units are not to be cut, those whose
+// start does.
+#ifndef PKV_TREE_UNIT_COST
+#define PKV_TREE_UNIT_COST 3
+#endif
+constexpr int kTreeUnitCost = PKV_TREE_UNIT_COST;
+
+// How many workers a line of T positions gets.
+__device__ __forceinline__ int tree_workers(long long T) { return (int)min((long long)gridDim.x, max(1LL, T / 4)); }
+
 // A worker's way along the line: one segment (a unit's chunks c0 .. c1 - 1) at a time.
 template <int D, bool kPair>
 struct TreeWalk {
@@ -148,34 +160,29 @@ struct TreeWalk {
     int s, unit, units;       // sequence, unit within it (kv head major, then row set), its units
     int len, q0, n, chunks, sets;
     int c0, c1;
-    long long pos, left;      // position of the segment's first chunk (or unit), positions left with it
+    long long x, end;         // position of the unit's start; end of the worker's range
 
-    __device__ __forceinline__ static long long weigh(const TreeParams &tp, int s, int per_set, bool whole, bool flag,
-                                                int &len, int &q0, int &n) {
+    // Positions of sequence s; flag: whether this call reports bad lengths and row counts.
+    __device__ __forceinline__ static long long weigh(const TreeParams &tp, int s, int per_set, bool flag, int &len,
+                                                int &q0, int &n) {
         len = seq_len(tp.d, s, flag);
         if (!tree_rows(tp.query_start, s, len, tp.max_query_len, tp.num_queries, q0, n)) {
             if (flag) raise_error(PKV_DEVERR_LENGTH);
             n = 0;
         }
         const int sets = (n + per_set - 1) / per_set;
-        return (long long)sets * tp.d.num_kv_heads * (whole ? 1 : (len + C::kKeys - 1) / C::kKeys);
+        return (long long)sets * tp.d.num_kv_heads * ((len + C::kKeys - 1) / C::kKeys + kTreeUnitCost);
     }
     __device__ __forceinline__ void enter(const TreeParams &tp, int per_set) {  // the sequence s
-        weigh(tp, s, per_set, false, false, len, q0, n);
+        weigh(tp, s, per_set, false, len, q0, n);
         sets = (n + per_set - 1) / per_set;
         units = sets * tp.d.num_kv_heads;
         chunks = (len + C::kKeys - 1) / C::kKeys;
     }
-    __device__ __forceinline__ void segment(bool whole) {
-        c1 = whole ? chunks : (int)min((long long)chunks, c0 + left);
-    }
-    // Moves to the next segment; false at the end of the range.
-    __device__ __forceinline__ bool next(const TreeParams &tp, int per_set, bool whole) {
-        const int took = whole ? 1 : c1 - c0;
-        pos += took;
-        left -= took;
-        if (left <= 0) return false;
-        c0 = 0;
+    // To the unit after this one; false past the end of the range.
+    __device__ __forceinline__ bool advance(const TreeParams &tp, int per_set) {
+        x += chunks + kTreeUnitCost;
+        if (x >= end) return false;
         if (++unit == units) {
             unit = 0;
             do {
@@ -183,8 +190,22 @@ struct TreeWalk {
                 enter(tp, per_set);
             } while (units == 0);
         }
-        segment(whole);
         return true;
+    }
+    // The worker's first segment, in the unit that holds position `start`, or the next; false: it has none.
+    __device__ __forceinline__ bool first(const TreeParams &tp, int per_set, bool whole, long long start) {
+        if (whole && x < start) {
+            if (!advance(tp, per_set)) return false;
+        }
+        c0 = (int)max(0LL, min((long long)chunks, start - x - kTreeUnitCost));
+        c1 = whole ? chunks : (int)max(0LL, min((long long)chunks, end - x - kTreeUnitCost));
+        return c1 > c0;
+    }
+    __device__ __forceinline__ bool next(const TreeParams &tp, int per_set, bool whole) {
+        if (!advance(tp, per_set)) return false;
+        c0 = 0;
+        c1 = whole ? chunks : (int)max(0LL, min((long long)chunks, end - x - kTreeUnitCost));
+        return c1 > 0;
     }
     // (one tile's worth of rows holds every tree where units are single tiles: one set)
     __device__ __forceinline__ int head() const { return kPair ? unit / sets : unit; }
@@ -350,7 +371,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         int len, q0, n;
         long long local = 0;
         for (int s = s_lo; s < s_hi; ++s)
-            local += TreeWalk<D, kPair>::weigh(tp, s, per_set, whole, blockIdx.x == 0, len, q0, n);
+            local += TreeWalk<D, kPair>::weigh(tp, s, per_set, blockIdx.x == 0, len, q0, n);
         long long incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -364,13 +385,12 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             if (w < warp) before += b.warp_sum[w];
             total += b.warp_sum[w];
         }
-        // workers: no more than the line has (cut units: pairs of) positions
-        const int W = (int)min((long long)gridDim.x, whole ? total : max(1LL, total / 2));
-        const long long start = W > 0 ? total * blockIdx.x / W : 0;
+        const int W = tree_workers(total);
+        const long long start = total * blockIdx.x / W;
         if ((int)blockIdx.x < W && start >= before && start < before + local) {
             long long at = before;
             for (int s = s_lo; s < s_hi; ++s) {
-                const long long wt = TreeWalk<D, kPair>::weigh(tp, s, per_set, whole, false, len, q0, n);
+                const long long wt = TreeWalk<D, kPair>::weigh(tp, s, per_set, false, len, q0, n);
                 if (start < at + wt) {
                     b.start_seq = s;
                     b.start_in = start - at;
@@ -387,21 +407,24 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     pdl_trigger();  // the merge may be set up; it waits for the states
     const uint32_t tmem = b.tmem_base;
     const long long T = b.total;
-    const int W = (int)min((long long)gridDim.x, whole ? T : max(1LL, T / 2)), w = blockIdx.x;
-    if (w >= W || T == 0) {
+    const int W = tree_workers(T), w = blockIdx.x;
+    TreeWalk<D, kPair> at;
+    bool work = w < W && T > 0;
+    if (work) {
+        const long long start = T * w / W;
+        at.s = b.start_seq;
+        at.enter(tp, per_set);
+        at.unit = (int)(b.start_in / (at.chunks + kTreeUnitCost));
+        at.x = start - (b.start_in - (long long)at.unit * (at.chunks + kTreeUnitCost));
+        at.end = T * (w + 1) / W;
+        work = at.first(tp, per_set, whole, start);
+    }
+    if (!work) {
         if (cuts && tid == 0) cuts[w].segments = 0;
         __syncthreads();
         if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
         return;
     }
-    TreeWalk<D, kPair> at;
-    at.pos = T * w / W;
-    at.left = T * (w + 1) / W - at.pos;
-    at.s = b.start_seq;
-    at.enter(tp, per_set);
-    at.unit = (int)(whole ? b.start_in : b.start_in / at.chunks);
-    at.c0 = whole ? 0 : (int)(b.start_in - (long long)at.unit * at.chunks);
-    at.segment(whole);
     const uint32_t q_s = smem_u32(base), k_s = smem_u32(base + C::kKOff), v_s = smem_u32(base + C::kVOff);
 
     if (warp < 4) {
@@ -418,19 +441,19 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 int seg = 0, r0 = 0;
                 uint32_t p_parity = 0;  // bit of a side
                 auto issue_s = [&](int side, int r) {
-                    const uint32_t qt = q_s + (kPair ? side * C::kQBytes : 0);
+                    const uint64_t qd = smem_desc_sw128(q_s + (kPair ? side * C::kQBytes : 0), 16, 1024);
+                    const uint64_t kd = smem_desc_sw128(k_s + (r % NS) * C::kStage, 16, 1024);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t off = (kk >> 2) * C::kHalfRows + (kk & 3) * 32;
-                        umma_bf16(tmem + side * C::kSideCols, smem_desc_sw128(qt + off, 16, 1024),
-                                  smem_desc_sw128(k_s + (r % NS) * C::kStage + off, 16, 1024), idesc_s, kk > 0);
+                        umma_bf16(tmem + side * C::kSideCols, desc_add(qd, off), desc_add(kd, off), idesc_s, kk > 0);
                     }
                 };
                 auto issue_pv = [&](int side, int r, bool first, bool split) {
+                    const uint64_t vd0 = smem_desc_sw128(v_s + (r % NS) * C::kStage, kBlock * 128, 1024);
 #pragma unroll
                     for (int kk = 0; kk < C::kChunkBlocks; ++kk) {
-                        const uint64_t vd =
-                            smem_desc_sw128(v_s + (r % NS) * C::kStage + kk * C::kBlockBytes, kBlock * 128, 1024);
+                        const uint64_t vd = desc_add(vd0, kk * C::kBlockBytes);
                         const uint32_t pa = tmem + side * C::kSideCols + (kk >> 1) * 32 + (kk & 1) * 8;
                         umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa, vd, idesc_o, !first || kk > 0);
                         if (split)
@@ -804,8 +827,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 tc_fence_before();
             }
             if (!uncut && at.c0 == 0) {  // begun here, ends further on (a worker cuts at most one unit so)
-                const long long x0 = at.pos;
-                cut.segments = (int)(((x0 + at.chunks) * W - 1) / T) - w + 1;
+                const long long last = at.x + kTreeUnitCost + at.chunks - 1;  // the unit's last chunk, and its worker
+                cut.segments = (int)(((last + 1) * W - 1) / T) - w + 1;
                 cut.q_row = at.q0 + at.first_draft(per_set);
                 cut.drafts = min(per_set, at.n - at.first_draft(per_set));
                 cut.head = h * g;
