@@ -545,21 +545,61 @@ def kv_append_layers(ks, vs, slot_mapping: torch.Tensor, k_caches, v_caches, *,
 # ---------------------------------------------------------------------------
 # the cache in 8-bit floating point
 # ---------------------------------------------------------------------------
+# The serving calls run once or more per layer and step, so their checks cost what the launch does:
+# device indexes are compared as integers, and the stream is taken without making a Stream object.
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
-    """Makes ``device`` current for a launch where it is not already."""
+    """Makes device ``index`` current for a launch on another one."""
     __slots__ = ("index", "saved")
 
-    def __init__(self, device: torch.device):
-        self.index = device.index
+    def __init__(self, index: int):
+        self.index = index
 
     def __enter__(self):
         self.saved = torch.cuda.current_device()
-        if self.saved != self.index:
-            torch.cuda.set_device(self.index)
+        torch.cuda.set_device(self.index)
 
     def __exit__(self, *exc):
-        if self.saved != self.index:
-            torch.cuda.set_device(self.saved)
+        torch.cuda.set_device(self.saved)
+
+
+def _launch(fn, what: str, index: int, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """Calls a C entry whose last argument is the stream, with device ``index`` current."""
+    st = _current_stream(index) if stream is None else stream.cuda_stream
+    if _current_device() == index:
+        rc = fn(*args, st)
+    else:
+        with _On(index):
+            rc = fn(*args, st)
+    if rc:
+        raise PagedKVError(rc, what)
+
+
+def _index(*ts: torch.Tensor) -> int:
+    """The CUDA device index that contiguous tensors share."""
+    i = ts[0].get_device()
+    if i < 0:
+        raise ValueError("tensors must be on a CUDA device")
+    for t in ts:
+        if t.get_device() != i:
+            raise ValueError("all tensors must be on the same device")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+    return i
+
+
+def _index_io(device_tensors, io_tensors) -> int:
+    """``_dev_io`` for the serving calls: ``io_tensors`` may also be pinned on the host."""
+    i = _index(*device_tensors)
+    for t in io_tensors:
+        if t.get_device() != i and t.numel() and not (t.device.type == "cpu" and t.is_pinned()):
+            raise ValueError("per-step arguments must be on the caches' device or in pinned host memory")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+    return i
 
 
 def e4m3_cache(num_blocks: int, num_kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
@@ -575,9 +615,10 @@ def e4m3_cache(num_blocks: int, num_kv_heads: int, head_dim: int, device=None) -
 def _e4m3_pool(k_cache: torch.Tensor, v_cache: torch.Tensor, head_dim: int) -> tuple:
     if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
         raise TypeError("e4m3 caches are uint8 tiles")
-    if k_cache.dim() != 3 or k_cache.shape[2] != BLOCK_SIZE * (head_dim + 1) or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 3 or shape[2] != BLOCK_SIZE * (head_dim + 1) or v_cache.shape != shape:
         raise ValueError("expected e4m3 caches [NB, Hkv, 16 * (D + 1)]")
-    return k_cache.shape[0], k_cache.shape[1]
+    return shape[0], shape[1]
 
 
 def kv_append_e4m3(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor, k_cache: torch.Tensor,
@@ -587,19 +628,19 @@ def kv_append_e4m3(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
     that brings its largest magnitude to at most 448, and written to its slot.
     No slot may be listed twice.  k, v and slot_mapping may be pinned host
     tensors (read in place)."""
-    dev = _dev_io([k_cache, v_cache], [k, v, slot_mapping])
+    dev = _index_io((k_cache, v_cache), (k, v, slot_mapping))
     dt = _dtype_code(k)
     if v.dtype != k.dtype or slot_mapping.dtype != torch.int64:
         raise TypeError("k and v of one dtype and slot_mapping int64")
-    if k.dim() != 3 or v.shape != k.shape or slot_mapping.shape != (k.shape[0],):
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or slot_mapping.shape != shape[:1]:
         raise ValueError("expected k, v [T, Hkv, D] and slot_mapping [T]")
-    T, Hkv, D = k.shape
+    T, Hkv, D = shape
     NB, Hkv2 = _e4m3_pool(k_cache, v_cache, D)
     if Hkv2 != Hkv:
         raise ValueError("k has another number of kv heads than the cache")
-    with _On(dev):
-        _check(_append_e4m3(_p(k), _p(v), _p(slot_mapping), _p(k_cache), _p(v_cache), T, Hkv, D, NB, dt,
-                            _stream_ptr(dev, stream)), "kv_append_e4m3")
+    _launch(_append_e4m3, "kv_append_e4m3", dev, stream, k.data_ptr(), v.data_ptr(), slot_mapping.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), T, Hkv, D, NB, dt)
 
 
 def dequantize_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Tensor, src_v: torch.Tensor,
@@ -610,7 +651,7 @@ def dequantize_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Ten
     [n, 2] on the device, destinations distinct; ``check`` and ``host_pairs``
     as for ``swap_blocks``).  Prefill over a quantised context reads the
     context's blocks back into a scratch cache and attends that."""
-    dev = _dev(dst_k, dst_v, src_k, src_v, src_dst_pairs)
+    dev = _index(dst_k, dst_v, src_k, src_v, src_dst_pairs)
     NBd, Hkv, D, dt = _pool_shape(dst_k)
     if dt == PKV_E4M3 or dst_v.shape != dst_k.shape or dst_v.dtype != dst_k.dtype:
         raise TypeError("the destination caches are bf16 or fp32 [NB, Hkv, 16, D], both alike")
@@ -624,9 +665,8 @@ def dequantize_blocks(dst_k: torch.Tensor, dst_v: torch.Tensor, src_k: torch.Ten
         raise ValueError("src_dst_pairs must be [n, 2]")
     if check:
         check_swap_pairs(host_pairs if host_pairs is not None else src_dst_pairs.cpu().numpy(), NBs, NBd)
-    with _On(dev):
-        _check(_dequantize(_p(dst_k), _p(dst_v), NBd, _p(src_k), _p(src_v), NBs, _p(src_dst_pairs) if n else None, n,
-                           Hkv, D, dt, _stream_ptr(dev, stream)), "dequantize_blocks")
+    _launch(_dequantize, "dequantize_blocks", dev, stream, dst_k.data_ptr(), dst_v.data_ptr(), NBd, src_k.data_ptr(),
+            src_v.data_ptr(), NBs, src_dst_pairs.data_ptr() if n else None, n, Hkv, D, dt)
 
 
 def e4m3_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
@@ -635,19 +675,19 @@ def e4m3_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, hea
     return int(_e4m3_ws(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len))
 
 
-def _workspace(need: int, workspace: Optional[torch.Tensor], dev: torch.device,
+def _workspace(need: int, workspace: Optional[torch.Tensor], index: int,
                stream: Optional[torch.cuda.Stream]) -> tuple:
-    """(tensor or None, bytes) of a call's partial states.  One made here is
-    allocated on the call's stream, whose order keeps it from other work until
-    the call is done."""
+    """(tensor or None, address, bytes) of a call's partial states.  One made
+    here is allocated on the call's stream, whose order keeps it from other
+    work until the call is done."""
     if workspace is None:
         if not need:
-            return None, 0
+            return None, None, 0
         with torch.cuda.stream(stream):           # (no-op for None: the current stream)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif _dev(workspace) != dev:
-        raise ValueError("the workspace must be on the caches' device")
-    return workspace, workspace.numel() * workspace.element_size()
+            workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous on the caches' device")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def paged_decode_attention_e4m3(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -663,36 +703,42 @@ def paged_decode_attention_e4m3(out: torch.Tensor, q: torch.Tensor, k_cache: tor
     device sync).  ``workspace``: at least ``e4m3_workspace_bytes(...)`` bytes,
     no initial value needed; calls that may overlap must not share it.  q,
     out, block_tables and context_lens may be pinned host tensors."""
-    dev = _dev_io([k_cache, v_cache], [out, q, block_tables, context_lens])
-    if q.dtype != torch.bfloat16 or out.dtype not in (torch.bfloat16, torch.float32):
+    dev = _index_io((k_cache, v_cache), (out, q, block_tables, context_lens))
+    out_dtype = out.dtype
+    if q.dtype != torch.bfloat16 or out_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("q is bf16, out bf16 or fp32")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if q.dim() != 3 or out.shape != q.shape:
+    shape, tables = q.shape, block_tables.shape
+    if len(shape) != 3 or out.shape != shape:
         raise ValueError("expected q and out [S, Hq, D]")
-    S, Hq, D = q.shape
+    S, Hq, D = shape
     NB, Hkv = _e4m3_pool(k_cache, v_cache, D)
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+    if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
         raise ValueError("expected block_tables [S, maxB] and context_lens [S]")
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
-    with _On(dev):
-        ws, ws_bytes = _workspace(_e4m3_ws(S, Hq, Hkv, D, max_context_len), workspace, dev, stream)
-        _check(_decode_e4m3(_p(out), _p(q), _p(k_cache), _p(v_cache), _p(block_tables), _p(context_lens),
-                            float(scale), Hkv, S, Hq, D, block_tables.shape[1], NB, int(max_context_len),
-                            PKV_BF16 if out.dtype == torch.bfloat16 else PKV_BF16_OUT_F32, _p(ws), ws_bytes,
-                            _stream_ptr(dev, stream)), "paged_decode_attention_e4m3")
+    max_context_len = int(max_context_len)
+    keep, ws, ws_bytes = _workspace(_e4m3_ws(S, Hq, Hkv, D, max_context_len), workspace, dev, stream)
+    _launch(_decode_e4m3, "paged_decode_attention_e4m3", dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale, Hkv, S, Hq, D, tables[1], NB,
+            max_context_len, PKV_BF16 if out_dtype == torch.bfloat16 else PKV_BF16_OUT_F32, ws, ws_bytes)
     return out
 
 
 # ---------------------------------------------------------------------------
 # from the projections to the cache
 # ---------------------------------------------------------------------------
-def _token_rows(t: torch.Tensor, what: str) -> int:
-    """The stride from one token of [T, H, D] rows to the next; heads must be contiguous."""
-    if t.dim() != 3 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]))):
-        raise ValueError(f"{what} must be [T, heads, D] with contiguous heads")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _token_rows(t: torch.Tensor, what: str) -> tuple:
+    """Shape of [T, H, D] rows and the stride from one token to the next; a token's heads must be contiguous."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{what} must be [T, heads, D]")
+    T, H, D = shape
+    st, sh, sd = t.stride()
+    if T and H and D and (sd != 1 or (H > 1 and sh != D)):
+        raise ValueError(f"{what} must have the heads of a token contiguous")
+    return shape, st if T > 1 else H * D
 
 
 def qk_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -715,49 +761,52 @@ def qk_norm_rope_append(q_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v
     first for all).  ``interleaved``: pairs are neighbours (2i, 2i + 1), not
     halves (i, i + R / 2).  slot_mapping int64 [T], negative slots skipped.
     Caches: [NB, Hkv, 16, D] of q's dtype, or e4m3 (``e4m3_cache``)."""
-    dev = _dev(k_cache, v_cache, slot_mapping, q_out)
-    for t in (q, k, v, positions, inv_freq, q_weight, k_weight, axes):
-        if t is not None and t.device != dev:
+    dev = _index(k_cache, v_cache, slot_mapping, q_out)
+    for t in (q, k, v):
+        if t.get_device() != dev:
             raise ValueError("all tensors must be on the same device")
     for t in (positions, inv_freq, q_weight, k_weight, axes):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("all tensors but q, k and v must be contiguous")
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("all tensors must be on the same device, all but q, k and v contiguous")
+    dtype = q.dtype
     dt = _dtype_code(q)
-    if not (q_out.dtype == k.dtype == v.dtype == q.dtype):
+    if not (q_out.dtype == k.dtype == v.dtype == dtype):
         raise TypeError("q, k, v and q_out must share one dtype")
-    qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
-    T, Hq, D = q.shape
-    Hkv = k.shape[1]
-    if k.shape != (T, Hkv, D) or v.shape != k.shape or q_out.shape != q.shape:
+    (q_shape, qs), (k_shape, ks), (v_shape, vs) = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    T, Hq, D = q_shape
+    Hkv = k_shape[1]
+    if k_shape != (T, Hkv, D) or v_shape != k_shape or q_out.shape != q_shape:
         raise ValueError("expected q, q_out [T, Hq, D] and k, v [T, Hkv, D]")
     NB, Hkv2, D2, cdt = _pool_shape(k_cache)
-    if (Hkv2, D2) != (Hkv, D) or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    if Hkv2 != Hkv or D2 != D or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("the caches must have k's heads and head_dim, both alike")
-    if cdt not in (dt, PKV_E4M3):
+    if cdt != dt and cdt != PKV_E4M3:
         raise TypeError("the caches have q's dtype or are e4m3")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise TypeError("slot_mapping must be int64 [T]")
     if (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight come together")
-    if q_weight is not None and not (q_weight.dtype == k_weight.dtype == q.dtype
+    if q_weight is not None and not (q_weight.dtype == k_weight.dtype == dtype
                                      and q_weight.shape == k_weight.shape == (D,)):
         raise TypeError("q_weight and k_weight are [D] of q's dtype")
     rot, num_axes = 0, 0
     if inv_freq is not None:
         if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
             raise TypeError("inv_freq must be fp32 [R / 2]")
-        if positions is None or positions.dtype != torch.int64 or positions.dim() not in (1, 2) \
-                or positions.shape[-1] != T:
+        if positions is None or positions.dtype != torch.int64:
             raise TypeError("positions must be int64 [T] or [A, T]")
-        rot, num_axes = 2 * inv_freq.shape[0], positions.shape[0] if positions.dim() == 2 else 1
+        pos_shape = positions.shape
+        if len(pos_shape) not in (1, 2) or pos_shape[-1] != T:
+            raise TypeError("positions must be int64 [T] or [A, T]")
+        rot, num_axes = 2 * inv_freq.shape[0], pos_shape[0] if len(pos_shape) == 2 else 1
         if axes is not None and (axes.dtype != torch.int32 or axes.shape != inv_freq.shape):
             raise TypeError("axes must be int32 [R / 2]")
     elif positions is not None or axes is not None:
         raise ValueError("positions and axes need inv_freq")
-    with _On(dev):
-        _check(_rope(_p(q_out), _p(q), _p(k), _p(v), qs, ks, vs, _p(q_weight), _p(k_weight), float(eps), _p(positions),
-                     num_axes, _p(inv_freq), _p(axes), rot, 1 if interleaved else 0, _p(slot_mapping), _p(k_cache),
-                     _p(v_cache), T, Hq, Hkv, D, NB, dt, cdt, _stream_ptr(dev, stream)), "qk_norm_rope_append")
+    _launch(_rope, "qk_norm_rope_append", dev, stream, q_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks,
+            vs, _p(q_weight), _p(k_weight), eps, _p(positions), num_axes, _p(inv_freq), _p(axes), rot,
+            1 if interleaved else 0, slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), T, Hq, Hkv, D, NB,
+            dt, cdt)
     return q_out
 
 
@@ -770,19 +819,19 @@ def tree_masks(parents: torch.Tensor, query_start: torch.Tensor, max_query_len: 
     64)]) from the drafts' parents: int32 [T], the index within the sequence
     of each draft's parent, which comes before it, or -1 for a child of the
     context.  Row i gets the bits of i and its ancestors."""
-    dev = _dev(parents, query_start)
+    dev = _index(parents, query_start)
     if parents.dtype != torch.int32 or query_start.dtype != torch.int32 or parents.dim() != 1 \
             or query_start.dim() != 1 or query_start.shape[0] < 1:
         raise TypeError("parents int32 [T] and query_start int32 [S + 1]")
+    max_query_len = int(max_query_len)
     T, words = parents.shape[0], (max_query_len + 63) // 64
     if out is None:
         with torch.cuda.stream(stream):
-            out = torch.zeros(T, words, dtype=torch.int64, device=dev)
-    elif out.dtype != torch.int64 or out.shape != (T, words) or _dev(out) != dev:
+            out = torch.zeros(T, words, dtype=torch.int64, device=parents.device)
+    elif out.dtype != torch.int64 or out.shape != (T, words) or _index(out) != dev:
         raise ValueError("out must be int64 [T, ceil(max_query_len / 64)]")
-    with _On(dev):
-        _check(_tree_masks(_p(out), _p(parents), _p(query_start), query_start.shape[0] - 1, T, int(max_query_len),
-                           _stream_ptr(dev, stream)), "tree_masks")
+    _launch(_tree_masks, "tree_masks", dev, stream, out.data_ptr(), parents.data_ptr(), query_start.data_ptr(),
+            query_start.shape[0] - 1, T, max_query_len)
     return out
 
 
@@ -808,32 +857,33 @@ def paged_tree_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
     and ``max_context_len`` default to the maxima of the device arrays (a
     sync).  ``workspace``: at least ``tree_workspace_bytes(...)`` bytes, no
     initial value needed; calls that may overlap must not share it."""
-    dev = _dev(out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask)
-    if q.dtype != torch.bfloat16 or not (out.dtype == k_cache.dtype == v_cache.dtype == q.dtype):
+    dev = _index(out, q, k_cache, v_cache, block_tables, context_lens, query_start, tree_mask)
+    if q.dtype != torch.bfloat16 or not (out.dtype == k_cache.dtype == v_cache.dtype == torch.bfloat16):
         raise TypeError("tree attention is bf16")
     if not (query_start.dtype == context_lens.dtype == block_tables.dtype == torch.int32):
         raise TypeError("query_start, context_lens and block_tables are int32")
-    if tree_mask.dtype != torch.int64 or tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]:
-        raise TypeError("tree_mask must be int64 [T, W]")
-    if q.dim() != 3 or out.shape != q.shape or k_cache.dim() != 4:
+    shape, cache, tables, words = q.shape, k_cache.shape, block_tables.shape, tree_mask.shape
+    if len(shape) != 3 or out.shape != shape or len(cache) != 4:
         raise ValueError("expected q, out [T, Hq, D] and caches [NB, Hkv, 16, D]")
+    T, Hq, D = shape
+    NB, Hkv, P, D2 = cache
+    if tree_mask.dtype != torch.int64 or len(words) != 2 or words[0] != T:
+        raise TypeError("tree_mask must be int64 [T, W]")
     S = context_lens.shape[0]
-    T, Hq, D = q.shape
-    NB, Hkv, P, D2 = k_cache.shape
-    if query_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if query_start.shape != (S + 1,) or len(tables) != 2 or tables[0] != S:
         raise ValueError("query_start must be [S + 1] and block_tables [S, maxB]")
-    if P != BLOCK_SIZE or D2 != D or v_cache.shape != k_cache.shape:
+    if P != BLOCK_SIZE or D2 != D or v_cache.shape != cache:
         raise ValueError("caches must be [NB, Hkv, 16, D] with q's head_dim")
     if max_query_len is None:
         max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
-    with _On(dev):
-        ws, ws_bytes = _workspace(_tree_ws(S, Hq, Hkv, D, max_query_len, max_context_len), workspace, dev, stream)
-        _check(_tree(_p(out), _p(q), _p(k_cache), _p(v_cache), _p(block_tables), _p(context_lens), _p(query_start),
-                     _p(tree_mask), tree_mask.shape[1], float(scale), Hkv, S, Hq, D,
-                     block_tables.shape[1] if S else 1, NB, T, int(max_query_len), int(max_context_len), PKV_BF16,
-                     _p(ws), ws_bytes, _stream_ptr(dev, stream)), "paged_tree_attention")
+    max_query_len, max_context_len = int(max_query_len), int(max_context_len)
+    keep, ws, ws_bytes = _workspace(_tree_ws(S, Hq, Hkv, D, max_query_len, max_context_len), workspace, dev, stream)
+    _launch(_tree, "paged_tree_attention", dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(),
+            tree_mask.data_ptr(), words[1], scale, Hkv, S, Hq, D, tables[1] if S else 1, NB, T, max_query_len,
+            max_context_len, PKV_BF16, ws, ws_bytes)
     return out
 
 
@@ -851,36 +901,39 @@ def kv_accept_layers(k_caches, v_caches, block_tables: torch.Tensor, context_len
     one per layer; accepted int32 [S, M], M at most MAX_ACCEPTED;
     num_accepted and new_lens int32 [S], new_lens another tensor than
     context_lens.  ``ptrs``: optional prebuilt (k_caches, v_caches) pointer
-    arrays from ``layer_pointers``."""
+    arrays from ``layer_pointers``; the lists' tensors past the first are then
+    taken as checked when the arrays were built."""
     if len(k_caches) != len(v_caches):
         raise ValueError("one K and one V cache per layer")
     if not k_caches:
         return new_lens
-    dev = _dev(k_caches[0], block_tables, context_lens, query_start, accepted, num_accepted, new_lens)
-    shape, dtype = k_caches[0].shape, k_caches[0].dtype
-    for t in (*k_caches, *v_caches):
-        if t.shape != shape or t.dtype != dtype or t.device != dev or not t.is_contiguous():
-            raise ValueError("every layer's caches must be contiguous, on one device and of one shape and dtype")
+    dev = _index(k_caches[0], v_caches[0], block_tables, context_lens, query_start, accepted, num_accepted, new_lens)
     NB, Hkv, D, dt = _pool_shape(k_caches[0])
     if dt == PKV_E4M3:
         raise TypeError("unsupported dtype: bf16 or fp32")
+    shape, dtype = k_caches[0].shape, k_caches[0].dtype
+    for t in (*k_caches, *v_caches) if ptrs is None else (v_caches[0],):
+        if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("every layer's caches must be contiguous, on one device and of one shape and dtype")
     for t in (block_tables, context_lens, query_start, accepted, num_accepted, new_lens):
         if t.dtype != torch.int32:
             raise TypeError("the metadata tensors are int32")
     S = context_lens.shape[0]
-    if accepted.dim() != 2 or accepted.shape[0] != S or num_accepted.shape != (S,) or new_lens.shape != (S,) \
-            or query_start.shape != (S + 1,) or block_tables.dim() != 2 or block_tables.shape[0] != S:
+    rows, tables = accepted.shape, block_tables.shape
+    if len(rows) != 2 or rows[0] != S or num_accepted.shape != (S,) or new_lens.shape != (S,) \
+            or query_start.shape != (S + 1,) or len(tables) != 2 or tables[0] != S:
         raise ValueError("expected accepted [S, M], num_accepted and new_lens [S], query_start [S + 1], "
                          "block_tables [S, maxB]")
-    st = stream if stream is not None else torch.cuda.current_stream(dev)
-    with _On(dev):
-        if ptrs is None:
-            with torch.cuda.stream(st):   # the pointer arrays are copied in on the launch stream
-                ptrs = (_ptr_array(k_caches, dev), _ptr_array(v_caches, dev))
-        _check(_accept(_p(ptrs[0]), _p(ptrs[1]), len(k_caches), _p(block_tables), _p(context_lens), _p(query_start),
-                       _p(accepted) if accepted.shape[1] else None, accepted.shape[1], _p(num_accepted),
-                       _p(new_lens), S, Hkv, D, max(1, block_tables.shape[1]), NB, dt, st.cuda_stream),
-               "kv_accept_layers")
+    if ptrs is None:
+        with torch.cuda.stream(stream):   # the pointer arrays are copied in on the launch stream
+            ptrs = (_ptr_array(k_caches, k_caches[0].device), _ptr_array(v_caches, k_caches[0].device))
+    elif ptrs[0].numel() != len(k_caches) or ptrs[1].numel() != len(k_caches) or _index(*ptrs) != dev \
+            or ptrs[0].dtype != torch.int64 or ptrs[1].dtype != torch.int64:
+        raise ValueError("ptrs: two int64 arrays of one pointer a layer, on the caches' device")
+    _launch(_accept, "kv_accept_layers", dev, stream, ptrs[0].data_ptr(), ptrs[1].data_ptr(), len(k_caches),
+            block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(),
+            accepted.data_ptr() if rows[1] else None, rows[1], num_accepted.data_ptr(), new_lens.data_ptr(), S, Hkv, D,
+            max(1, tables[1]), NB, dt)
     return new_lens
 
 

@@ -160,7 +160,7 @@ def test_binding_refuses_bad_tensors():
     assert b.e4m3_cache(2, 3, 128, device="cpu").shape == (2, 3, 16 * 129)
     with pytest.raises(ValueError):                                   # heads apart
         b._token_rows(z(4, 3, 64)[:, ::2], "q")
-    assert b._token_rows(z(4, 3, 64)[:, 1:], "q") == 192
+    assert b._token_rows(z(4, 3, 64)[:, 1:], "q") == ((4, 2, 64), 192)
 
 
 def test_the_64_bit_forms():
