@@ -186,15 +186,26 @@ int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMa
                       static_cast<const pkv::TreeCut *>(cuts), C::kUnitRows, g, tp.d.num_q_heads, tile_tokens);
 }
 
+#ifndef PKV_ROPE_WARPS
+#define PKV_ROPE_WARPS 24
+#endif
+
 template <typename T, int D>
-int launch_rope(const pkv::RopeParams &p, bool interleaved, bool e4m3, cudaStream_t st) {
+int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st) {
     auto kern = interleaved ? (e4m3 ? pkv::qk_norm_rope_append_kernel<T, D, true, true>
                                     : pkv::qk_norm_rope_append_kernel<T, D, true, false>)
                             : (e4m3 ? pkv::qk_norm_rope_append_kernel<T, D, false, true>
                                     : pkv::qk_norm_rope_append_kernel<T, D, false, false>);
-    const int lanes = (p.num_q_heads + 2 * p.num_kv_heads) * (D / 8);
-    const int threads = lanes >= 256 ? 256 : (lanes + 31) / 32 * 32;
-    kern<<<p.num_tokens, threads, 0, st>>>(p);
+    // warps to a token: as many as its rows can use while there are few tokens, one where tokens alone fill
+    // the SMs' warps
+    constexpr int rows_per_warp = 256 / D;
+    const int passes = (p.num_q_heads + 2 * p.num_kv_heads + rows_per_warp - 1) / rows_per_warp;
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    const int want = (int)((long long)sms * PKV_ROPE_WARPS / p.num_tokens);
+    p.warps_per_token = want < 1 ? 1 : want > passes ? passes : want;
+    const long long blocks = ((long long)p.num_tokens * p.warps_per_token + pkv::kRopeWarps - 1) / pkv::kRopeWarps;
+    kern<<<(unsigned)blocks, pkv::kRopeWarps * 32, 0, st>>>(p);
     return check_launch();
 }
 
@@ -308,7 +319,7 @@ int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v
     if (q_out == q && q_stride != (int64_t)num_q_heads * head_dim) return PKV_ERR_OVERLAP;
     pkv::RopeParams p{q_out, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, positions, inv_freq, axes,
                       slot_mapping, k_cache, v_cache, eps, num_axes, rot_dim, num_tokens, num_q_heads, num_kv_heads,
-                      num_blocks};
+                      num_blocks, 1};
     const bool e4 = cache_dtype == PKV_E4M3, il = interleaved != 0;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (dtype == PKV_BF16)
