@@ -471,8 +471,8 @@ int kv_append_e4m3(const void *k, const void *v, const int64_t *slot_mapping, vo
  * cache of `dst_dtype` (PKV_BF16 or PKV_F32; the values are exact in both),
  * for both caches. Pairs as for swap_blocks: destinations distinct
  * (pkv_check_swap_pairs), pairs out of range skipped and flagged
- * (PKV_DEVERR_PAIR); at most 2^30 pairs. Slots never written come out as
- * whatever their bytes stand for.
+ * (PKV_DEVERR_PAIR). Slots never written come out as whatever their bytes
+ * stand for.
  */
 int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const void *src_k_cache,
                       const void *src_v_cache, int src_num_blocks, const int64_t *src_dst_pairs, int num_pairs,

@@ -98,39 +98,39 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], uint32_t &scale_
 }
 
 // =====================================================================================
-// Append: D / 8 lanes to a (token, kv head) row of K and the same row of V, 8 elements a lane.
-// Bound by its bytes (and by the launch for a decode step's few rows).
+// Append: D / 8 lanes to a (token, kv head) row of K and the same row of V, 8 elements a lane; a CTA takes the
+// rows of one head and 16 (D = 128) or 32 tokens: tokens mostly come in slot order, and then their rows and
+// scale bytes fill whole tiles (by token with all heads, a tile's pieces came from 16 CTAs: 117 us on 16393
+// tokens of 40 heads, 100 us so). Bound by its bytes, and by the launch for a decode step's few rows.
 // =====================================================================================
+constexpr int kAppendThreads = 256;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kAppendThreads)
     kv_append_e4m3_kernel(const T *__restrict__ k, const T *__restrict__ v, const int64_t *__restrict__ slots,
                           uint8_t *__restrict__ kc, uint8_t *__restrict__ vc, int num_tokens, int num_kv_heads,
                           int num_blocks) {
     constexpr int LPR = D / 8;
     constexpr int kTile = PKV_E4M3_TILE_BYTES(D);
-    const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
-    const int l = threadIdx.x % LPR;
-    bool live = row < (long long)num_tokens * num_kv_heads;
-    const int t = live ? (int)(row / num_kv_heads) : 0;
-    const int h = (int)(row - (long long)t * num_kv_heads);
-    int64_t slot = live ? __ldg(slots + t) : -1;
-    if (slot >= (int64_t)num_blocks * kBlock) {
-        if (h == 0 && l == 0) raise_error(PKV_DEVERR_SLOT);
-        slot = -1;
-    }
-    live = slot >= 0;
+    const int l = threadIdx.x % LPR, h = blockIdx.y;
+    const long long t = (long long)blockIdx.x * (kAppendThreads / LPR) + threadIdx.x / LPR;
+    int64_t slot = t < num_tokens ? __ldg(slots + t) : -1;
     float x[2][8];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[c][i] = 0.f;
-        if (live) load8((c ? v : k) + row * D + 8 * l, x[c]);
+        if (t < num_tokens) load8((c ? v : k) + (t * num_kv_heads + h) * D + 8 * l, x[c]);
+    }
+    if (slot >= (int64_t)num_blocks * kBlock) {
+        if (h == 0 && l == 0) raise_error(PKV_DEVERR_SLOT);
+        slot = -1;
     }
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         uint32_t sb;
         const uint2 codes = quantise8<LPR>(x[c], sb);
-        if (live) {
+        if (slot >= 0) {
             uint8_t *tile = (c ? vc : kc) + ((size_t)(slot >> 4) * num_kv_heads + h) * kTile;
             *reinterpret_cast<uint2 *>(tile + (slot & 15) * D + 8 * l) = codes;
             if (l == 0) tile[kBlock * D + (slot & 15)] = (uint8_t)sb;
@@ -139,42 +139,46 @@ __global__ void __launch_bounds__(256)
 }
 
 // =====================================================================================
-// Reading back: one CTA per (pair, kv head); 2 D threads take 8 codes each of the K tile's
-// 16 D, then of the V tile's.
+// Reading back: grid (parts of a block, pairs, K / V). A block's tiles of all heads are one run in both caches; a
+// thread takes 16 codes of it (more a thread, or both caches, measured slower: 191 us for a prompt's append and
+// read-back of 13 x 1261 tokens of 40 heads, 184 us so).
 // =====================================================================================
+constexpr int kReadBackThreads = 128;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(2 * D)
+__global__ void __launch_bounds__(kReadBackThreads)
     dequantize_blocks_kernel(T *__restrict__ dk, T *__restrict__ dv, const uint8_t *__restrict__ sk,
-                             const uint8_t *__restrict__ sv, const int64_t *__restrict__ pairs, int num_kv_heads,
-                             int src_num_blocks, int dst_num_blocks) {
+                             const uint8_t *__restrict__ sv, const int64_t *__restrict__ pairs, int num_pairs,
+                             int num_kv_heads, int src_num_blocks, int dst_num_blocks) {
     constexpr int kTile = PKV_E4M3_TILE_BYTES(D);
-    const int64_t src = __ldg(pairs + 2 * (int64_t)blockIdx.x), dst = __ldg(pairs + 2 * (int64_t)blockIdx.x + 1);
-    const int h = blockIdx.y, tid = threadIdx.x;
-    if (src < 0 || src >= src_num_blocks || dst < 0 || dst >= dst_num_blocks) {
-        if (h == 0 && tid == 0) raise_error(PKV_DEVERR_PAIR);
-        return;
-    }
-    const size_t from = ((size_t)src * num_kv_heads + h) * kTile, to = ((size_t)dst * num_kv_heads + h) * kBlock * D;
-    uint2 c[2];
-    uint32_t sb[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint8_t *tile = (i ? sv : sk) + from;
-        c[i] = *reinterpret_cast<const uint2 *>(tile + 8 * tid);
-        sb[i] = tile[kBlock * D + 8 * tid / D];
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float scale = e8m0_value(sb[i]);
-        float x[8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t w = cvt_f16x2_e4m3x2((q < 2 ? c[i].x : c[i].y) >> (16 * (q & 1)));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-            x[2 * q] = f.x * scale;
-            x[2 * q + 1] = f.y * scale;
+    const int i = blockIdx.x * kReadBackThreads + threadIdx.x;  // 16-code piece of the block: D to a tile
+    const int h = i / D, u = i % D;
+    const bool live = h < num_kv_heads;
+    for (int pr = blockIdx.y; pr < num_pairs; pr += gridDim.y) {
+        const int64_t src = __ldg(pairs + 2 * (int64_t)pr), dst = __ldg(pairs + 2 * (int64_t)pr + 1);
+        if (src < 0 || src >= src_num_blocks || dst < 0 || dst >= dst_num_blocks) {
+            if (i == 0 && blockIdx.z == 0) raise_error(PKV_DEVERR_PAIR);
+            continue;
         }
-        store8((i ? dv : dk) + to + 8 * tid, x);
+        if (!live) continue;
+        const size_t from = ((size_t)src * num_kv_heads + h) * kTile;
+        const size_t to = (size_t)dst * num_kv_heads * kBlock * D + (size_t)16 * i;
+        const uint8_t *tile = (blockIdx.z ? sv : sk) + from;
+        const uint4 c = *reinterpret_cast<const uint4 *>(tile + 16 * u);
+        const float scale = e8m0_value(tile[kBlock * D + 16 * u / D]);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t f2 = cvt_f16x2_e4m3x2(w[2 * half + (q >> 1)] >> (16 * (q & 1)));
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&f2));
+                x[2 * q] = f.x * scale;
+                x[2 * q + 1] = f.y * scale;
+            }
+            store8((blockIdx.z ? dv : dk) + to + 8 * half, x);
+        }
     }
 }
 

@@ -49,13 +49,11 @@ int attention_params(pkv::DecodeParams &p, void *out, const void *q, const void 
 template <typename T>
 int launch_append_e4m3(const void *k, const void *v, const int64_t *slots, void *kc, void *vc, int num_tokens,
                        int num_kv_heads, int head_dim, int num_blocks, cudaStream_t st) {
-    const int threads = 256;
-    const long long blocks = ((long long)num_tokens * num_kv_heads * (head_dim / 8) + threads - 1) / threads;
-    if (blocks > 0x7fffffffLL) return PKV_ERR_UNSUPPORTED;
+    const int per = pkv::kAppendThreads / (head_dim / 8);  // tokens of a CTA
     auto kern = head_dim == 128 ? pkv::kv_append_e4m3_kernel<T, 128> : pkv::kv_append_e4m3_kernel<T, 64>;
-    kern<<<(unsigned)blocks, threads, 0, st>>>(static_cast<const T *>(k), static_cast<const T *>(v), slots,
-                                               static_cast<uint8_t *>(kc), static_cast<uint8_t *>(vc), num_tokens,
-                                               num_kv_heads, num_blocks);
+    kern<<<dim3((num_tokens + per - 1) / per, num_kv_heads), pkv::kAppendThreads, 0, st>>>(
+        static_cast<const T *>(k), static_cast<const T *>(v), slots, static_cast<uint8_t *>(kc),
+        static_cast<uint8_t *>(vc), num_tokens, num_kv_heads, num_blocks);
     return check_launch();
 }
 
@@ -63,9 +61,11 @@ template <typename T>
 int launch_dequantize(void *dk, void *dv, int dst_nb, const void *sk, const void *sv, int src_nb,
                       const int64_t *pairs, int num_pairs, int num_kv_heads, int head_dim, cudaStream_t st) {
     auto kern = head_dim == 128 ? pkv::dequantize_blocks_kernel<T, 128> : pkv::dequantize_blocks_kernel<T, 64>;
-    kern<<<dim3(num_pairs, num_kv_heads), 2 * head_dim, 0, st>>>(
-        static_cast<T *>(dk), static_cast<T *>(dv), static_cast<const uint8_t *>(sk),
-        static_cast<const uint8_t *>(sv), pairs, num_kv_heads, src_nb, dst_nb);
+    const dim3 grid((num_kv_heads * head_dim + pkv::kReadBackThreads - 1) / pkv::kReadBackThreads,
+                    num_pairs < 65535 ? num_pairs : 65535, 2);
+    kern<<<grid, pkv::kReadBackThreads, 0, st>>>(static_cast<T *>(dk), static_cast<T *>(dv),
+                                                 static_cast<const uint8_t *>(sk), static_cast<const uint8_t *>(sv),
+                                                 pairs, num_pairs, num_kv_heads, src_nb, dst_nb);
     return check_launch();
 }
 
@@ -236,7 +236,7 @@ int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, 
     int rc;
     if ((rc = check_pool(num_kv_heads, src_num_blocks, head_dim)) != PKV_OK) return rc;
     if ((rc = check_pool(num_kv_heads, dst_num_blocks, head_dim)) != PKV_OK) return rc;
-    if (!dtype_ok(dst_dtype) || num_pairs > (1 << 30)) return PKV_ERR_UNSUPPORTED;
+    if (!dtype_ok(dst_dtype)) return PKV_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PKV_OK;
     if (!dst_k_cache || !dst_v_cache || !src_k_cache || !src_v_cache || !src_dst_pairs) return PKV_ERR_ARG;
     if (!aligned16(dst_k_cache) || !aligned16(dst_v_cache) || !aligned16(src_k_cache) || !aligned16(src_v_cache))
@@ -407,10 +407,14 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
         (max_accepted > 0 && !accepted))
         return PKV_ERR_ARG;
     if (new_lens < context_lens + num_seqs && context_lens < new_lens + num_seqs) return PKV_ERR_OVERLAP;
+    const int row_vecs = head_dim * elem_bytes(dtype) / 16;
+    // heads of a CTA: as many as 12 KiB hold the rows of, one at least (64 accepted rows of 512 bytes take 64 KiB)
+    const int head_bytes = 2 * max_accepted * row_vecs * 16;
+    int heads = head_bytes > 0 ? 12288 / head_bytes : num_kv_heads;
+    heads = heads < 1 ? 1 : heads > num_kv_heads ? num_kv_heads : heads;
     pkv::AcceptParams p{k_caches, v_caches, block_tables, context_lens, query_start, accepted, num_accepted, new_lens,
-                        max_accepted, num_kv_heads, max_blocks_per_seq, num_blocks,
-                        head_dim * elem_bytes(dtype) / 16};
-    const size_t smem = (size_t)2 * max_accepted * p.row_vecs * 16;  // at most 64 KiB
+                        max_accepted, num_kv_heads, max_blocks_per_seq, num_blocks, row_vecs, heads};
+    const size_t smem = (size_t)heads * head_bytes;  // at most 64 KiB
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -420,8 +424,8 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
             return PKV_ERR_CUDA;
         configured_device = dev;
     }
-    pkv::kv_accept_kernel<<<dim3(num_kv_heads, num_layers, num_seqs), 128, smem, static_cast<cudaStream_t>(stream)>>>(
-        p);
+    pkv::kv_accept_kernel<<<dim3((num_kv_heads + heads - 1) / heads, num_layers, num_seqs), 128, smem,
+                            static_cast<cudaStream_t>(stream)>>>(p);
     return check_launch();
 }
 
