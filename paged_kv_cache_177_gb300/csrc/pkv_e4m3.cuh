@@ -706,73 +706,91 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (cuts && !cuts_by_unit && lane == 0) cuts[w] = cut;
 }
 
-// Merges the states of every cut unit, one CTA per (record, query head of the group): its warps share
-// the segments, eight at a time with all their loads in flight, and join through shared memory. Bound
-// by those loads' latency: many units' few segments take four warps, few units' many sixteen.
+// Merges the states of every cut unit: grid (records, head groups). A unit of a few segments is merged by a warp per
+// query head; the warps of a CTA share longer ones, head by head, and join through shared memory. Either way
+// eight segments' loads are in flight at a time; their latency is what the merge takes. Many units: four
+// warps a record. Few units, of many segments each: sixteen warps a record and head.
 template <int D, int NW, typename OutT>
 __global__ void __launch_bounds__(NW * 32)
     e4m3_merge_kernel(OutT *out, const float *__restrict__ partials, const E4m3Cut *__restrict__ cuts, int g) {
-    constexpr int PER = D / 32, NB = 8;
+    constexpr int PER = D / 32, NB = 8, kAlone = 16;  // segments one warp takes alone
     __shared__ float part[NW][2 + D];
-    const int head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     const E4m3Cut cut = cuts[blockIdx.x];
     const int nseg = cut.segments;
     if (nseg <= 0) return;
-    float M = -INFINITY, L = 0.f, acc[PER];
+    float M, L, acc[PER];
+    auto gather = [&](int head, int first, int step) {
+        M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) acc[i] = 0.f;
-    for (int k0 = warp; k0 < nseg; k0 += NW * NB) {
-        float m[NB], l[NB], o[NB][PER];
+        for (int i = 0; i < PER; ++i) acc[i] = 0.f;
+        for (int k0 = first; k0 < nseg; k0 += step * NB) {
+            float m[NB], l[NB], o[NB][PER];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const int k = k0 + b * NW;
-            m[b] = -INFINITY;
-            l[b] = 0.f;
+            for (int b = 0; b < NB; ++b) {
+                const int k = k0 + b * step;
+                m[b] = -INFINITY;
+                l[b] = 0.f;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) o[b][i] = 0.f;
-            if (k < nseg) {  // the first segment ends its worker's range, the others begin theirs
-                const float *r = partials + ((size_t)(2 * (cut.worker + k) + (k == 0 ? 1 : 0)) * g + head) * (2 + D);
-                m[b] = __ldcg(r);
-                l[b] = __ldcg(r + 1);
+                for (int i = 0; i < PER; ++i) o[b][i] = 0.f;
+                if (k < nseg) {  // the first segment ends its worker's range, the others begin theirs
+                    const float *r =
+                        partials + ((size_t)(2 * (cut.worker + k) + (k == 0 ? 1 : 0)) * g + head) * (2 + D);
+                    m[b] = __ldcg(r);
+                    l[b] = __ldcg(r + 1);
 #pragma unroll
-                for (int i = 0; i < PER; ++i) o[b][i] = __ldcg(r + 2 + lane + 32 * i);
+                    for (int i = 0; i < PER; ++i) o[b][i] = __ldcg(r + 2 + lane + 32 * i);
+                }
+            }
+            float top = M;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) top = fmaxf(top, m[b]);
+            const float al = ex2_approx(M - top);
+            M = top;
+            L *= al;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) acc[i] *= al;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float f = ex2_approx(m[b] - top);
+                L = fmaf(l[b], f, L);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) acc[i] = fmaf(o[b][i], f, acc[i]);
             }
         }
-        float top = M;
+    };
+    if (nseg <= kAlone) {
+        for (int head = blockIdx.y * NW + warp; head < g; head += gridDim.y * NW) {
+            gather(head, 0, 1);
+            const float inv = 1.f / L;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) top = fmaxf(top, m[b]);
-        const float al = ex2_approx(M - top);
-        M = top;
-        L *= al;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) acc[i] *= al;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            const float f = ex2_approx(m[b] - top);
-            L = fmaf(l[b], f, L);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) acc[i] = fmaf(o[b][i], f, acc[i]);
+            for (int i = 0; i < PER; ++i)
+                out[(size_t)(cut.row + head) * D + lane + 32 * i] = to_out<OutT>(acc[i] * inv);
         }
+        return;
     }
-    if (lane == 0) {
-        part[warp][0] = M;
-        part[warp][1] = L;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) part[warp][2 + lane + 32 * i] = acc[i];
-    __syncthreads();
-    const int used = min(NW, nseg);  // (the other warps saw no segment)
-    for (int d = threadIdx.x; d < D; d += NW * 32) {
-        float top = -INFINITY;
-        for (int v = 0; v < used; ++v) top = fmaxf(top, part[v][0]);
-        float sum = 0.f, o = 0.f;
-        for (int v = 0; v < used; ++v) {
-            const float f = ex2_approx(part[v][0] - top);
-            sum = fmaf(part[v][1], f, sum);
-            o = fmaf(part[v][2 + d], f, o);
+    for (int head = blockIdx.y; head < g; head += gridDim.y) {
+        gather(head, warp, NW);
+        if (lane == 0) {
+            part[warp][0] = M;
+            part[warp][1] = L;
         }
-        out[(size_t)(cut.row + head) * D + d] = to_out<OutT>(o / sum);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) part[warp][2 + lane + 32 * i] = acc[i];
+        __syncthreads();
+        for (int d = threadIdx.x; d < D; d += NW * 32) {  // (every warp saw a segment: nseg > kAlone >= NW)
+            float top = -INFINITY;
+            for (int v = 0; v < NW; ++v) top = fmaxf(top, part[v][0]);
+            float sum = 0.f, o = 0.f;
+            for (int v = 0; v < NW; ++v) {
+                const float f = ex2_approx(part[v][0] - top);
+                sum = fmaf(part[v][1], f, sum);
+                o = fmaf(part[v][2 + d], f, o);
+            }
+            out[(size_t)(cut.row + head) * D + d] = to_out<OutT>(o / sum);
+        }
+        __syncthreads();
     }
 }
 
