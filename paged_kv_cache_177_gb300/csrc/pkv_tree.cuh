@@ -449,15 +449,20 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                         umma_bf16(tmem + side * C::kSideCols, desc_add(qd, off), desc_add(kd, off), idesc_s, kk > 0);
                     }
                 };
+                // `first`: O starts here; `split`: the remainders' product too (compiled apart: a branch between the
+                // MMAs made the eight take 1500 cycles to issue)
                 auto issue_pv = [&](int side, int r, bool first, bool split) {
                     const uint64_t vd0 = smem_desc_sw128(v_s + (r % NS) * C::kStage, kBlock * 128, 1024);
+                    const uint32_t d = tmem + side * C::kSideCols + C::kOCol, p0 = tmem + side * C::kSideCols;
 #pragma unroll
-                    for (int kk = 0; kk < C::kChunkBlocks; ++kk) {
-                        const uint64_t vd = desc_add(vd0, kk * C::kBlockBytes);
-                        const uint32_t pa = tmem + side * C::kSideCols + (kk >> 1) * 32 + (kk & 1) * 8;
-                        umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa, vd, idesc_o, !first || kk > 0);
-                        if (split)
-                            umma_bf16_tmem_a(tmem + side * C::kSideCols + C::kOCol, pa + 16, vd, idesc_o, true);
+                    for (int kk = 0; kk < C::kChunkBlocks; ++kk)
+                        umma_bf16_tmem_a(d, p0 + (kk >> 1) * 32 + (kk & 1) * 8, desc_add(vd0, kk * C::kBlockBytes),
+                                         idesc_o, kk > 0 || !first);
+                    if (split) {
+#pragma unroll 1
+                        for (int kk = 0; kk < C::kChunkBlocks; ++kk)
+                            umma_bf16_tmem_a(d, p0 + (kk >> 1) * 32 + (kk & 1) * 8 + 16,
+                                             desc_add(vd0, kk * C::kBlockBytes), idesc_o, true);
                     }
                 };
                 auto wait_k = [&](int r) { return mbar_wait(&b.k_full[r % NS], (r / NS) & 1); };
