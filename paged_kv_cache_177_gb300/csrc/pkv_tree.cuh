@@ -128,6 +128,7 @@ struct TreeBars {
     int any_bad;                                // a draft's value was not finite
     int start_seq;                              // where this CTA's range begins: sequence ...
     long long start_in;                         // ... position within the sequence, ...
+    int start_rows[3];                          // ... its length, first row and drafts,
     long long total;                            // and the line's length
     long long warp_sum[12];
 };
@@ -175,6 +176,9 @@ struct TreeWalk {
     }
     __device__ __forceinline__ void enter(const TreeParams &tp, int per_set) {  // the sequence s
         weigh(tp, s, per_set, false, len, q0, n);
+        derive(tp, per_set);
+    }
+    __device__ __forceinline__ void derive(const TreeParams &tp, int per_set) {
         sets = (n + per_set - 1) / per_set;
         units = sets * tp.d.num_kv_heads;
         chunks = (len + C::kKeys - 1) / C::kKeys;
@@ -394,6 +398,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 if (start < at + wt) {
                     b.start_seq = s;
                     b.start_in = start - at;
+                    b.start_rows[0] = len, b.start_rows[1] = q0, b.start_rows[2] = n;
                     break;
                 }
                 at += wt;
@@ -413,7 +418,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     if (work) {
         const long long start = T * w / W;
         at.s = b.start_seq;
-        at.enter(tp, per_set);
+        at.len = b.start_rows[0], at.q0 = b.start_rows[1], at.n = b.start_rows[2];
+        at.derive(tp, per_set);
         at.unit = (int)(b.start_in / (at.chunks + kTreeUnitCost));
         at.x = start - (b.start_in - (long long)at.unit * (at.chunks + kTreeUnitCost));
         at.end = T * (w + 1) / W;
