@@ -721,7 +721,7 @@ def paged_decode_attention_e4m3(out: torch.Tensor, q: torch.Tensor, k_cache: tor
     max_context_len = int(max_context_len)
     keep, ws, ws_bytes = _workspace(_e4m3_ws(S, Hq, Hkv, D, max_context_len), workspace, dev, stream)
     _launch(_decode_e4m3, "paged_decode_attention_e4m3", dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), scale, Hkv, S, Hq, D, tables[1], NB,
+            v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale), Hkv, S, Hq, D, tables[1], NB,
             max_context_len, PKV_BF16 if out_dtype == torch.bfloat16 else PKV_BF16_OUT_F32, ws, ws_bytes)
     return out
 
@@ -882,7 +882,7 @@ def paged_tree_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
     keep, ws, ws_bytes = _workspace(_tree_ws(S, Hq, Hkv, D, max_query_len, max_context_len), workspace, dev, stream)
     _launch(_tree, "paged_tree_attention", dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), query_start.data_ptr(),
-            tree_mask.data_ptr(), words[1], scale, Hkv, S, Hq, D, tables[1] if S else 1, NB, T, max_query_len,
+            tree_mask.data_ptr(), words[1], float(scale), Hkv, S, Hq, D, tables[1] if S else 1, NB, T, max_query_len,
             max_context_len, PKV_BF16, ws, ws_bytes)
     return out
 

@@ -126,8 +126,8 @@ int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t
     if (rc != PKV_OK || whole) return rc;
     const bool few = by_unit && 8 * units <= grid * NW;
     auto merge = [&](auto kernel, int warps) {
-        return launch_pdl(kernel, dim3(by_unit ? (unsigned)units : grid * NW, few ? p.group : (p.group + 3) / 4), dim3(warps * 32), 0,
-                          st, static_cast<OutT *>(p.out), static_cast<const float *>(p.partials),
+        return launch_pdl(kernel, dim3(by_unit ? (unsigned)units : grid * NW, few ? p.group : (p.group + 3) / 4),
+                          dim3(warps * 32), 0, st, static_cast<OutT *>(p.out), static_cast<const float *>(p.partials),
                           static_cast<const pkv::E4m3Cut *>(cuts), p.group);
     };
     return few ? merge(pkv::e4m3_merge_kernel<D, 16, OutT>, 16) : merge(pkv::e4m3_merge_kernel<D, 4, OutT>, 4);

@@ -213,6 +213,33 @@ def test_decode_many_sequences():
     c.check(out)
 
 
+def test_decode_more_sequences_than_one_launch_takes():
+    """4100 sequences of one and two tokens, and a few longer ones: the batch goes in two launches."""
+    b = S.lib()
+    rng = np.random.default_rng(79)
+    lens = [int(x) for x in rng.integers(0, 3, size=4100)]
+    lens[5], lens[4095], lens[4096], lens[4099] = 40, 33, 70, 300
+    c = Case(80, lens, 1, 2, 64)
+    q, k, v, t, n = c.cuda()
+    for most in (300, 512):
+        out = torch.full_like(q, float("nan"))
+        b.paged_decode_attention_e4m3(out, q, k, v, t, n, c.scale, max_context_len=most)
+        assert b.device_error() == 0
+        c.check(out)
+
+
+def test_decode_one_long_context_among_many_short_ones():
+    """A unit of many segments beside units of one or two: both ways the merge works in one call."""
+    b = S.lib()
+    lens = [3] * 700 + [30000] + [17] * 20
+    c = Case(81, lens, 1, 4, 64)
+    q, k, v, t, n = c.cuda()
+    out = torch.full_like(q, float("nan"))
+    b.paged_decode_attention_e4m3(out, q, k, v, t, n, c.scale)
+    assert b.device_error() == 0
+    c.check(out)
+
+
 def test_decode_far_scales():
     """Rows whose scales lie far apart: the weight of a tiny value still counts in the sum, and a huge value with a
     small weight is not lost."""

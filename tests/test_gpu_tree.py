@@ -159,6 +159,39 @@ def test_many_sequences():
     case.check(out)
 
 
+@pytest.mark.parametrize("most_ctx", [150, 4096])
+def test_more_sequences_than_threads(most_ctx):
+    """900 sequences, some without drafts: short contexts as whole units, and the same batch cut."""
+    b = S.lib()
+    rng = np.random.default_rng(12)
+    ctx = [int(x) for x in rng.integers(0, 100, size=900)]
+    ns = [int(x) for x in rng.integers(0, 5, size=900)]
+    case = Case(13, ctx, ns, 2, 4, 64)
+    out = attend(b, case, max_query_len=5, max_context_len=most_ctx)
+    assert b.device_error() == 0
+    case.check(out)
+
+
+def test_one_long_context_among_many_short_ones():
+    b = S.lib()
+    ctx = [5] * 300 + [20000] + [130] * 20
+    case = Case(14, ctx, [2] * 300 + [16] + [1] * 20, 2, 8, 64)
+    out = attend(b, case)
+    assert b.device_error() == 0
+    case.check(out)
+
+
+def test_no_drafts_at_all():
+    b = S.lib()
+    case = Case(15, [10, 20], [0, 0], 2, 4, 64, extra_rows=3)
+    out = attend(b, case, max_query_len=4)
+    assert b.device_error() == 0 and bool(torch.isnan(out.float()).all())
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    q, k, v, t, n, st, m = case.cuda()
+    b.kv_accept_layers([k], [v], t, n, st, torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.zeros_like(new), new)
+    assert new.tolist() == [10, 20] and b.device_error() == 0
+
+
 def test_masks_that_leave_rows_empty_and_rows_behind_the_last():
     """No context and an empty mask: zeros. Bits past the drafts are ignored. Rows behind the last sequence stay."""
     b = S.lib()
@@ -334,6 +367,32 @@ def test_acceptance_without_sequences_layers_or_room():
     b.kv_accept_layers([c], [c.clone()], i32([[0]]), i32([3]), i32([0, 1]), torch.zeros(1, 0, dtype=torch.int32, device="cuda"),
                        i32([0]), new)
     assert new.item() == 2 and b.device_error() == 0
+
+
+def test_acceptance_replayed_from_a_graph():
+    """Each replay moves the path of that step: counts, paths and lengths change in place."""
+    b = S.lib()
+    rng = np.random.default_rng(40)
+    ns, ctx = [6, 9], [20, 3]
+    lens = [a + n for a, n in zip(ctx, ns)]
+    tables, nb = S.layout(rng, lens)
+    kc, vc = (torch.randn(nb, 2, 16, 64, device="cuda").bfloat16() for _ in range(2))
+    i32 = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    t, n, st = i32(tables), i32(lens), i32([0, 6, 15])
+    acc, count, new = i32([[0, 0, 0], [0, 0, 0]]), i32([0, 0]), i32([0, 0])
+    ptrs = b.layer_pointers([kc]), b.layer_pointers([vc])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        b.kv_accept_layers([kc], [vc], t, n, st, acc, count, new, ptrs=ptrs)
+    for paths, counts in (([[0, 2, 5], [1, 3, 8]], [3, 2]), ([[4, 1, 0], [8, 8, 8]], [2, 3])):
+        want = [S.f64(kc), S.f64(vc)]
+        new_want = accept_reference(want, tables, lens, ns, np.array(paths), counts)
+        acc.copy_(i32(paths))
+        count.copy_(i32(counts))
+        g.replay()
+        torch.cuda.synchronize()
+        assert new.tolist() == new_want and np.array_equal(S.f64(kc), want[0]) and np.array_equal(S.f64(vc), want[1])
+    assert b.device_error() == 0
 
 
 # ---- a speculative step as a server runs it ---------------------------------------------
