@@ -92,20 +92,20 @@ struct Raw8 {
 // =====================================================================================
 // A row is held by D / 8 neighbouring lanes, 8 elements each (16 bytes in bf16), so the mean square is
 // a few shuffles and the other element of a half-split pair sits in the same place of the lane rot / 16
-// further. A warp works on one token, 32 / (D / 8) rows at a time; a token's warps (one in a prompt, up to
-// eight in a decode step, where they are what keeps the SMs busy) share its rows.
+// further. A warp works on one token, 32 / (D / 8) rows at a time; a token's warps (one in a prompt, more
+// in a decode step, where they are what keeps the SMs busy) share its rows.
 //
 // Norm and rotation are one multiply-add per element: with x' the pair's other element, w' its weight,
 //   y = (x * w cos + x' * (-+) w' sin) / sqrt(mean x^2 + eps)
 // and the two products of weight and angle belong to the lane's place in the row, not to the row: they
 // are made once per token and kept in registers (the angles' fp32 sines and cosines once per warp, two
 // a lane, through shared memory). So the pass is bound by its bytes: each row is read once and
-// written once (16381 tokens of 48 heads of 128, bf16: 75 us, 5.4 TB/s).
+// written once (16381 tokens of 48 heads of 128, bf16: 72 us, 5.6 TB/s).
 // =====================================================================================
-constexpr int kRopeWarps = 8;
+constexpr int kRopeWarps = 2;  // of a CTA (nothing is shared but the launch: eight took 75 us where two take 72)
 
 template <typename T, int D, bool kInterleaved, bool kE4m3>
-__global__ void __launch_bounds__(kRopeWarps * 32, 4) qk_norm_rope_append_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeWarps * 32, 16) qk_norm_rope_append_kernel(const RopeParams p) {
     constexpr int LPR = D / 8, RPW = 32 / LPR;  // lanes to a row, rows to a warp
     constexpr int kBatch = 8 / sizeof(T);       // row passes whose loads are in flight together: 64 bytes a lane
     constexpr int kTile = PKV_E4M3_TILE_BYTES(D);
