@@ -93,7 +93,7 @@ template <int D, int NT, typename OutT>
 int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t st) {
     // Two column tiles need more than the 168 registers that twelve warps leave: eight warps. The ring is
     // 16 KB a warp. At head_dim 128 a step takes one block, whose stage is refilled at once (32K-128K
-    // contexts: 234 us, and 249 us with two blocks a step, whose stages wait for each other); at 64 a
+    // contexts, merge left out: 234 us, and 249 us with two blocks a step, whose stages wait for each other); at 64 a
     // step of two blocks hides its latencies better than it costs.
     constexpr int NW = NT == 2 ? PKV_E4M3_WARPS2 : kE4m3Warps;
     constexpr int NS = D == 128 ? PKV_E4M3_STAGES : 2 * PKV_E4M3_STAGES;
