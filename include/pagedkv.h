@@ -83,7 +83,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_BF16_OUT_F32 = 2, PKV_E4M3 = 4 /* 
 #define PKV_ERR_ARG -1          /* bad scalar argument, null pointer, shape mismatch */
 #define PKV_ERR_UNSUPPORTED -2  /* head_dim, dtype or group size not supported */
 #define PKV_ERR_INDEX -3        /* index out of range (copy pairs checked on the host) */
-#define PKV_ERR_OVERLAP -4      /* copy pairs overlap: repeated destination, or a destination that is also a source */
+#define PKV_ERR_OVERLAP -4      /* copy pairs overlap: repeated destination, or a destination that is also a source;
+                                 * or an output over an input of the same call */
 #define PKV_ERR_CUDA -5         /* a CUDA runtime/driver call or launch failed */
 #define PKV_ERR_WORKSPACE -6    /* workspace missing or smaller than pkv_decode_workspace_bytes */
 #define PKV_ERR_ALIGN -7        /* a pointer is not 16-byte aligned */
@@ -481,7 +482,8 @@ int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, 
 /*
  * paged_decode_attention over e4m3 caches: q and out bf16 (PKV_BF16), or q
  * bf16 and out fp32 (PKV_BF16_OUT_F32); every other argument, an empty
- * context, masking and errors as for paged_decode_attention. The workspace
+ * context, masking and errors as for paged_decode_attention (2^31 blocks in
+ * 4096 sequences, or over a sequence's kv heads, are PKV_ERR_UNSUPPORTED). The workspace
  * holds partial states only: it needs no initial value and may be a buffer
  * that other decode calls use (the counter header is left alone). Concurrent
  * calls must not share it.
@@ -514,7 +516,8 @@ size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
  *   q_stride, k_stride, v_stride are the elements from one token to the next
  *   (at least heads * head_dim, a multiple of 16 bytes), so the three may be
  *   slices of one projection's output. q_out: [num_tokens][num_q_heads]
- *   [head_dim], contiguous; it may be q itself and overlaps no input otherwise.
+ *   [head_dim], contiguous; it may be q itself and overlaps no input otherwise
+ *   (PKV_ERR_OVERLAP).
  * q_weight, k_weight: [head_dim] of `dtype`, both or neither (NULL: no norm).
  * positions: int64 [num_axes][num_tokens]; axes: int32 [rot_dim / 2], the axis
  *   each frequency follows (NULL: axis 0 for all), e.g. time, height and width
@@ -600,7 +603,7 @@ int tree_masks(int64_t *tree_mask, const int32_t *parents, const int32_t *query_
  *   moves nothing, raises PKV_DEVERR_LENGTH and gives new_lens[s] =
  *   context_lens[s].
  * k_caches, v_caches: pointer arrays as for copy_blocks_layers; bf16 or fp32
- *   caches. new_lens must not overlap context_lens. The destination blocks
+ *   caches. new_lens must not overlap an input (PKV_ERR_OVERLAP). The destination blocks
  *   must belong to one sequence only (copy shared ones first: the drafts'
  *   append needed that too).
  */

@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -468,7 +469,7 @@ const char *pkv_status_string(int status) {
         case PKV_ERR_ARG: return "bad argument";
         case PKV_ERR_UNSUPPORTED: return "unsupported head_dim, dtype or group size";
         case PKV_ERR_INDEX: return "index out of range";
-        case PKV_ERR_OVERLAP: return "copy pairs overlap";
+        case PKV_ERR_OVERLAP: return "copy pairs, or an output and an input, overlap";
         case PKV_ERR_CUDA: return "CUDA error";
         case PKV_ERR_WORKSPACE: return "workspace missing or too small";
         case PKV_ERR_ALIGN: return "pointer not 16-byte aligned";

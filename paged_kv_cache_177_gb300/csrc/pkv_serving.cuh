@@ -5,6 +5,12 @@
 
 namespace {
 
+// Whether two stretches of memory share a byte.
+bool overlaps(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
 // Arguments that every call over [num_blocks][num_kv_heads] tiles shares.
 int check_pool(int num_kv_heads, int num_blocks, int head_dim) {
     if (num_kv_heads <= 0 || num_blocks <= 0) return PKV_ERR_ARG;
@@ -269,6 +275,10 @@ int paged_decode_attention_e4m3(void *out, const void *q, const void *k_cache, c
                                num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len, 16)) != PKV_OK)
         return rc;
     if (dtype != PKV_BF16 && dtype != PKV_BF16_OUT_F32) return PKV_ERR_UNSUPPORTED;
+    // the kernel counts a launch's blocks, and a sequence's over its kv heads, in 32 bits
+    const int64_t long_blocks = std::min<int64_t>(((int64_t)max_context_len + 15) / 16, max_blocks_per_seq);
+    if (long_blocks * std::max(num_kv_heads, std::min(num_seqs, kE4m3MaxSeqs)) > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_ARG;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
@@ -316,7 +326,16 @@ int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v
         !aligned16(v_cache) || !aligned16(q_weight) || !aligned16(k_weight))
         return PKV_ERR_ALIGN;
     // rows may be turned in place only where each is read by the lanes that write it
-    if (q_out == q && q_stride != (int64_t)num_q_heads * head_dim) return PKV_ERR_OVERLAP;
+    const int eb = elem_bytes(dtype);
+    auto bytes = [&](int64_t stride, int heads) {  // of a tensor's rows, the gaps between them included
+        return (size_t)((num_tokens - 1) * stride + (int64_t)heads * head_dim) * eb;
+    };
+    const int64_t dense = (int64_t)num_q_heads * head_dim;
+    const size_t out_bytes = bytes(dense, num_q_heads);
+    if ((!(q_out == q && q_stride == dense) && overlaps(q_out, out_bytes, q, bytes(q_stride, num_q_heads))) ||
+        overlaps(q_out, out_bytes, k, bytes(k_stride, num_kv_heads)) ||
+        overlaps(q_out, out_bytes, v, bytes(v_stride, num_kv_heads)))
+        return PKV_ERR_OVERLAP;
     pkv::RopeParams p{q_out, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, positions, inv_freq, axes,
                       slot_mapping, k_cache, v_cache, eps, num_axes, rot_dim, num_tokens, num_q_heads, num_kv_heads,
                       num_blocks, 1};
@@ -406,7 +425,12 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
     if (!k_caches || !v_caches || !block_tables || !context_lens || !query_start || !num_accepted || !new_lens ||
         (max_accepted > 0 && !accepted))
         return PKV_ERR_ARG;
-    if (new_lens < context_lens + num_seqs && context_lens < new_lens + num_seqs) return PKV_ERR_OVERLAP;
+    const size_t lens = (size_t)num_seqs * 4;  // every CTA reads these after some have written
+    if (overlaps(new_lens, lens, context_lens, lens) || overlaps(new_lens, lens, num_accepted, lens) ||
+        overlaps(new_lens, lens, query_start, lens + 4) ||
+        (max_accepted > 0 && overlaps(new_lens, lens, accepted, lens * max_accepted)) ||
+        overlaps(new_lens, lens, block_tables, lens * max_blocks_per_seq))
+        return PKV_ERR_OVERLAP;
     const int row_vecs = head_dim * elem_bytes(dtype) / 16;
     // heads of a CTA: as many as 12 KiB hold the rows of, one at least (64 accepted rows of 512 bytes take 64 KiB)
     const int head_bytes = 2 * max_accepted * row_vecs * 16;

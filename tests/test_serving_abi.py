@@ -73,6 +73,8 @@ def test_decode_refusals(lib):
     assert f(scale=float("nan")) == ARG and f(scale=float("inf")) == ARG and f(out=None) == ARG and f(cl=None) == ARG
     assert f(d=80) == UNSUPPORTED and f(hq=8 * 17) == UNSUPPORTED and f(dt=0) == UNSUPPORTED and f(dt=4) == UNSUPPORTED
     assert f(S=65536) == UNSUPPORTED and f(nb=1 << 28) == UNSUPPORTED and f(maxb=1 << 28) == UNSUPPORTED
+    assert f(S=4096, maxb=1 << 19, maxlen=1 << 30) == UNSUPPORTED      # 2^31 blocks in a launch
+    assert f(hkv=1024, hq=1024, maxb=1 << 21, maxlen=1 << 30) == UNSUPPORTED
     assert f(q=A + 8) == ALIGN
     assert f(S=0) == OK
 
@@ -92,6 +94,20 @@ def test_rope_refusals(lib):
     assert f(qs=8 * 64 + 4) == ALIGN and f(kc=A + 8) == ALIGN and f(kw=A + 8) == ALIGN
     assert f(qo=2 * A, qs=9 * 64) == OVERLAP
     assert f(T=0) == OK
+
+
+def test_rope_refuses_outputs_over_its_inputs(lib):
+    """q_out over k, v or a part of q; T = 4 tokens of 8 heads of 64 bf16 (4 KiB), k and v 1 KiB."""
+    f = caller(lib, "qk_norm_rope_append", [
+        ("qo", VP, 16 * A), ("q", VP, 8 * A), ("k", VP, 32 * A), ("v", VP, 33 * A), ("qs", I64, 8 * 64), ("ks", I64, 2 * 64),
+        ("vs", I64, 2 * 64), ("qw", VP, None), ("kw", VP, None), ("eps", CF, 1e-6), ("pos", VP, None), ("axes_n", CI, 0),
+        ("freq", VP, None), ("axes", VP, None), ("rot", CI, 0), ("inter", CI, 0), ("slots", VP, A), ("kc", VP, A),
+        ("vc", VP, A), ("T", CI, 4), ("hq", CI, 8), ("hkv", CI, 2), ("d", CI, 64), ("nb", CI, 8), ("dt", CI, 1),
+        ("cdt", CI, 1), ("st", VP, None)])
+    assert f(k=16 * A) == OVERLAP and f(v=17 * A - 16) == OVERLAP and f(k=16 * A - 1024 + 16) == OVERLAP
+    assert f(q=16 * A + 16) == OVERLAP and f(q=15 * A + 16) == OVERLAP
+    assert f(q=13 * A, qs=4 * 8 * 64) == OVERLAP            # the last token's row reaches into q_out
+    assert f(k=14 * A, ks=4 * 8 * 64) == OVERLAP
 
 
 def test_tree_refusals(lib):
@@ -122,6 +138,9 @@ def test_acceptance_refusals(lib):
     assert f(d=96) == UNSUPPORTED and f(dt=4) == UNSUPPORTED and f(M=65) == UNSUPPORTED and f(S=65536) == UNSUPPORTED
     assert f(new=A) == OVERLAP and f(new=A + 8) == OVERLAP and f(new=A - 8) == OVERLAP
     assert f(L=0) == OK and f(S=0) == OK
+    for other in ("num", "qs", "acc", "bt"):                # every CTA reads these after some have written
+        assert f(new=2 * A, **{other: 2 * A}) == OVERLAP and f(new=2 * A + 8, **{other: 2 * A}) == OVERLAP
+    assert f(new=2 * A - 12, qs=2 * A - 24) == OVERLAP      # S + 1 entries
 
 
 def test_constants_match_the_header():
