@@ -293,7 +293,7 @@ struct WarpAttnE4m3 {
     }
 
     // NB staged blocks of one unit: one softmax update, and enough independent MMAs to keep the
-    // tensor pipe fed from three warps a scheduler. Rows of the last block from `valid` on are not
+    // tensor pipe fed from three or four warps a scheduler. Rows of the last block from `valid` on are not
     // tokens. tile: shared address of each block's K tile, its V tile one tile further.
     template <int NB>
     __device__ __forceinline__ void blocks(const uint32_t (&tile)[NB], int valid, int lane) {

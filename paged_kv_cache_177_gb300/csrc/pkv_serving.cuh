@@ -75,20 +75,28 @@ int launch_dequantize(void *dk, void *dv, int dst_nb, const void *sk, const void
     return check_launch();
 }
 
-// Decode over e4m3 tiles: the persistent kernel's shape, workers and their ring.
+// Decode over e4m3 tiles: the persistent kernel's shape, workers and their ring. A worker's step is one chain of
+// dependent instructions, so as many warps run as their registers allow without spilling: twelve at head_dim 128
+// and sixteen at 64 with up to 8 heads to a kv head, eight and twelve with more, whose accumulators are
+// twice as many. (head_dim 64, 128 contexts around 1000, 32 q / 8 kv heads: 45 us with twelve, 40 with sixteen, 43 with
+// twenty; 8 contexts of 32K-128K, 64 q / 8 kv: 123, 108, 111. 16 heads to a kv head: 38 us with eight, 35 with
+// twelve. head_dim 128, 16 heads to a kv head: 36 us with eight, 45 with ten.)
 #ifndef PKV_E4M3_WARPS
 #define PKV_E4M3_WARPS 12
-#endif
-#ifndef PKV_E4M3_STAGES
-#define PKV_E4M3_STAGES 4
 #endif
 #ifndef PKV_E4M3_WARPS2
 #define PKV_E4M3_WARPS2 8
 #endif
-#ifndef PKV_E4M3_NB2
-#define PKV_E4M3_NB2 1
+#ifndef PKV_E4M3_WARPS64
+#define PKV_E4M3_WARPS64 16
 #endif
-constexpr int kE4m3Warps = PKV_E4M3_WARPS;
+#ifndef PKV_E4M3_WARPS64_2
+#define PKV_E4M3_WARPS64_2 12
+#endif
+constexpr int e4m3_warps(int head_dim, int group) {
+    return head_dim == 128 ? (group <= 8 ? PKV_E4M3_WARPS : PKV_E4M3_WARPS2)
+                           : (group <= 8 ? PKV_E4M3_WARPS64 : PKV_E4M3_WARPS64_2);
+}
 constexpr int kE4m3MaxSeqs = 4096;  // sequences of one launch: their block counts lie in shared memory
 
 // Contexts this short are not cut: a worker takes whole (sequence, kv head) units and writes
@@ -97,13 +105,11 @@ bool e4m3_whole_units(int max_context_len) { return max_context_len <= 256; }
 
 template <int D, int NT, typename OutT>
 int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t st) {
-    // Two column tiles need more than the 168 registers that twelve warps leave: eight warps. The ring is
-    // 16 KB a warp. At head_dim 128 a step takes one block, whose stage is refilled at once (32K-128K
-    // contexts, merge left out: 234 us, and 249 us with two blocks a step, whose stages wait for each other); at 64 a
-    // step of two blocks hides its latencies better than it costs.
-    constexpr int NW = NT == 2 ? PKV_E4M3_WARPS2 : kE4m3Warps;
-    constexpr int NS = D == 128 ? PKV_E4M3_STAGES : 2 * PKV_E4M3_STAGES;
-    constexpr int NB = D == 128 ? (NT == 2 ? PKV_E4M3_NB2 : 1) : 2;
+    // Four stages of a block's K and V: 16 KB a warp at head_dim 128, where a step takes one block, whose stage is
+    // refilled at once (32K-128K contexts, merge left out: 234 us, and 249 us with two blocks a step, whose stages
+    // wait for each other); at 64 a step of two blocks hides its latencies better than it costs (128
+    // contexts around 1000: 40 us, 44 with one).
+    constexpr int NW = e4m3_warps(D, 8 * NT), NS = 4, NB = D == 128 ? 1 : 2;
     using C = pkv::E4m3Cfg<D, NS, NW>;
     static_assert(C::smem_bytes(kE4m3MaxSeqs) + 64 <= kSmemLimit, "shared memory");
     auto kern = pkv::decode_e4m3_kernel<D, NT, NB, NS, NW, OutT>;
@@ -259,7 +265,7 @@ size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
     if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_q_heads % num_kv_heads != 0 ||
         e4m3_whole_units(max_context_len))
         return 0;
-    const size_t workers = (size_t)kPersistMaxCtas * kE4m3Warps;
+    const size_t workers = (size_t)kPersistMaxCtas * e4m3_warps(head_dim, num_q_heads / num_kv_heads);
     return kCounterBytes + workers * sizeof(pkv::E4m3Cut) +
            workers * 2 * (num_q_heads / num_kv_heads) * (2 + (size_t)head_dim) * sizeof(float);
 }
