@@ -446,7 +446,8 @@ int paged_decode_attention_static_workspace(void *out, const void *q, const void
  * The scale is a power of two, so x * 2^-e is exact and codes are defined bit
  * for bit. Rows past 448 * 2^50 saturate; NaN and infinities become NaN and
  * do not take part in the maximum. Against a 16-bit cache this reads and
- * writes (head_dim + 1) / (2 head_dim) of the bytes.
+ * writes (head_dim + 1) / (2 head_dim) of the bytes. A zeroed cache holds rows
+ * of zeros.
  *
  * kv_append_e4m3 quantises and writes new tokens, dequantize_blocks reads
  * blocks back into a bf16 or fp32 cache (for paged_prefill_attention over a
@@ -483,8 +484,9 @@ int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, 
  * paged_decode_attention over e4m3 caches: q and out bf16 (PKV_BF16), or q
  * bf16 and out fp32 (PKV_BF16_OUT_F32); every other argument, an empty
  * context, masking and errors as for paged_decode_attention (2^31 blocks in
- * 4096 sequences, or over a sequence's kv heads, are PKV_ERR_UNSUPPORTED). The workspace
- * holds partial states only: it needs no initial value and may be a buffer
+ * 4096 sequences, or over a sequence's kv heads, are PKV_ERR_UNSUPPORTED). A
+ * value row's scale byte below 63, which no quantiser writes, counts as 63.
+ * The workspace holds partial states only: it needs no initial value and may be a buffer
  * that other decode calls use (the counter header is left alone). Concurrent
  * calls must not share it.
  */

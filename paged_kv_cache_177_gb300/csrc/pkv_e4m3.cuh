@@ -23,6 +23,9 @@ struct IntConst {  // a compile-time number passed to a generic lambda
 
 constexpr int kE4m3ExpLo = -50, kE4m3ExpHi = 50;  // range of a row's scale exponent
 
+// The least scale byte that the decode kernel takes a value row to have, 2^-64.
+constexpr uint32_t kE4m3LeastByte = 127 - 64;
+
 // Two floats to two e4m3 codes (a in the low byte), nearest even, saturating; NaN to NaN.
 __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {
     uint16_t r;
@@ -204,7 +207,8 @@ __global__ void __launch_bounds__(kReadBackThreads)
 // K's enters the score, V's the exponent of the weight. The reference m' follows y, not x, so the
 // weights -- the one thing rounded here, to f16's 11 bits -- are largest where their values
 // matter most, whatever the rows' scales. A row's exponent lies in [-50, 50], so sum 2^(x - m')
-// neither overflows nor loses a term that counts.
+// neither overflows nor loses a term that counts. Scale bytes below a quantiser's, 0 above all, which
+// every row that nothing was written to has, would undo that: they count as kE4m3LeastByte.
 //
 // A tile, codes and scales, is one contiguous run of 16 (D + 1) bytes and comes by one untiled bulk
 // copy: the runs start at any multiple of 16 bytes, and a tiled copy of 128-byte rows from such a
@@ -306,6 +310,8 @@ struct WarpAttnE4m3 {
             const uint32_t at = tile[b] + kBlock * D + gq;
             kb[b][0] = ld_shared_u8(at), kb[b][1] = ld_shared_u8(at + 8);
             vb[b][0] = ld_shared_u8(at + kTile), vb[b][1] = ld_shared_u8(at + kTile + 8);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) vb[b][i] = max(kE4m3LeastByte, vb[b][i]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
