@@ -23,7 +23,9 @@ struct IntConst {  // a compile-time number passed to a generic lambda
 
 constexpr int kE4m3ExpLo = -50, kE4m3ExpHi = 50;  // range of a row's scale exponent
 
-// The least scale byte that the decode kernel takes a value row to have, 2^-64.
+// The least scale byte that the decode kernel takes a value row to have, 2^-64, and the one of a row without
+// magnitude: lower than any quantiser's, so that the row does not lift the weights' reference, and high enough that
+// its weight adds to the sum all that counts.
 constexpr uint32_t kE4m3LeastByte = 127 - 64;
 
 // Two floats to two e4m3 codes (a in the low byte), nearest even, saturating; NaN to NaN.
@@ -207,8 +209,13 @@ __global__ void __launch_bounds__(kReadBackThreads)
 // K's enters the score, V's the exponent of the weight. The reference m' follows y, not x, so the
 // weights -- the one thing rounded here, to f16's 11 bits -- are largest where their values
 // matter most, whatever the rows' scales. A row's exponent lies in [-50, 50], so sum 2^(x - m')
-// neither overflows nor loses a term that counts. Scale bytes below a quantiser's, 0 above all, which
-// every row that nothing was written to has, would undo that: they count as kE4m3LeastByte.
+// neither overflows nor loses a term that counts.
+//
+// That holds as long as a row's scale says how large its values are. It does not for a row of zeros, whose
+// scale byte is 127 as if it held values up to 448: it would lift m' over the rows that make up O. Blocks
+// with a byte 127 in them are looked at (a warp's vote), and rows without magnitude (zeros, or NaN and
+// zeros) take kE4m3LeastByte. So do bytes below it, which no quantiser writes: 0, the scale of every row
+// that nothing was written to, is one.
 //
 // A tile, codes and scales, is one contiguous run of 16 (D + 1) bytes and comes by one untiled bulk
 // copy: the runs start at any multiple of 16 bytes, and a tiled copy of 128-byte rows from such a
@@ -296,6 +303,20 @@ struct WarpAttnE4m3 {
         }
     }
 
+    // Bits 2 r and 2 r + 1: whether row r of the tile at this shared address has a code that is neither zero nor NaN in its
+    // first and second half.
+    static __device__ __noinline__ uint32_t rows_with_magnitude(uint32_t tile, int lane) {
+        uint32_t some = 0;
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+            uint32_t c[4];
+            ld_shared_v4(tile + lane * (D / 2) + 16 * i, c);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) some |= ((c[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x7e7e7e7eu;
+        }
+        return __ballot_sync(0xffffffffu, some != 0);
+    }
+
     // NB staged blocks of one unit: one softmax update, and enough independent MMAs to keep the
     // tensor pipe fed from three or four warps a scheduler. Rows of the last block from `valid` on are not
     // tokens. tile: shared address of each block's K tile, its V tile one tile further.
@@ -305,13 +326,17 @@ struct WarpAttnE4m3 {
         const int gq = lane >> 2, t4 = lane & 3;
         float sc[NB][NT][4], sb[NB][NT][4];
         uint32_t kb[NB][2], vb[NB][2];  // scale bytes of this lane's two token rows gq and gq + 8
+        bool look = false;              // a value row may be without magnitude
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             const uint32_t at = tile[b] + kBlock * D + gq;
             kb[b][0] = ld_shared_u8(at), kb[b][1] = ld_shared_u8(at + 8);
             vb[b][0] = ld_shared_u8(at + kTile), vb[b][1] = ld_shared_u8(at + kTile + 8);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) vb[b][i] = max(kE4m3LeastByte, vb[b][i]);
+            for (int i = 0; i < 2; ++i) {
+                look |= vb[b][i] == 127u;
+                vb[b][i] = max(kE4m3LeastByte, vb[b][i]);
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -334,6 +359,15 @@ struct WarpAttnE4m3 {
                         mma_f16_16816(w & 1 ? sb[b][nt] : sc[b][nt], a, qf[4 * j + w][nt][0], qf[4 * j + w][nt][1]);
                 }
             }
+        if (__builtin_expect(__any_sync(0xffffffffu, look), 0)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const uint32_t rows = rows_with_magnitude(tile[b] + kTile, lane);
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (!(rows >> (2 * (gq + 8 * i)) & 3u)) vb[b][i] = kE4m3LeastByte;
+            }
+        }
         float kv[NB][2], ev[NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -621,11 +655,8 @@ __global__ void __launch_bounds__(NW * 32, 1)
                 bulk_load_hint(stage + C::kTile, static_cast<const uint8_t *>(p.v_cache) + from, C::kTile, &full[st],
                                policy);
             }
-        } else {  // a bad block id reads as zeros (scale 1)
-            for (int i = lane; i < C::kStage / 16; i += 32) {
-                const uint32_t w = i % (C::kTile / 16) == D ? 0x7f7f7f7fu : 0u;
-                reinterpret_cast<uint4 *>(stage)[i] = make_uint4(w, w, w, w);
-            }
+        } else {  // a bad block id reads as zeros, as a block that nothing was written to
+            for (int i = lane; i < C::kStage / 16; i += 32) reinterpret_cast<uint4 *>(stage)[i] = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();  // these writes before the copy that refills the stage
             __syncwarp();
             if (lane == 0) {

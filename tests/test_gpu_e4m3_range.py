@@ -1,6 +1,8 @@
 """Decode over e4m3 tiles where the rows' scale bytes say little about their
-size: blocks that nothing was written to. Against a 64-bit softmax over the
-values that the tiles stand for, under the bound of the ordinary decode tests."""
+size: blocks that nothing was written to, value rows of zeros, blocks with a
+bad id. Each against a 64-bit softmax over the values that the tiles stand
+for, under the bound of the ordinary decode tests."""
+import numpy as np
 import pytest
 import torch
 
@@ -47,4 +49,76 @@ def test_fresh_blocks_that_fill_whole_segments(hkv, g, d):
     freshen(c, 0, [*range(0, 90), *range(200, 300), *range(1240, 1250)])
     out = decode(b, c)
     assert b.device_error() == 0
+    c.check(out)
+
+
+def set_value_row(c, s, token, x):
+    """Value row `token` of sequence s, every kv head: the row x [D]."""
+    codes, scales = S.e4m3_rows(x)
+    d = len(x)
+    blk, off = c.tables[s, token // 16], token % 16
+    c.v[blk, :, off * d:(off + 1) * d] = torch.from_numpy(codes)
+    c.v[blk, :, 16 * d + off] = int(scales)
+
+
+def lift_key(c, s, token, by):
+    """Key row `token` of sequence s gives its one query head a score of about `by` (natural log)."""
+    q = S.f64(c.q[s, 0])
+    codes, scales = S.e4m3_rows(q * (by / c.scale / (q @ q)))
+    d = len(q)
+    blk, off = c.tables[s, token // 16], token % 16
+    c.k[blk, :, off * d:(off + 1) * d] = torch.from_numpy(codes)
+    c.k[blk, :, 16 * d + off] = int(scales)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -7, 2.0 ** -10, 2.0 ** -17, 2.0 ** -40, 1.0, 300.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_value_row_of_zeros_under_the_highest_score(d, size):
+    """It takes most of the weight, adds nothing, and costs the other rows' weights no precision."""
+    b = S.lib()
+    c = Case(70 + d, [64, 33, 500], 1, 1, d)
+    rng = np.random.default_rng(d)
+    for s, n in enumerate(c.lens):
+        for t in range(n):
+            set_value_row(c, s, t, rng.standard_normal(d) * size)
+        for t in (5, n - 1):
+            set_value_row(c, s, t, np.zeros(d))
+            lift_key(c, s, t, 6.0)
+    for most in (max(c.lens), 512):
+        out = decode(b, c, max_context_len=most)
+        assert b.device_error() == 0
+        c.check(out)
+
+
+def test_a_row_of_nan_only_costs_the_others_nothing():
+    """A value row whose elements are NaN and zeros: NaN where it is NaN, the others' average elsewhere."""
+    b = S.lib()
+    d = 128
+    c = Case(75, [40], 1, 1, d)
+    rng = np.random.default_rng(1)
+    for t in range(40):
+        set_value_row(c, 0, t, rng.standard_normal(d) * 2.0 ** -17)
+    set_value_row(c, 0, 7, np.where(np.arange(d) == 3, np.nan, 0.0))
+    lift_key(c, 0, 7, 6.0)
+    out = S.f64(decode(b, c))
+    assert b.device_error() == 0 and np.isnan(out[0, 0, 3])
+    set_value_row(c, 0, 7, np.zeros(d))
+    want, spread = c.want()
+    rest = np.arange(d) != 3
+    S.close(out[..., rest], want[..., rest], (2.0 ** -24 * np.abs(want) + (2.0 ** -11 + 2.0 ** -12) * spread)[..., rest])
+
+
+@pytest.mark.parametrize("size", [2.0 ** -17, 1.0])
+def test_a_bad_block_costs_small_values_nothing(size):
+    """A block id out of range reads as zeros, beside values of any size."""
+    b = S.lib()
+    d = 128
+    c = Case(80, [90], 1, 1, d)
+    rng = np.random.default_rng(2)
+    for t in range(90):
+        set_value_row(c, 0, t, rng.standard_normal(d) * size)
+    c.q *= 4                                     # scores of size 4 around the zeros' 0
+    c.tables[0, 2] = c.nb + 5
+    out = decode(b, c)
+    assert b.device_error() == b.DEVERR_BLOCK_ID
     c.check(out)
