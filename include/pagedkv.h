@@ -484,8 +484,11 @@ int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, 
  * paged_decode_attention over e4m3 caches: q and out bf16 (PKV_BF16), or q
  * bf16 and out fp32 (PKV_BF16_OUT_F32); every other argument, an empty
  * context, masking and errors as for paged_decode_attention (2^31 blocks in
- * 4096 sequences, or over a sequence's kv heads, are PKV_ERR_UNSUPPORTED). A
- * value row's scale byte below 63, which no quantiser writes, counts as 63.
+ * 4096 sequences, or over a sequence's kv heads, are PKV_ERR_UNSUPPORTED).
+ * Weights are rounded to 11 bits (f16) for the tensor cores, and what lies
+ * below 2^-36 of a row's largest weighted value is lost; their sum is fp32. A
+ * value row's scale byte outside [63, 253], which no quantiser writes, counts
+ * as the nearest of these, and a block id out of range reads as zeros.
  * The workspace holds partial states only: it needs no initial value and may be a buffer
  * that other decode calls use (the counter header is left alone). Concurrent
  * calls must not share it.

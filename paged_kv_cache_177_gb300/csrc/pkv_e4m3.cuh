@@ -23,9 +23,11 @@ struct IntConst {  // a compile-time number passed to a generic lambda
 
 constexpr int kE4m3ExpLo = -50, kE4m3ExpHi = 50;  // range of a row's scale exponent
 
-// The least scale byte that the decode kernel takes a value row to have, 2^-64, and the one of a row without
-// magnitude: lower than any quantiser's, so that the row does not lift the weights' reference, and high enough that
-// its weight adds to the sum all that counts.
+// The decode kernel's reference for the weights' exponents: set kE4m3RefSet under the largest, moved when one passes
+// kE4m3RefUp. kE4m3LeastByte stands for 2^-64, what a value row without magnitude takes there: lower than any
+// quantiser's, so that the row does not lift the reference, and high enough that its weight, which fp32 holds
+// down to 2^-126, adds to the sum all that counts beside the 2^-39 that a row of the largest scale adds at least.
+constexpr float kE4m3RefSet = 11.f, kE4m3RefUp = 15.5f;
 constexpr uint32_t kE4m3LeastByte = 127 - 64;
 
 // Two floats to two e4m3 codes (a in the low byte), nearest even, saturating; NaN to NaN.
@@ -202,17 +204,20 @@ __global__ void __launch_bounds__(kReadBackThreads)
 //
 // The step over staged (K, V) blocks, for the group's query heads as the MMA's N:
 //   x_t = (scale log2 e) 2^(ek_t + eq) <codes K_t, q'>      q = q' 2^eq, q' in f16
-//   y_t = x_t + ev_t;   m' = max(m, max_t y_t);   w_t = 2^(y_t - m')
-//   l = l 2^(m - m') + sum_t 2^(x_t - m');   O = O 2^(m - m') + sum_t w_t codes V_t
+//   y_t = x_t + ev_t;   w_t = 2^(y_t - m)
+//   l = sum_t w_t 2^-ev_t;   O = sum_t w_t codes V_t
 // and the output is O / l. Codes widen to f16 without loss, and products with a query of 8
 // significant bits are exact in the tensor cores' fp32 sums, so no code is multiplied by its scale:
-// K's enters the score, V's the exponent of the weight. The reference m' follows y, not x, so the
+// K's enters the score, V's the exponent of the weight. The reference m follows y, not x, so the
 // weights -- the one thing rounded here, to f16's 11 bits -- are largest where their values
-// matter most, whatever the rows' scales. A row's exponent lies in [-50, 50], so sum 2^(x - m')
-// neither overflows nor loses a term that counts.
+// matter most, whatever the rows' scales. m lies 2^11 to 2^15.5 (kE4m3RefUp, below f16's largest value)
+// under the largest y so far: a weight has its 11 bits down to 2^-25 of the largest, and what is lost
+// below f16's last step is at most 2^-36 of the largest w |codes| a row. O and l take the same w, each
+// before or after its rounding, so a score so large that fp32 cannot add ev to it moves both alike.
+// A row's exponent lies in [-50, 50], so l neither overflows nor loses a term that counts.
 //
 // That holds as long as a row's scale says how large its values are. It does not for a row of zeros, whose
-// scale byte is 127 as if it held values up to 448: it would lift m' over the rows that make up O. Blocks
+// scale byte is 127 as if it held values up to 448: it would lift m over the rows that make up O. Blocks
 // with a byte 127 in them are looked at (a warp's vote), and rows without magnitude (zeros, or NaN and
 // zeros) take kE4m3LeastByte. So do bytes below it, which no quantiser writes: 0, the scale of every row
 // that nothing was written to, is one.
@@ -335,7 +340,8 @@ struct WarpAttnE4m3 {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 look |= vb[b][i] == 127u;
-                vb[b][i] = max(kE4m3LeastByte, vb[b][i]);
+                // (253: the largest exponent whose 2^-ev is a normal number; past the end a row's byte may be any)
+                vb[b][i] = max(kE4m3LeastByte, min(253u, vb[b][i]));
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -368,57 +374,60 @@ struct WarpAttnE4m3 {
                     if (!(rows >> (2 * (gq + 8 * i)) & 3u)) vb[b][i] = kE4m3LeastByte;
             }
         }
-        float kv[NB][2], ev[NB][2];
+        float kv[NB][2], ev[NB][2], un[NB][2];  // 2^ek, ev, 2^-ev
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 kv[b][i] = e8m0_value(kb[b][i]);
                 ev[b][i] = __uint_as_float(0x4b000000u | vb[b][i]) - (8388608.f + 127.f);  // byte - 127
+                un[b][i] = e8m0_value(254u - vb[b][i]);
             }
         uint32_t p0[NB][NT], p1[NB][NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float x[NB][4], y[NB][4], mx0 = -INFINITY, mx1 = -INFINITY;
+            float y[NB][4], mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[b][e] = (sc[b][nt][e] + sb[b][nt][e]) * kv[b][e >> 1] * qs[nt][e & 1];
-                    y[b][e] = x[b][e] + ev[b][e >> 1];
-                    if (b == NB - 1 && gq + 8 * (e >> 1) >= valid) x[b][e] = y[b][e] = -INFINITY;
+                    y[b][e] = fmaf((sc[b][nt][e] + sb[b][nt][e]) * kv[b][e >> 1], qs[nt][e & 1], ev[b][e >> 1]);
+                    if (b == NB - 1 && gq + 8 * (e >> 1) >= valid) y[b][e] = -INFINITY;
                 }
-                mx0 = max3f(mx0, y[b][0], y[b][2]);
-                mx1 = max3f(mx1, y[b][1], y[b][3]);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) mx[c] = max3f(mx[c], y[b][c], y[b][c + 2]);
             }
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
-            }
-            // finite: a block holds a token
-            const bool up = mx0 > m[nt][0] || mx1 > m[nt][1];
-            if (__any_sync(0xffffffffu, up)) {  // (most blocks move no maximum)
-                const float mn0 = fmaxf(m[nt][0], mx0), mn1 = fmaxf(m[nt][1], mx1);
-                const float al0 = ex2_approx(m[nt][0] - mn0), al1 = ex2_approx(m[nt][1] - mn1);
-                m[nt][0] = mn0;
-                m[nt][1] = mn1;
-                l[nt][0] *= al0;
-                l[nt][1] *= al1;
+            for (int o = 4; o < 32; o <<= 1)
 #pragma unroll
-                for (int i = 0; i < kMmas; ++i) {
-                    acc[i][nt][0] *= al0;
-                    acc[i][nt][1] *= al1;
-                    acc[i][nt][2] *= al0;
-                    acc[i][nt][3] *= al1;
+                for (int c = 0; c < 2; ++c) mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], o));
+            if (__any_sync(0xffffffffu, mx[0] - m[nt][0] > kE4m3RefUp || mx[1] - m[nt][1] > kE4m3RefUp)) {  // (seldom)
+                float al[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float to = m[nt][c];
+                    if (mx[c] - to > kE4m3RefUp) {
+                        to = mx[c] - kE4m3RefSet;
+                        if (mx[c] - to > kE4m3RefUp) to = mx[c];  // the step of fp32 is larger than that
+                    }
+                    al[c] = to == m[nt][c] ? 1.f : ex2_approx(m[nt][c] - to);
+                    m[nt][c] = to;
+                    l[nt][c] *= al[c];
                 }
+#pragma unroll
+                for (int i = 0; i < kMmas; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][nt][e] *= al[e & 1];
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                l[nt][0] += ex2_approx(x[b][0] - m[nt][0]) + ex2_approx(x[b][2] - m[nt][0]);
-                l[nt][1] += ex2_approx(x[b][1] - m[nt][1]) + ex2_approx(x[b][3] - m[nt][1]);
-                const __half2 w0 = __floats2half2_rn(ex2_approx(y[b][0] - m[nt][0]), ex2_approx(y[b][1] - m[nt][1]));
-                const __half2 w1 = __floats2half2_rn(ex2_approx(y[b][2] - m[nt][0]), ex2_approx(y[b][3] - m[nt][1]));
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    w[e] = ex2_approx(y[b][e] - m[nt][e & 1]);
+                    l[nt][e & 1] = fmaf(w[e], un[b][e >> 1], l[nt][e & 1]);
+                }
+                const __half2 w0 = __floats2half2_rn(w[0], w[1]), w1 = __floats2half2_rn(w[2], w[3]);
                 p0[b][nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&w0));
                 p1[b][nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&w1));
             }

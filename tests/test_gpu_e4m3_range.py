@@ -1,7 +1,8 @@
 """Decode over e4m3 tiles where the rows' scale bytes say little about their
-size: blocks that nothing was written to, value rows of zeros, blocks with a
-bad id. Each against a 64-bit softmax over the values that the tiles stand
-for, under the bound of the ordinary decode tests."""
+size, or lie far apart: blocks that nothing was written to, value rows of
+zeros, blocks with a bad id, one value row far larger than the others. Each
+against a 64-bit softmax over the values that the tiles stand for, under the
+bound of the ordinary decode tests."""
 import numpy as np
 import pytest
 import torch
@@ -122,3 +123,41 @@ def test_a_bad_block_costs_small_values_nothing(size):
     out = decode(b, c)
     assert b.device_error() == b.DEVERR_BLOCK_ID
     c.check(out)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("far", [12, 20, 24])
+def test_one_value_row_far_above_the_others(far, d):
+    """An outlier in one element of one row must not round away the other elements' averages: a weight keeps f16's
+    11 bits down to 2^-25 of the largest weighted value."""
+    b = S.lib()
+    c = Case(90 + far, [300, 20], 1, 4, d)
+    rng = np.random.default_rng(far)
+    for s, n in enumerate(c.lens):
+        for t in range(n):
+            set_value_row(c, s, t, np.sign(rng.standard_normal(d)) * rng.uniform(1.0, 1.75, d))
+        set_value_row(c, s, n // 2, np.where(np.arange(d) == 9, 2.0 ** far, 0.0))
+    c.q *= 0.03                                  # weights within a factor of two of one another
+    out = decode(b, c)
+    assert b.device_error() == 0
+    c.check(out)
+
+
+def test_scores_as_large_as_fp32_resolves():
+    """Scores around 2^27, where the step of fp32 exceeds the reference's distance from the maximum: one row takes all
+    the weight."""
+    b = S.lib()
+    d = 64
+    c = Case(95, [100, 40], 1, 1, d)
+    c.q[:] = 2.0 ** 45
+    c.k[:, :, :16 * d] = 0x30                    # 0.5
+    c.k[:, :, 16 * d:] = 127 - 20
+    c.scale = 2.0 ** -3
+    for s, top in ((0, 33), (1, 17)):
+        c.k[c.tables[s, top // 16], 0, 16 * d + top % 16] = 127 - 19
+    out = S.f64(decode(b, c))
+    assert b.device_error() == 0
+    values = S.tile_values(c.v)
+    for s, top in ((0, 33), (1, 17)):
+        want = values[c.tables[s, top // 16], 0, top % 16]
+        assert np.all(np.abs(out[s, 0] - want) <= (2.0 ** -11 + 2.0 ** -24) * np.abs(want))
