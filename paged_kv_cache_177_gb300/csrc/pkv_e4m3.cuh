@@ -753,9 +753,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
     if (!waited) {
         // a copy never landed: the output is unspecified; wait (bounded) for the others before leaving
         if (lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
+        const int left = cnt - i;
         for (; i < issued; ++i) mbar_wait(&full[i & (NS - 1)], (i / NS) & 1);
+        // nothing of the units begun here and from here on is merged (their records hold what the workspace held)
         cut.segments = 0;
-        if (cuts_by_unit && seg_j0 == 0 && lane == 0) cuts[c.s * Hkv + c.h] = cut;
+        if (cuts_by_unit && lane == 0) {
+            if (seg_j0 == 0) cuts[c.s * Hkv + c.h] = cut;
+            units_begun_later(c, left, prefix, Hkv, [&](int s, int h) { cuts[s * Hkv + h] = cut; });
+        }
     }
     if (cuts && !cuts_by_unit && lane == 0) cuts[w] = cut;
 }
