@@ -96,7 +96,8 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_BF16_OUT_F32 = 2, PKV_E4M3 = 4 /* 
 #define PKV_DEVERR_BLOCK_ID 0x1u    /* a block-table entry outside [0, num_blocks): its K/V read as zeros */
 #define PKV_DEVERR_SLOT 0x2u        /* a slot >= num_blocks*16 in kv_append: that token was skipped */
 #define PKV_DEVERR_PAIR 0x4u        /* a copy pair outside [0, num_blocks): that pair was skipped */
-#define PKV_DEVERR_TIMEOUT 0x8u     /* a bounded wait inside a kernel ran out: output unspecified */
+#define PKV_DEVERR_TIMEOUT 0x8u     /* a bounded wait inside a kernel ran out, or its shared memory did not start where
+                                     * its layout needs: output unspecified */
 #define PKV_DEVERR_LENGTH 0x10u     /* context_len < 0, > max_blocks_per_seq*16 or > max_context_len: clamped */
 #define PKV_DEVERR_POINTER 0x20u    /* a pointer in a per-layer pointer array is null or not 16-byte aligned: skipped */
 #define PKV_DEVERR_INDEX 0x40u      /* a position axis, a draft's parent or an accepted draft out of range: see the call */

@@ -334,7 +334,10 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     const bool whole = cuts == nullptr;
     uint8_t *const base = tree_smem;
     if (smem_u32(base) & 1023u) {  // the swizzle's atoms would not be where the descriptors say
-        if (tid == 0) raise_error(PKV_DEVERR_TIMEOUT);
+        if (tid == 0) {
+            raise_error(PKV_DEVERR_TIMEOUT);
+            if (cuts) cuts[blockIdx.x].segments = 0;  // (the merge reads every CTA's record)
+        }
         return;
     }
     TreeBars &b = *reinterpret_cast<TreeBars *>(base + C::kBarOff);
