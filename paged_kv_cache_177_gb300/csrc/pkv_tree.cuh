@@ -86,9 +86,11 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 //
 // A row's max moves only when it grows by more than 8 (log2), as in the prefill kernels, and as there the
 // weights of rows that may see few keys enter P V as two bf16 values, the rounded weight and its
-// remainder (16 significant bits): such a row would carry the full rounding of its weights. Over more
-// keys the roundings average out, to about the output's own (the remainder on every chunk took 360 us on
-// eight contexts of 32K-128K with 16 drafts and 8 heads to a kv head, 335 us without).
+// remainder (16 significant bits): such a row would carry the full rounding of its weights. These are the
+// sequences of less than kPrefillSplitPositions context tokens, in all of their chunks: a draft far down a
+// wide tree may see itself and a few others only. Over more keys the roundings average out, to about the
+// output's own (the remainder everywhere took 360 us on eight contexts of 32K-128K with 16 drafts and 8 heads
+// to a kv head, 335 us without).
 //
 // Every wait is bounded; on a timeout the role records PKV_DEVERR_TIMEOUT, waits (bounded) for its own
 // copies and MMAs in flight, and the CTA frees its tensor memory and exits.
@@ -139,7 +141,7 @@ struct TreeCut {
     int segments, q_row, drafts, head;  // first query row of the unit, its drafts, first query head
 };
 
-// Whether a unit's first chunk gives its weights' remainders too: where a row may see fewer than 64 keys.
+// Whether a unit's weights come with their remainders: where a row may see fewer than 64 keys.
 __device__ __forceinline__ bool tree_split(int ctx) { return ctx < kPrefillSplitPositions; }
 
 // The line that is cut into the workers' ranges: every unit takes kTreeUnitCost positions for its start and end (Q, a
@@ -502,7 +504,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             ok = values_ready(k) && (k + 1 == nc || wait_k(r0 + k + 1));
                             for (int t = 0; t < tiles && ok; ++t) {
                                 if (!(ok = weights_ready(t))) break;
-                                issue_pv(t, r0 + k, k == 0, at.c0 + k == 0 && tree_split(at.len - at.n));
+                                issue_pv(t, r0 + k, k == 0, tree_split(at.len - at.n));
                                 if (k + 1 < nc) {
                                     issue_s(t, r0 + k + 1);
                                     umma_commit(&b.s_full[t]);
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             if (k + 1 < nc && !(ok = scores(k + 1))) break;
                             if (k < 0) continue;
                             if (!(ok = values_ready(k) && weights_ready(k & 1))) break;
-                            issue_pv(k & 1, r0 + k, k < 2, at.c0 + k == 0 && tree_split(at.len - at.n));
+                            issue_pv(k & 1, r0 + k, k < 2, tree_split(at.len - at.n));
                             umma_commit(&b.v_empty[(r0 + k) % NS]);
                             if (k + 2 >= nc) umma_commit(&b.o_done[k & 1]);
                         }
@@ -690,7 +692,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     uint64_t rss[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
-                    if (__builtin_expect(j == 0 && tree_split(ctx), 0)) {
+                    if (__builtin_expect(tree_split(ctx), 0)) {
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
                             float x[32];
