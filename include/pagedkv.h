@@ -556,7 +556,8 @@ int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v
  * context_lens[s] - 1. Row i of s attends every position before the drafts,
  * and draft j exactly if bit j % 64 of tree_mask[row][j / 64] is set (its own
  * bit included; bits from n_s on are ignored). A row that sees nothing yields
- * zeros.
+ * zeros; a value that is not finite shows in its element of the rows that see
+ * it, and in no other.
  *
  * q, out, query_start, context_lens, num_queries, max_query_len and
  *   max_context_len as for paged_prefill_attention (a bad n_s leaves the

@@ -77,7 +77,9 @@ __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const i
 //                        ring waits for the other's stages)
 //   warp 1, one thread   MMA: S = Q K^T (128 x 128, fp32 in tensor memory); O += P V with P from tensor memory
 //   warp 3               the values of the drafts: a row that does not see a draft must not meet its
-//                        NaN (0 * NaN is NaN), so non-finite elements there are zeroed before P V
+//                        NaN or infinity (0 times either is NaN), so such elements are zeroed before P V and
+//                        added at the end, by element, to the rows that see them. (Of the context too where
+//                        weights come with remainders, which are zero or negative as well.)
 //   warps 4-7, 8-11      softmax, one thread per row (tensor-memory lane): two sides
 // The two sides are two row tiles of a unit (kPair, units of more than 128 rows), or take turns at the
 // chunks of one tile, each with its own S, O and running max; their two states are joined, half
@@ -127,7 +129,7 @@ struct TreeBars {
     uint64_t x_full[2], x_done[2];             // per side: its state is in shared memory; it has read both O
     uint64_t drain;
     uint32_t tmem_base;
-    int any_bad;                                // a draft's value was not finite
+    int any_bad;                                // a value was not finite, and was zeroed
     int start_seq;                              // where this CTA's range begins: sequence ...
     long long start_in;                         // ... position within the sequence, ...
     int start_rows[3];                          // ... its length, first row and drafts,
@@ -143,6 +145,10 @@ struct TreeCut {
 
 // Whether a unit's weights come with their remainders: where a row may see fewer than 64 keys.
 __device__ __forceinline__ bool tree_split(int ctx) { return ctx < kPrefillSplitPositions; }
+
+// The first position whose values are cleaned before P V: the drafts', which not every row sees, and all that a
+// remainder meets.
+__device__ __forceinline__ int tree_first_clean(int ctx) { return tree_split(ctx) ? 0 : ctx; }
 
 // The line that is cut into the workers' ranges: every unit takes kTreeUnitCost positions for its start and end (Q, a
 // masked chunk, the join of the sides, the output: about as long as that many chunks), then one per chunk.
@@ -320,6 +326,28 @@ __device__ __forceinline__ void tree_produce(const CUtensorMap &tm, const CUtens
     // no copy may land after the CTA is gone
     for (int i = max(0, r - NS); i < r; ++i) mbar_wait(&full[i % NS], (i / NS) & 1);
     if (seg > 0) mbar_wait(&b.q_full, (seg - 1) & 1);
+}
+
+// Adds what the values cleaner zeroed at positions [from, to) of a sequence to the columns d0 .. d0 + cols - 1 of a
+// row that this thread has written (dst, or the state po): an element that meets one is not finite whatever its weight.
+// Not in line: it is seldom called, and the epilogue has no registers for it.
+__device__ __noinline__ void tree_add_zeroed(const DecodeParams &p, const int64_t *words, int s, int h, int from, int to,
+                                             int ctx, int head_dim, int d0, int cols, __nv_bfloat16 *dst, float *po) {
+#pragma unroll 1
+    for (int ps = from; ps < to; ++ps) {
+        if (ps >= ctx && !((__ldg(words + (ps - ctx) / 64) >> ((ps - ctx) % 64)) & 1)) continue;
+        const int pb = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + ps / kBlock);
+        if (pb < 0 || pb >= p.num_blocks) continue;
+        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                 (((size_t)pb * p.num_kv_heads + h) * kBlock + ps % kBlock) * head_dim + d0;
+#pragma unroll 1
+        for (int c = 0; c < cols; ++c) {
+            const float x = __bfloat162float(v[c]);
+            if (fabsf(x) < INFINITY) continue;
+            if (dst) dst[c] = __float2bfloat16_rn(__bfloat162float(dst[c]) + x);
+            else po[c] += x;
+        }
+    }
 }
 
 template <int D, bool kPair>
@@ -555,7 +583,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             bool ok = true;
             int r0 = 0;
             do {
-                const int nc = at.c1 - at.c0, ctx = at.len - at.n;
+                const int nc = at.c1 - at.c0, first = tree_first_clean(at.len - at.n);
                 const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
                 // every chunk is waited for and passed on, drafts or not, so that no stage's phase runs
                 // away from this role's count
@@ -563,20 +591,25 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     const int st = (r0 + k) % NS;
                     if (!(ok = warp_wait(&b.v_full[st], ((r0 + k) / NS) & 1))) break;
                     const int blk0 = (at.c0 + k) * C::kChunkBlocks;
-                    const int b_lo = max(0, ctx / kBlock - blk0), b_hi = min(C::kChunkBlocks, nblk - blk0);
+                    const int b_lo = max(0, first / kBlock - blk0), b_hi = min(C::kChunkBlocks, nblk - blk0);
                     uint8_t *vst = base + C::kVOff + st * C::kStage;
                     for (int i = b_lo * (C::kBlockBytes / 16) + lane; i < b_hi * (C::kBlockBytes / 16); i += 32) {
                         const uint4 v = reinterpret_cast<const uint4 *>(vst)[i];
                         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t keep[4];
                         bool bad = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            bad |= (x[e] & 0x7f80u) == 0x7f80u || (x[e] & 0x7f800000u) == 0x7f800000u;
+                        for (int e = 0; e < 4; ++e) {
+                            keep[e] = ((x[e] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                      ((x[e] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                            bad |= keep[e] != ~0u;
+                        }
                         if (bad) {
                             const int blk = blk0 + i / (C::kBlockBytes / 16), row = (i >> 3) & 15;
                             const int pos = blk * kBlock + row - (blk == nblk - 1 ? lo : 0);
-                            if (pos >= ctx) {
-                                reinterpret_cast<uint4 *>(vst)[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (pos >= first) {
+                                reinterpret_cast<uint4 *>(vst)[i] =
+                                    make_uint4(x[0] & keep[0], x[1] & keep[1], x[2] & keep[2], x[3] & keep[3]);
                                 *reinterpret_cast<volatile int *>(&b.any_bad) = 1;
                             }
                         }
@@ -780,19 +813,6 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     f[side ^ 1] = ex2_approx(other.x - ms);
                     L = l * f[side] + other.y * f[side ^ 1];
                 }
-                // a value that was not finite was zeroed: the rows that see its draft get NaN instead
-                bool poison = false;
-                if (__builtin_expect(row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0, 0)) {
-                    for (int jd = 0; jd < at.n && !poison; ++jd) {
-                        if (!((__ldg(words + jd / 64) >> (jd % 64)) & 1)) continue;
-                        const int ps = ctx + jd;
-                        const int pb = __ldg(p.block_tables + (size_t)at.s * p.max_blocks_per_seq + ps / kBlock);
-                        if (pb < 0 || pb >= p.num_blocks) continue;
-                        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
-                                                 (((size_t)pb * p.num_kv_heads + h) * kBlock + ps % kBlock) * D;
-                        for (int d = 0; d < D; ++d) poison |= !(fabsf(__bfloat162float(v[d])) < INFINITY);
-                    }
-                }
                 const float inv = !uncut ? 1.f : L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // (NaN stays)
                 f[0] *= inv;
                 f[1] *= inv;
@@ -819,10 +839,6 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                         if (!kPair && both) v = fma_f2(pack_f2(o1[e], o1[e + 1]), g1, v);
                         unpack_f2(v, o[e], o[e + 1]);
                     }
-                    if (__builtin_expect(poison, 0)) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(0x7fc00000u);
-                    }
                     if (row_ok && uncut) {
                         uint32_t v[8];
 #pragma unroll
@@ -839,6 +855,9 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                                 make_float4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
                     }
                 }
+                if (__builtin_expect(row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0, 0))
+                    tree_add_zeroed(p, words, at.s, h, max(tree_first_clean(ctx), at.c0 * C::kKeys),
+                                    min(at.len, at.c1 * C::kKeys), ctx, D, d0, kMine, uncut ? dst : nullptr, po);
                 tc_fence_before();
             }
             if (!uncut && at.c0 == 0) {  // begun here, ends further on (a worker cuts at most one unit so)
