@@ -516,7 +516,8 @@ size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
  *     by the angle positions[axes[i]][t] * inv_freq[i]:
  *     a' = a cos - b sin,  b' = b cos + a sin;  elements past rot_dim stay.
  * Everything is computed in fp32 (the angle is reduced in 64 bits, so far
- * positions keep their accuracy) and rounded once, on the way out.
+ * positions keep their accuracy, at frequencies up to 2^40) and rounded once, on
+ * the way out.
  *
  * q, k, v: [num_tokens][heads][head_dim] of `dtype` (PKV_BF16 or PKV_F32);
  *   q_stride, k_stride, v_stride are the elements from one token to the next

@@ -23,8 +23,8 @@ struct RopeParams {
     int warps_per_token;
 };
 
-// f / (2 pi), its whole turns off, as a 64-bit fraction of a turn, rounded down; |f| < 16. With f = m 2^(e - 150),
-// m its 24-bit significand, the product of m and 2^96 / (2 pi) only needs a shift.
+// f / (2 pi), its whole turns off, as a 64-bit fraction of a turn, rounded down; |f| < 16 (every model's). With
+// f = m 2^(e - 150), m its 24-bit significand, the product of m and 2^96 / (2 pi) only needs a shift.
 __device__ __forceinline__ uint64_t turn_fraction(float f) {
     constexpr unsigned __int128 kTurn = (unsigned __int128)0x28be60dbu << 64 | 0x9391054a7f09d5f4ull;  // 2^96 / (2 pi)
     const uint32_t bits = __float_as_uint(f) & 0x7fffffffu;
@@ -35,18 +35,25 @@ __device__ __forceinline__ uint64_t turn_fraction(float f) {
     return f < 0.f ? 0ull - r : r;
 }
 
-// cos and sin of pos * f. The product is taken in turns and in integers, where whole turns fall off by themselves: the
-// fraction is off by at most |pos| 2^-64 of a turn, and rounded to fp32 once, so that a small angle has all its bits. (In fp64 it is as good, but this GPU's fp64 rate then
-// bounds a decode step's few tokens: 6.4 us against 4.8 us for 64 of 48 heads.)
+// The same for any other finite f: f times 1 / (2 pi) as a sum of two doubles, the first product's rounding kept by a
+// multiply-add, whole turns off each part; to the nearest, good to 2^-64 of a turn up to |f| = 2^40.
+__device__ __noinline__ uint64_t turn_fraction_far(float f) {
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi)
+    const double p = (double)f * kHi, hi = p - rint(p);
+    double lo = fma((double)f, kHi, -p);
+    lo = (lo - rint(lo)) + (double)f * kLo;
+    lo -= rint(lo);
+    return ((uint64_t)__double2ll_rn(hi * 0x1p63) << 1) + (uint64_t)__double2ll_rn(lo * 0x1p64);
+}
+
+// cos and sin of pos * f, NaN for a frequency that is not finite. The product is taken in turns and in integers, where
+// whole turns fall off by themselves: the fraction is off by at most |pos| 2^-64 of a turn, and rounded to fp32
+// once, so that a small angle has all its bits. (In fp64 it is as good, but this GPU's fp64 rate then bounds a
+// decode step's few tokens: 6.4 us against 4.8 us for 64 of 48 heads.)
 __device__ __forceinline__ float2 rotation(int64_t pos, float f) {
-    float turns;
-    if (fabsf(f) < 16.f) {
-        turns = (float)(int64_t)((uint64_t)pos * turn_fraction(f)) * 0x1p-64f;
-    } else {  // no model's frequencies
-        constexpr double kTurnsPerRadian = 0.15915494309189533577;
-        double d = (double)pos * (double)f * kTurnsPerRadian;
-        turns = (float)(d - rint(d));
-    }
+    const uint64_t per_position = fabsf(f) < 16.f ? turn_fraction(f) : turn_fraction_far(f);
+    float turns = (float)(int64_t)((uint64_t)pos * per_position) * 0x1p-64f;
+    if (!(fabsf(f) < INFINITY)) turns = __uint_as_float(0x7fc00000u);
     float2 cs;
     sincospif(2.f * turns, &cs.y, &cs.x);
     return cs;

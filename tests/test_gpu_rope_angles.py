@@ -1,12 +1,16 @@
 """The angles of the pass from the projections to the cache: small ones to the
-accuracy of fp32, at positions of either sign."""
+accuracy of fp32, far and negative positions, and frequencies on both sides of
+16, where their reduction changes form."""
 import numpy as np
 import pytest
 import torch
 
 from tests import serving_helpers as S
+from tests.test_gpu_rope import ARITH
 
 pytestmark = pytest.mark.gpu
+
+PI_200 = 0x3243f6a8885a308d313198a2e03707344a4093822299f31d008   # pi 2^200, rounded down
 
 
 def turned(q, pos, freq, interleaved=False, **kw):
@@ -44,3 +48,37 @@ def test_small_angles_keep_their_bits(interleaved):
     turn = 2 * np.longdouble("3.14159265358979323846264338327950288")
     reduced = np.abs(angle - np.rint(angle / turn) * turn).astype(np.float64)
     assert np.all(np.abs(got - want) <= 2.0 ** -24 * (reduced + 5 * np.abs(want)) + fraction)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("lo,hi", [(-2 ** 31, 2 ** 31), (-5000, 0), (0, 40)])
+def test_high_frequencies_and_negative_positions(lo, hi, interleaved):
+    """Frequencies on both sides of 16, up to 2^39, at positions of either sign. Exact angles from whole numbers: a
+    frequency is m 2^-e, so position times frequency is a fraction of integers, reduced by 2 pi to 200 bits."""
+    rng = np.random.default_rng(hi % 1000)
+    d, half, t = 128, 64, 9
+    pos = rng.integers(lo, hi, size=t)
+    freq = (2.0 ** rng.uniform(-3, 39, size=half)).astype(np.float32) * np.where(np.arange(half) % 5 == 4, -1, 1).astype(np.float32)
+    freq[:4] = [16.0, 15.999999, 17.5, 1024.0]
+    x = rng.standard_normal((t, 2, d)).astype(np.float32)
+    got = turned(torch.from_numpy(x).cuda(), pos, freq, interleaved)
+    angle = np.zeros((t, half))
+    for i in range(t):
+        for j in range(half):
+            num, den = float(freq[j]).as_integer_ratio()
+            angle[i, j] = (int(pos[i]) * num << 200) // den % (2 * PI_200) / 2 ** 200
+    i = np.arange(half)
+    ia, ib = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+    a, b = x[..., ia].astype(np.float64), x[..., ib].astype(np.float64)
+    c, s = np.cos(angle)[:, None], np.sin(angle)[:, None]
+    want, mag = np.zeros(x.shape), np.zeros(x.shape)
+    want[..., ia], want[..., ib] = a * c - b * s, b * c + a * s
+    mag[..., ia] = mag[..., ib] = np.abs(a) + np.abs(b)
+    S.close(got, want, 2.0 ** -24 * np.abs(want) + ARITH * mag)
+
+
+def test_frequencies_that_are_not_finite_give_nan():
+    x = torch.ones(2, 1, 64, device="cuda")
+    freq = np.array([np.inf, np.nan, -np.inf] + [1.0] * 29)
+    got = turned(x, [0, 5], freq)
+    assert np.isnan(got[:, 0, [0, 1, 2, 32, 33, 34]]).all() and np.isfinite(got[:, 0, 3:32]).all()
