@@ -523,8 +523,8 @@ size_t pkv_e4m3_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
  *   q_stride, k_stride, v_stride are the elements from one token to the next
  *   (at least heads * head_dim, a multiple of 16 bytes), so the three may be
  *   slices of one projection's output. q_out: [num_tokens][num_q_heads]
- *   [head_dim], contiguous; it may be q itself and overlaps no input otherwise
- *   (PKV_ERR_OVERLAP).
+ *   [head_dim], contiguous; it may be q itself and overlaps no input otherwise,
+ *   nor the caches (PKV_ERR_OVERLAP).
  * q_weight, k_weight: [head_dim] of `dtype`, both or neither (NULL: no norm).
  * positions: int64 [num_axes][num_tokens]; axes: int32 [rot_dim / 2], the axis
  *   each frequency follows (NULL: axis 0 for all), e.g. time, height and width

@@ -331,7 +331,8 @@ int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v
     if (!aligned16(q_out) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(k_cache) ||
         !aligned16(v_cache) || !aligned16(q_weight) || !aligned16(k_weight))
         return PKV_ERR_ALIGN;
-    // rows may be turned in place only where each is read by the lanes that write it
+    // rows may be turned in place only where each is read by the lanes that write it; what every token reads, and
+    // what other warps write, may not lie under q_out at all
     const int eb = elem_bytes(dtype);
     auto bytes = [&](int64_t stride, int heads) {  // of a tensor's rows, the gaps between them included
         return (size_t)((num_tokens - 1) * stride + (int64_t)heads * head_dim) * eb;
@@ -342,6 +343,16 @@ int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v
         overlaps(q_out, out_bytes, k, bytes(k_stride, num_kv_heads)) ||
         overlaps(q_out, out_bytes, v, bytes(v_stride, num_kv_heads)))
         return PKV_ERR_OVERLAP;
+    const size_t weight_bytes = q_weight ? (size_t)head_dim * eb : 0, freq_bytes = (size_t)rot_dim / 2 * 4;
+    const size_t cache_bytes = (size_t)num_blocks * num_kv_heads * tile_vecs(cache_dtype, head_dim) * 16;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } others[] = {{q_weight, weight_bytes}, {k_weight, weight_bytes}, {slot_mapping, (size_t)num_tokens * 8},
+                  {positions, freq_bytes > 0 ? (size_t)num_axes * num_tokens * 8 : 0}, {inv_freq, freq_bytes},
+                  {axes, axes ? freq_bytes : 0}, {k_cache, cache_bytes}, {v_cache, cache_bytes}};
+    for (const auto &o : others)
+        if (o.bytes > 0 && overlaps(q_out, out_bytes, o.p, o.bytes)) return PKV_ERR_OVERLAP;
     pkv::RopeParams p{q_out, q, k, v, q_stride, k_stride, v_stride, q_weight, k_weight, positions, inv_freq, axes,
                       slot_mapping, k_cache, v_cache, eps, num_axes, rot_dim, num_tokens, num_q_heads, num_kv_heads,
                       num_blocks, 1};
