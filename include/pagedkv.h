@@ -475,7 +475,8 @@ int kv_append_e4m3(const void *k, const void *v, const int64_t *slot_mapping, vo
  * for both caches. Pairs as for swap_blocks: destinations distinct
  * (pkv_check_swap_pairs), pairs out of range skipped and flagged
  * (PKV_DEVERR_PAIR). Slots never written come out as whatever their bytes
- * stand for.
+ * stand for. The destination caches overlap neither each other nor the source
+ * ones (PKV_ERR_OVERLAP).
  */
 int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, const void *src_k_cache,
                       const void *src_v_cache, int src_num_blocks, const int64_t *src_dst_pairs, int num_pairs,
@@ -589,7 +590,8 @@ size_t pkv_tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
  * the context; a draft comes after its parent. Row i gets the bits of i and
  * all its ancestors, in ceil(max_query_len / 64) words. A parent that is not
  * in [-1, i) ends the walk and raises PKV_DEVERR_INDEX. Bad n_s (as above)
- * raise PKV_DEVERR_LENGTH and leave the sequence's rows unwritten.
+ * raise PKV_DEVERR_LENGTH and leave the sequence's rows unwritten. tree_mask
+ * overlaps no input (PKV_ERR_OVERLAP).
  */
 int tree_masks(int64_t *tree_mask, const int32_t *parents, const int32_t *query_start, int num_seqs, int num_queries,
                int max_query_len, void *stream);

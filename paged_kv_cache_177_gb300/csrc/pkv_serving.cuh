@@ -253,6 +253,12 @@ int dequantize_blocks(void *dst_k_cache, void *dst_v_cache, int dst_num_blocks, 
     if (!dst_k_cache || !dst_v_cache || !src_k_cache || !src_v_cache || !src_dst_pairs) return PKV_ERR_ARG;
     if (!aligned16(dst_k_cache) || !aligned16(dst_v_cache) || !aligned16(src_k_cache) || !aligned16(src_v_cache))
         return PKV_ERR_ALIGN;
+    const size_t dst_bytes = (size_t)dst_num_blocks * num_kv_heads * tile_vecs(dst_dtype, head_dim) * 16;
+    const size_t src_bytes = (size_t)src_num_blocks * num_kv_heads * tile_vecs(PKV_E4M3, head_dim) * 16;
+    for (const void *dst : {dst_k_cache, dst_v_cache})
+        for (const void *src : {src_k_cache, src_v_cache})
+            if (overlaps(dst, dst_bytes, src, src_bytes)) return PKV_ERR_OVERLAP;
+    if (overlaps(dst_k_cache, dst_bytes, dst_v_cache, dst_bytes)) return PKV_ERR_OVERLAP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dst_dtype == PKV_BF16
                ? launch_dequantize<__nv_bfloat16>(dst_k_cache, dst_v_cache, dst_num_blocks, src_k_cache, src_v_cache,
@@ -371,6 +377,10 @@ int tree_masks(int64_t *tree_mask, const int32_t *parents, const int32_t *query_
     if (num_seqs == 0 || num_queries == 0 || max_query_len == 0) return PKV_OK;
     if (!tree_mask || !parents || !query_start) return PKV_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(tree_mask) & 7) != 0) return PKV_ERR_ALIGN;
+    const size_t mask_bytes = (size_t)num_queries * ((max_query_len + 63) / 64) * 8;
+    if (overlaps(tree_mask, mask_bytes, parents, (size_t)num_queries * 4) ||
+        overlaps(tree_mask, mask_bytes, query_start, ((size_t)num_seqs + 1) * 4))
+        return PKV_ERR_OVERLAP;
     pkv::tree_masks_kernel<<<num_seqs, 64, 0, static_cast<cudaStream_t>(stream)>>>(
         tree_mask, parents, query_start, num_queries, max_query_len, (max_query_len + 63) / 64);
     return check_launch();
