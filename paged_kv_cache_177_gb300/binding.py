@@ -869,6 +869,8 @@ def paged_tree_attention(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tens
     NB, Hkv, P, D2 = cache
     if tree_mask.dtype != torch.int64 or len(words) != 2 or words[0] != T:
         raise TypeError("tree_mask must be int64 [T, W]")
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [S]")
     S = context_lens.shape[0]
     if query_start.shape != (S + 1,) or len(tables) != 2 or tables[0] != S:
         raise ValueError("query_start must be [S + 1] and block_tables [S, maxB]")
@@ -918,6 +920,8 @@ def kv_accept_layers(k_caches, v_caches, block_tables: torch.Tensor, context_len
     for t in (block_tables, context_lens, query_start, accepted, num_accepted, new_lens):
         if t.dtype != torch.int32:
             raise TypeError("the metadata tensors are int32")
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [S]")
     S = context_lens.shape[0]
     rows, tables = accepted.shape, block_tables.shape
     if len(rows) != 2 or rows[0] != S or num_accepted.shape != (S,) or new_lens.shape != (S,) \
