@@ -137,6 +137,32 @@ class BlockManager:
         seq.length += 1
         return slot, cow
 
+    def append_slots(self, seq_id: int, n: int) -> Tuple[List[int], Optional[Tuple[int, int]]]:
+        """Reserve the slots of the sequence's next ``n`` tokens (a step's
+        drafts), all or nothing; the slots in order, and ``cow`` as for
+        ``append_slot`` (only the first of them can meet a shared block).
+        ``truncate`` gives back what the step does not keep."""
+        seq = self._seqs[seq_id]
+        if n < 0:
+            raise ValueError("n must not be negative")
+        copies = n > 0 and seq.length % self.block_size != 0 and self.refcount[seq.table[-1]] > 1
+        need = blocks_needed(seq.length + n, self.block_size) - len(seq.table) + int(copies)
+        if not self.can_allocate(need):
+            raise NoFreeBlocks(f"need {need} blocks, {self.num_free} free")
+        taken = [self.append_slot(seq_id) for _ in range(n)]
+        return [slot for slot, _ in taken], next((cow for _, cow in taken if cow is not None), None)
+
+    def truncate(self, seq_id: int, num_tokens: int) -> None:
+        """Keep the sequence's first ``num_tokens`` tokens (its new length
+        after a step of drafts) and release the blocks behind them."""
+        seq = self._seqs[seq_id]
+        if not 0 <= num_tokens <= seq.length:
+            raise ValueError(f"sequence {seq_id} has {seq.length} tokens")
+        keep = blocks_needed(num_tokens, self.block_size)
+        while len(seq.table) > keep:
+            self._decref(seq.table.pop())
+        seq.length = int(num_tokens)
+
     def swap_out(self, seq_id: int, host: "BlockManager") -> List[Tuple[int, int]]:
         """Moves a sequence to a host pool (preemption by swapping, "Juntándolo
         todo: Arquitectura de vLLM"): one host block per table entry, all or
