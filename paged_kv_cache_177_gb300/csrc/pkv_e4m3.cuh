@@ -12,6 +12,7 @@
 
 #include <cuda_fp16.h>
 
+#include "pkv_cursor.cuh"
 #include "pkv_kernels.cuh"
 
 namespace pkv {
@@ -759,7 +760,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         cut.segments = 0;
         if (cuts_by_unit && lane == 0) {
             if (seg_j0 == 0) cuts[c.s * Hkv + c.h] = cut;
-            units_begun_later(c, left, prefix, Hkv, [&](int s, int h) { cuts[s * Hkv + h] = cut; });
+            units_begun_later(
+                c, left, [&](Cursor &at, int k) { cursor_advance(at, k, prefix, Hkv); },
+                [&](int s, int h) { cuts[s * Hkv + h] = cut; });
         }
     }
     if (cuts && !cuts_by_unit && lane == 0) cuts[w] = cut;

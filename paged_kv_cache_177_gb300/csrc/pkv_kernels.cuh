@@ -22,7 +22,6 @@
 #include <climits>
 
 #include "pagedkv.h"
-#include "pkv_cursor.cuh"
 #include "pkv_ptx.cuh"
 
 namespace pkv {
@@ -813,6 +812,28 @@ struct PersistCfg {
     static constexpr int kPrefixOffset = kBarOffset + 2 * NW * NS * 8;
     static constexpr size_t smem_bytes(int num_seqs) { return kPrefixOffset + (size_t)(num_seqs + 1) * 4 + 1024; }
 };
+
+// Position cursor: sequence s (with n = its blocks), kv head h, block j.
+struct Cursor {
+    int s, h, j, n;
+};
+
+// Moves c forward by k >= 0 positions; prefix[] holds the block-count prefix
+// sums. The caller guarantees the target position exists.
+__device__ __forceinline__ void cursor_advance(Cursor &c, int k, const int *prefix, int num_kv_heads) {
+    while (c.j + k >= c.n) {
+        k -= c.n - c.j;
+        c.j = 0;
+        if (++c.h == num_kv_heads) {
+            c.h = 0;
+            do {
+                ++c.s;
+                c.n = prefix[c.s + 1] - prefix[c.s];
+            } while (c.n == 0);
+        }
+    }
+    c.j += k;
+}
 
 // Merges the nseg segment states of one cut unit (worker w1's second slot,
 // then the first slots of workers w1+1 ..) with the log-sum-exp rule and

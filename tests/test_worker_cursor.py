@@ -2,8 +2,8 @@
 up, and wherever, every unit that holds tokens has a record written by the
 worker whose range it begins in. (The merge behind the decode kernel takes
 what it reads and writes from these records, and the workspace that holds
-them has no initial value.)  The walk is the kernel's own header, compiled
-with the host compiler; the loop around it restates the kernel's."""
+them has no initial value.)  The walk and the cursor are the kernel's own source,
+compiled with the host compiler; the loop around them restates the kernel's."""
 import ctypes
 import os
 import subprocess
@@ -13,9 +13,20 @@ import pytest
 
 from paged_kv_cache_177_gb300.build import CSRC
 
+
+def cursor_source():
+    """The cursor and its advance, from the kernels' header."""
+    with open(os.path.join(CSRC, "pkv_kernels.cuh")) as f:
+        text = f.read()
+    end = "    c.j += k;\n}\n"
+    span = text[text.index("struct Cursor {"):text.index(end) + len(end)]
+    return span.replace("__device__ __forceinline__ ", "static ")
+
+
 SOURCE = r"""
 #include "pkv_cursor.cuh"
 using namespace pkv;
+@CURSOR@
 // One worker's range [start, end): its loop up to the block of position start + stop, where it gives up
 // (stop = end - start: it does not). written[s * hkv + h] counts the unit's records.
 extern "C" void worker(const int *prefix, int S, int hkv, int start, int end, int stop, int *written) {
@@ -36,7 +47,8 @@ extern "C" void worker(const int *prefix, int S, int hkv, int start, int end, in
     while (true) {
         if (i == stop) {
             if (seg_j0 == 0) ++written[c.s * hkv + c.h];
-            units_begun_later(c, cnt - i, prefix, hkv, [&](int s, int h) { ++written[s * hkv + h]; });
+            units_begun_later(c, cnt - i, [&](Cursor &at, int k) { cursor_advance(at, k, prefix, hkv); },
+                              [&](int s, int h) { ++written[s * hkv + h]; });
             return;
         }
         const bool unit_end = c.j == c.n - 1;
@@ -58,7 +70,7 @@ extern "C" void worker(const int *prefix, int S, int hkv, int start, int end, in
 def worker(tmp_path_factory):
     d = tmp_path_factory.mktemp("cursor")
     src, lib = d / "worker.cpp", d / "worker.so"
-    src.write_text(SOURCE)
+    src.write_text(SOURCE.replace("@CURSOR@", cursor_source()))
     subprocess.check_call(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", CSRC, str(src), "-o", str(lib)])
     fn = ctypes.CDLL(os.fspath(lib)).worker
     fn.restype = None
