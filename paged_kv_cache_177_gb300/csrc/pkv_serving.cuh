@@ -75,28 +75,14 @@ int launch_dequantize(void *dk, void *dv, int dst_nb, const void *sk, const void
     return check_launch();
 }
 
-// Decode over e4m3 tiles: the persistent kernel's shape, workers and their ring. A worker's step is one chain of
-// dependent instructions, so as many warps run as their registers allow without spilling: twelve at head_dim 128
-// and sixteen at 64 with up to 8 heads to a kv head, eight and twelve with more, whose accumulators are
-// twice as many. (head_dim 64, 128 contexts around 1000, 32 q / 8 kv heads: 45 us with twelve, 40 with sixteen, 43 with
-// twenty; 8 contexts of 32K-128K, 64 q / 8 kv: 123, 108, 111. 16 heads to a kv head: 38 us with eight, 35 with
-// twelve. head_dim 128, 16 heads to a kv head: 36 us with eight, 45 with ten.)
-#ifndef PKV_E4M3_WARPS
-#define PKV_E4M3_WARPS 12
-#endif
-#ifndef PKV_E4M3_WARPS2
-#define PKV_E4M3_WARPS2 8
-#endif
-#ifndef PKV_E4M3_WARPS64
-#define PKV_E4M3_WARPS64 16
-#endif
-#ifndef PKV_E4M3_WARPS64_2
-#define PKV_E4M3_WARPS64_2 12
-#endif
-constexpr int e4m3_warps(int head_dim, int group) {
-    return head_dim == 128 ? (group <= 8 ? PKV_E4M3_WARPS : PKV_E4M3_WARPS2)
-                           : (group <= 8 ? PKV_E4M3_WARPS64 : PKV_E4M3_WARPS64_2);
-}
+// Decode over e4m3 tiles: the persistent kernel's warps, each a worker with its ring. A worker's step is one chain of
+// dependent instructions, so as many run as their registers allow without spilling: twelve at head_dim 128 and
+// sixteen at 64 with up to 8 heads to a kv head, eight and twelve with more, whose accumulators are twice as many.
+// head_dim 128, 256 contexts around 1000, 32 q / 8 kv heads: 119 us, 132 with ten, 142 with eight; 64: 128 such contexts
+// 39.6 us, 43.4 with twelve, 40.6 with twenty. 16 heads to a kv head, 8 kv heads, 256 contexts around 1000, head_dim 128: 175 us,
+// 222 with six, 223 with ten (64 contexts of 2 kv heads, which make few states: 29, 26, 34); head_dim 64, 256 contexts
+// of 1000-2000: 112 us, 138 with ten.
+constexpr int e4m3_warps(int head_dim, int group) { return head_dim == 128 ? (group <= 8 ? 12 : 8) : (group <= 8 ? 16 : 12); }
 constexpr int kE4m3MaxSeqs = 4096;  // sequences of one launch: their block counts lie in shared memory
 
 // Contexts this short are not cut: a worker takes whole (sequence, kv head) units and writes
@@ -136,6 +122,7 @@ int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t
     kern<<<grid, C::kThreads, C::smem_bytes(p.num_seqs), st>>>(p, cuts, whole ? 1 : 0, by_unit ? 1 : 0);
     const int rc = check_launch();
     if (rc != PKV_OK || whole) return rc;
+    // (80 units of 8000 tokens: 37.3 us with the wide merge, 40.5 with the narrow one; 224 of 4000: 47.1, 45.8; 512: 95, 89)
     const bool few = by_unit && 8 * units <= grid * NW;
     auto merge = [&](auto kernel, int warps) {
         return launch_pdl(kernel, dim3(by_unit ? (unsigned)units : grid * NW, few ? p.group : (p.group + 3) / 4),
@@ -154,7 +141,8 @@ int launch_decode_e4m3(pkv::DecodeParams &p, int head_dim, void *workspace, cuda
                         : launch_decode_e4m3_shape<64, 2, OutT>(p, workspace, st);
 }
 
-// Trees: contexts of at most four chunks of 128 keys are not cut, so no merge is launched.
+// Trees: contexts of at most four chunks of 128 keys are not cut, so no merge is launched. (16 drafts, 32 q / 8 kv heads,
+// whole and cut: 4 contexts of 240-480 tokens 13.2 and 15.7 us, of 450-900 18.0 and 16.6; 64: 35.0 and 35.4, 47.6 and 45.2.)
 bool tree_whole_units(int max_context_len) { return max_context_len <= 512; }
 
 // Two row tiles to a unit where one does not hold the largest tree's rows.
@@ -198,9 +186,9 @@ int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMa
                       static_cast<const pkv::TreeCut *>(cuts), C::kUnitRows, g, tp.d.num_q_heads, tile_tokens);
 }
 
-#ifndef PKV_ROPE_WARPS
-#define PKV_ROPE_WARPS 24
-#endif
+// Warps an SM that few tokens are spread over. (Tokens of 48 heads of 128, bf16: 256 take 6.1 us, 5.8 with 12 warps and 8.4
+// with 48; 700 take 7.8, 8.0 and 10.3; 1500 take 9.8, 11.1 and 13.0; 64 and fewer are the launch either way.)
+constexpr int kRopeWarpsPerSm = 24;
 
 template <typename T, int D>
 int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st) {
@@ -214,7 +202,7 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
     const int passes = (p.num_q_heads + 2 * p.num_kv_heads + rows_per_warp - 1) / rows_per_warp;
     int sms = 0;
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
-    const int want = (int)((long long)sms * PKV_ROPE_WARPS / p.num_tokens);
+    const int want = (int)((long long)sms * kRopeWarpsPerSm / p.num_tokens);
     p.warps_per_token = want < 1 ? 1 : want > passes ? passes : want;
     const long long blocks = ((long long)p.num_tokens * p.warps_per_token + pkv::kRopeWarps - 1) / pkv::kRopeWarps;
     kern<<<(unsigned)blocks, pkv::kRopeWarps * 32, 0, st>>>(p);
@@ -459,7 +447,9 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
         overlaps(new_lens, lens, block_tables, lens * max_blocks_per_seq))
         return PKV_ERR_OVERLAP;
     const int row_vecs = head_dim * elem_bytes(dtype) / 16;
-    // heads of a CTA: as many as 12 KiB hold the rows of, one at least (64 accepted rows of 512 bytes take 64 KiB)
+    // heads of a CTA: as many as 12 KiB hold the rows of, one at least (64 accepted rows of 512 bytes take 64 KiB). More
+    // heads share the lookups, fewer leave more CTAs: 64 sequences and 32 layers of 8 heads with 6 rows 13.6 us (17.8 with
+    // 4 KiB, 15.4 with 48), with 16 rows 34.8 (34.9, 70); 8 sequences 5.7 (4.6, 8.1).
     const int head_bytes = 2 * max_accepted * row_vecs * 16;
     int heads = head_bytes > 0 ? 12288 / head_bytes : num_kv_heads;
     heads = heads < 1 ? 1 : heads > num_kv_heads ? num_kv_heads : heads;
