@@ -86,8 +86,10 @@ constexpr int e4m3_warps(int head_dim, int group) { return head_dim == 128 ? (gr
 constexpr int kE4m3MaxSeqs = 4096;  // sequences of one launch: their block counts lie in shared memory
 
 // Contexts this short are not cut: a worker takes whole (sequence, kv head) units and writes
-// their outputs itself, so no merge is launched.
-bool e4m3_whole_units(int max_context_len) { return max_context_len <= 256; }
+// their outputs itself, so no merge is launched. (32 q / 8 kv heads, whole and cut: 4 contexts of up to 64 tokens
+// 8.5 and 12.2 us, of up to 96 12.0 and 11.5; 64 of up to 96 12.3 and 12.7, of up to 128 14.4 and 12.8, of up to
+// 256 22.8 and 14.0; 1000 of up to 64 32.6 and 34.6, of up to 128 51.9 and 48.3.)
+bool e4m3_whole_units(int max_context_len) { return max_context_len <= 96; }
 
 template <int D, int NT, typename OutT>
 int launch_decode_e4m3_shape(pkv::DecodeParams &p, void *workspace, cudaStream_t st) {

@@ -1,6 +1,7 @@
 """Decode over e4m3 tiles where the rows' scale bytes say little about their
 size, or lie far apart: blocks that nothing was written to, value rows of
-zeros, blocks with a bad id, one value row far larger than the others. Each
+zeros, blocks with a bad id, one value row far larger than the others; and
+contexts around the length from which they are cut among the workers. Each
 against a 64-bit softmax over the values that the tiles stand for, under the
 bound of the ordinary decode tests."""
 import numpy as np
@@ -161,3 +162,17 @@ def test_scores_as_large_as_fp32_resolves():
     for s, top in ((0, 33), (1, 17)):
         want = values[c.tables[s, top // 16], 0, top % 16]
         assert np.all(np.abs(out[s, 0] - want) <= (2.0 ** -11 + 2.0 ** -24) * np.abs(want))
+
+
+@pytest.mark.parametrize("most", [96, 97, 128, 257])
+@pytest.mark.parametrize("hkv,g,d,seqs", [(4, 4, 128, 300), (3, 1, 64, 40), (1, 16, 128, 7), (1, 2, 64, 4100)])
+def test_short_contexts_whole_and_cut(hkv, g, d, seqs, most):
+    """Contexts on both sides of the length up to which a worker takes whole units."""
+    b = S.lib()
+    rng = np.random.default_rng(seqs)
+    lens = [int(x) for x in rng.integers(0, 97 if seqs < 1000 else 20, size=seqs)]
+    lens[0], lens[-1] = 96, 0
+    c = Case(99, lens, hkv, g, d)
+    out = decode(b, c, torch.bfloat16, max_context_len=most)
+    assert b.device_error() == 0
+    c.check(out)
