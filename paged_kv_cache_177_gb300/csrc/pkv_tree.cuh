@@ -339,11 +339,16 @@ __device__ __noinline__ void tree_add_zeroed(const DecodeParams &p, const int64_
         const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
                                  (((size_t)pb * p.num_kv_heads + h) * kBlock + ps % kBlock) * head_dim + d0;
 #pragma unroll 1
-        for (int c = 0; c < cols; ++c) {
-            const float x = __bfloat162float(v[c]);
-            if (fabsf(x) < INFINITY) continue;
-            if (dst) dst[c] = __float2bfloat16_rn(__bfloat162float(dst[c]) + x);
-            else po[c] += x;
+        for (int c = 0; c < cols; c += 8) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(v + c);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = __uint_as_float(e & 1 ? u[e >> 1] & 0xffff0000u : u[e >> 1] << 16);
+                if (fabsf(x) < INFINITY) continue;
+                if (dst) dst[c + e] = __float2bfloat16_rn(__bfloat162float(dst[c + e]) + x);
+                else po[c + e] += x;
+            }
         }
     }
 }
