@@ -559,7 +559,9 @@ int qk_norm_rope_append(void *q_out, const void *q, const void *k, const void *v
  * and draft j exactly if bit j % 64 of tree_mask[row][j / 64] is set (its own
  * bit included; bits from n_s on are ignored). A row that sees nothing yields
  * zeros; a value that is not finite shows in its element of the rows that see
- * it, and in no other.
+ * it, and in no other. Weights are rounded to bf16 for the tensor cores; where
+ * a sequence has less than 64 context tokens, whose rows may see few keys, they
+ * keep 16 bits. Sums are fp32.
  *
  * q, out, query_start, context_lens, num_queries, max_query_len and
  *   max_context_len as for paged_prefill_attention (a bad n_s leaves the
@@ -588,7 +590,8 @@ size_t pkv_tree_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads,
  * tree_mask of paged_tree_attention from the drafts' parents: parents[row] is
  * the index within the sequence of the row's parent draft, -1 for a child of
  * the context; a draft comes after its parent. Row i gets the bits of i and
- * all its ancestors, in ceil(max_query_len / 64) words. A parent that is not
+ * all its ancestors, in ceil(max_query_len / 64) words (one load after another
+ * up a draft's ancestors: meant for trees, slow for long chains). A parent that is not
  * in [-1, i) ends the walk and raises PKV_DEVERR_INDEX. Bad n_s (as above)
  * raise PKV_DEVERR_LENGTH and leave the sequence's rows unwritten. tree_mask
  * overlaps no input (PKV_ERR_OVERLAP).

@@ -26,7 +26,9 @@ __device__ __forceinline__ bool tree_rows(const int32_t *query_start, int s, int
 
 // =====================================================================================
 // Masks from parents: one thread per draft walks up. Parents come before their children, so
-// the walk meets falling indexes and fills the row's words from the last to the first.
+// the walk meets falling indexes and fills the row's words from the last to the first. Its time is the deepest draft's
+// chain of loads, and a thread's drafts are 64 apart: 64 sequences of 32 drafts 2.5 us (4.6 as chains), 8 of 256 17 us
+// (68 as chains), one of 1024 217 us and, as one chain, 990 us.
 // =====================================================================================
 __global__ void tree_masks_kernel(int64_t *mask, const int32_t *parents, const int32_t *query_start, int num_queries,
                                   int max_query_len, int words) {
