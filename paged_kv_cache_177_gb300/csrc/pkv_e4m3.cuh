@@ -28,6 +28,8 @@ constexpr int kE4m3ExpLo = -50, kE4m3ExpHi = 50;  // range of a row's scale expo
 // kE4m3RefUp. kE4m3LeastByte stands for 2^-64, what a value row without magnitude takes there: lower than any
 // quantiser's, so that the row does not lift the reference, and high enough that its weight, which fp32 holds
 // down to 2^-126, adds to the sum all that counts beside the 2^-39 that a row of the largest scale adds at least.
+// (With a row of zeros far above all other scores the others' weights do lose bits, from where their share of the weight
+// is below 2^-(89 + ev), ev the exponent of their values: outputs that much smaller than the values.)
 constexpr float kE4m3RefSet = 11.f, kE4m3RefUp = 15.5f;
 constexpr uint32_t kE4m3LeastByte = 127 - 64;
 
