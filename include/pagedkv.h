@@ -627,6 +627,53 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
                      int num_kv_heads, int head_dim, int max_blocks_per_seq, int num_blocks, pkv_dtype dtype,
                      void *stream);
 
+/*
+ * Between paged_tree_attention and kv_accept_layers: which drafts stand, and the
+ * token that follows, so that the tokens are distributed as if the target
+ * had drawn each by itself. Random numbers are inputs.
+ *
+ * Sequence s owns rows query_start[s] .. query_start[s+1]-1, n_s of them. Row 0
+ * is the last token already chosen (the tree's root, always kept; its token,
+ * parent and uniform are not read), row i > 0 a draft, child of row parents[i]
+ * of its sequence, 0 <= parents[i] < i. target_probs[row] are the target's
+ * probabilities of the token behind that row, draft_probs[row] those the drafts
+ * behind it were drawn from: independent samples each, repeats allowed.
+ * NULL draft_probs: every draft was proposed for certain (q = 1).
+ *
+ * From row 0 on, with p and q the current row's probabilities, a = 0, Z = 1:
+ *   the row's children are tried in order; child i with token x stands if
+ *     uniforms[i] q(x) Z < max(p(x) - a q(x), 0)     and becomes the current row;
+ *   otherwise a becomes a + Z, and Z the sum of max(p - a q, 0) (unless that is 0:
+ *   then both stay). Without draft_probs a refused token's p counts as 0
+ *   instead, and Z is the sum of what is left.
+ * Where no child stands (or max_accepted rows do), next_tokens[s] is the first v
+ * whose running sum of max(p - a q, 0) exceeds final_uniforms[s] times the
+ * whole sum.
+ *
+ * accepted: int32 [num_seqs][max_accepted], the rows kept, from row 0 down, then -1;
+ *   num_accepted: int32 [num_seqs]; both as kv_accept_layers takes them
+ *   (up to PKV_MAX_ACCEPTED there). next_tokens: int64 [num_seqs].
+ * tokens: int64 and parents: int32 [num_queries]; uniforms: fp32 [num_queries],
+ *   final_uniforms: fp32 [num_seqs], in [0, 1). Probabilities: `dtype`
+ *   (PKV_F32 or PKV_BF16) [num_queries][vocab], rows target_stride and
+ *   draft_stride elements apart (at least vocab; any alignment, 16 bytes is faster).
+ * Probabilities enter sums as multiples of 2^-60, truncated, in 64-bit integers:
+ *   results do not depend on any order of addition. Negative ones and NaN count as
+ *   0, and sums must stay below 8 (they are 1 up to rounding).
+ * A sequence without rows, or with bad ones (n_s as for paged_tree_attention;
+ *   PKV_DEVERR_LENGTH), gets 0 rows and token -1; so does next_tokens where a
+ *   row holds no positive probability. A parent outside [0, i) makes a draft
+ *   that is never tried, a token outside [0, vocab) one that never stands;
+ *   both raise PKV_DEVERR_INDEX.
+ * max_accepted >= 1, max_query_len at most PKV_TREE_MAX_DRAFTS, vocab at most 2^30.
+ * Outputs overlap no input and no other output (PKV_ERR_OVERLAP).
+ */
+int verify_drafts(int32_t *accepted, int max_accepted, int32_t *num_accepted, int64_t *next_tokens,
+                  const int64_t *tokens, const int32_t *parents, const int32_t *query_start, const void *target_probs,
+                  int64_t target_stride, const void *draft_probs, int64_t draft_stride, const float *uniforms,
+                  const float *final_uniforms, int num_seqs, int num_queries, int max_query_len, int vocab,
+                  pkv_dtype dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -81,6 +81,8 @@ _tree = _decl("paged_tree_attention", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp
               _i, _i, _vp, _sz, _vp)
 _tree_ws = _decl("pkv_tree_workspace_bytes", _sz, _i, _i, _i, _i, _i, _i)
 _accept = _decl("kv_accept_layers", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp)
+_verify = _decl("verify_drafts", _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _i,
+                _vp)
 _device_error = _decl("pkv_device_error", _i, ctypes.POINTER(ctypes.c_uint32), _i)
 
 
@@ -939,6 +941,68 @@ def kv_accept_layers(k_caches, v_caches, block_tables: torch.Tensor, context_len
             accepted.data_ptr() if rows[1] else None, rows[1], num_accepted.data_ptr(), new_lens.data_ptr(), S, Hkv, D,
             max(1, tables[1]), NB, dt)
     return new_lens
+
+
+def _prob_rows(t: torch.Tensor, index: int, shape: Optional[tuple], dtype: Optional[torch.dtype], what: str) -> int:
+    """The distance of the rows of probabilities [T, V]."""
+    if t.get_device() != index:
+        raise ValueError("all tensors must be on the same device")
+    if t.dim() != 2 or (shape is not None and t.shape != shape) or t.shape[1] < 1:
+        raise ValueError(f"{what} must be [T, V]")
+    if t.dtype not in (torch.float32, torch.bfloat16) or (dtype is not None and t.dtype != dtype):
+        raise TypeError("probabilities are fp32 or bf16, both alike")
+    T, V = t.shape
+    st, se = t.stride()
+    if T and ((V > 1 and se != 1) or (T > 1 and st < V)):
+        raise ValueError(f"{what} must have contiguous rows that do not overlap")
+    return st if T > 1 else V
+
+
+def verify_drafts(accepted: torch.Tensor, num_accepted: torch.Tensor, next_tokens: torch.Tensor, tokens: torch.Tensor,
+                  parents: torch.Tensor, query_start: torch.Tensor, target_probs: torch.Tensor,
+                  uniforms: torch.Tensor, final_uniforms: torch.Tensor, *, draft_probs: Optional[torch.Tensor] = None,
+                  max_query_len: Optional[int] = None, stream: Optional[torch.cuda.Stream] = None) -> tuple:
+    """Walks each sequence's tree of drafts against the target's
+    probabilities, with the caller's random numbers: which rows are kept
+    (``accepted`` int32 [S, M] from row 0 down, then -1; ``num_accepted`` int32
+    [S], both as ``kv_accept_layers`` takes them) and the token behind the last
+    of them (``next_tokens`` int64 [S]); see include/pagedkv.h.
+
+    Row 0 of a sequence is its last chosen token, which is always kept; row i
+    > 0 is a draft below row parents[i] of its sequence (int32 [T], parents
+    first).  tokens: int64 [T].  target_probs [T, V]: the target's
+    probabilities of what follows each row; draft_probs [T, V]: those that the
+    drafts below each row were drawn from, independently (None: each draft was
+    proposed for certain); fp32 or bf16, rows any distance apart.  uniforms
+    fp32 [T] and final_uniforms fp32 [S], in [0, 1).  ``max_query_len`` defaults
+    to the most rows of a sequence (a sync).  Returns the three outputs."""
+    dev = _index(accepted, num_accepted, next_tokens, tokens, parents, query_start, uniforms, final_uniforms)
+    ts = _prob_rows(target_probs, dev, None, None, "target_probs")
+    T, V = target_probs.shape
+    ds = 0
+    if draft_probs is not None:
+        ds = _prob_rows(draft_probs, dev, target_probs.shape, target_probs.dtype, "draft_probs")
+    if not (accepted.dtype == num_accepted.dtype == parents.dtype == query_start.dtype == torch.int32):
+        raise TypeError("accepted, num_accepted, parents and query_start are int32")
+    if tokens.dtype != torch.int64 or next_tokens.dtype != torch.int64:
+        raise TypeError("tokens and next_tokens are int64")
+    if uniforms.dtype != torch.float32 or final_uniforms.dtype != torch.float32:
+        raise TypeError("uniforms and final_uniforms are fp32")
+    rows = accepted.shape
+    if len(rows) != 2:
+        raise ValueError("accepted must be [S, M]")
+    S, M = rows
+    if num_accepted.shape != (S,) or next_tokens.shape != (S,) or final_uniforms.shape != (S,) \
+            or query_start.shape != (S + 1,) or tokens.shape != (T,) or parents.shape != (T,) or uniforms.shape != (T,):
+        raise ValueError("expected num_accepted, next_tokens, final_uniforms [S], query_start [S + 1] and tokens, "
+                         "parents, uniforms [T]")
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
+    _launch(_verify, "verify_drafts", dev, stream, accepted.data_ptr(), M, num_accepted.data_ptr(),
+            next_tokens.data_ptr(), tokens.data_ptr(), parents.data_ptr(), query_start.data_ptr(),
+            target_probs.data_ptr(), ts, _p(draft_probs), ds, uniforms.data_ptr(), final_uniforms.data_ptr(), S, T,
+            int(max_query_len), V, PKV_F32 if target_probs.dtype == torch.float32 else PKV_BF16)
+    return accepted, num_accepted, next_tokens
 
 
 def validate(block_tables: torch.Tensor, context_lens: torch.Tensor, num_blocks: int, max_context_len: int,

@@ -211,6 +211,33 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
     return check_launch();
 }
 
+// CTAs of a cluster that takes a sequence's rows of the vocabulary. One CTA streams them alone; with few sequences more
+// CTAs share a row, up to eight and not below a few steps of every warp.
+int verify_ctas(int num_seqs, int vocab, int sms) {
+    int c = 8;
+    while (c > 1 && ((long long)num_seqs * c > 2LL * sms || (long long)vocab < 2048LL * c)) c /= 2;
+    return c;
+}
+
+template <typename T>
+int launch_verify(const pkv::VerifyParams &p, int num_seqs, cudaStream_t st) {
+    int sms = 0;
+    if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
+    const int c = verify_ctas(num_seqs, p.vocab, sms);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)num_seqs * c);
+    cfg.blockDim = dim3(pkv::kVerifyThreads);
+    cfg.dynamicSmemBytes = sizeof(pkv::VerifyShared);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, pkv::verify_drafts_kernel<T>, p) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -470,6 +497,47 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
     pkv::kv_accept_kernel<<<dim3((num_kv_heads + heads - 1) / heads, num_layers, num_seqs), 128, smem,
                             static_cast<cudaStream_t>(stream)>>>(p);
     return check_launch();
+}
+
+int verify_drafts(int32_t *accepted, int max_accepted, int32_t *num_accepted, int64_t *next_tokens,
+                  const int64_t *tokens, const int32_t *parents, const int32_t *query_start, const void *target_probs,
+                  int64_t target_stride, const void *draft_probs, int64_t draft_stride, const float *uniforms,
+                  const float *final_uniforms, int num_seqs, int num_queries, int max_query_len, int vocab,
+                  pkv_dtype dtype, void *stream) {
+    if (num_seqs < 0 || num_queries < 0 || max_query_len < 0 || max_accepted < 1 || vocab <= 0) return PKV_ERR_ARG;
+    if (!dtype_ok(dtype) || max_query_len > PKV_TREE_MAX_DRAFTS || vocab > (1 << 30) || num_seqs > (1 << 24))
+        return PKV_ERR_UNSUPPORTED;
+    if (target_stride < vocab || (draft_probs && draft_stride < vocab)) return PKV_ERR_ARG;
+    const int eb = elem_bytes(dtype);
+    const int64_t most = (INT64_MAX / 8) / (num_queries > 0 ? num_queries : 1);  // (rows' bytes fit 63 bits)
+    if (target_stride > most || (draft_probs && draft_stride > most)) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!accepted || !num_accepted || !next_tokens || !query_start || !final_uniforms) return PKV_ERR_ARG;
+    if (num_queries > 0 && (!tokens || !parents || !target_probs || !uniforms)) return PKV_ERR_ARG;
+    auto off = [](const void *p, int bytes) { return reinterpret_cast<uintptr_t>(p) % bytes != 0; };
+    if (off(accepted, 4) || off(num_accepted, 4) || off(next_tokens, 8) || off(tokens, 8) || off(parents, 4) ||
+        off(query_start, 4) || off(target_probs, eb) || off(draft_probs, eb) || off(uniforms, 4) ||
+        off(final_uniforms, 4))
+        return PKV_ERR_ALIGN;
+    auto row_bytes = [&](int64_t stride) { return num_queries > 0 ? (size_t)((num_queries - 1) * stride + vocab) * eb : 0; };
+    const size_t seqs = num_seqs, rows = num_queries;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } all[] = {{accepted, seqs * max_accepted * 4}, {num_accepted, seqs * 4}, {next_tokens, seqs * 8},
+               {tokens, rows * 8}, {parents, rows * 4}, {query_start, (seqs + 1) * 4},
+               {target_probs, row_bytes(target_stride)}, {draft_probs, draft_probs ? row_bytes(draft_stride) : 0},
+               {uniforms, rows * 4}, {final_uniforms, seqs * 4}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < (int)(sizeof(all) / sizeof(all[0])); ++j)
+            if (all[j].bytes > 0 && overlaps(all[i].p, all[i].bytes, all[j].p, all[j].bytes)) return PKV_ERR_OVERLAP;
+    const bool vector_rows = aligned16(target_probs) && target_stride * eb % 16 == 0 &&
+                             (!draft_probs || (aligned16(draft_probs) && draft_stride * eb % 16 == 0));
+    const pkv::VerifyParams p{accepted, num_accepted, next_tokens, tokens, parents, query_start, target_probs, draft_probs,
+                              target_stride, draft_stride, uniforms, final_uniforms, num_queries, max_query_len,
+                              max_accepted, vocab, vector_rows ? 1 : 0};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == PKV_BF16 ? launch_verify<__nv_bfloat16>(p, num_seqs, st) : launch_verify<float>(p, num_seqs, st);
 }
 
 }  // extern "C"
