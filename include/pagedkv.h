@@ -657,9 +657,9 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
  *   final_uniforms: fp32 [num_seqs], in [0, 1). Probabilities: `dtype`
  *   (PKV_F32 or PKV_BF16) [num_queries][vocab], rows target_stride and
  *   draft_stride elements apart (at least vocab; any alignment, 16 bytes is faster).
- * Probabilities enter sums as multiples of 2^-60, truncated, in 64-bit integers:
+ * Probabilities enter sums as multiples of 2^-44, rounded to nearest, in integers:
  *   results do not depend on any order of addition. Negative ones and NaN count as
- *   0, and sums must stay below 8 (they are 1 up to rounding).
+ *   0, ones above 1 as 1.
  * A sequence without rows, or with bad ones (n_s as for paged_tree_attention;
  *   PKV_DEVERR_LENGTH), gets 0 rows and token -1; so does next_tokens where a
  *   row holds no positive probability. A parent outside [0, i) makes a draft

@@ -211,11 +211,14 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
     return check_launch();
 }
 
-// CTAs of a cluster that takes a sequence's rows of the vocabulary. One CTA streams them alone; with few sequences more
-// CTAs share a row, up to eight and not below a few steps of every warp.
-int verify_ctas(int num_seqs, int vocab, int sms) {
+// CTAs of the cluster that takes a sequence. Few sequences share their rows among up to eight CTAs, as long as all fit
+// the card at once (two an SM) and a CTA's warps have a step each; rows of more than 512 KB are shared anyway, so that the
+// sequences whose drafts are refused more than once, which read on when the others are done, take less long.
+// (With one, two, four and eight: 16 trees of 131072 tokens, p and q in fp32, 42, 27, 19.5, 15.9 us; 64 48, 32, 27, 27;
+// 256 79, 64, 62, 80; 64 of 32000 21, 17, 17, 23; without q, 64 rows of 131072 24, 17, 16, 22, 256 42, 42, 49, 72.)
+int verify_ctas(int num_seqs, int vocab, size_t row_bytes, int sms) {
     int c = 8;
-    while (c > 1 && ((long long)num_seqs * c > 2LL * sms || (long long)vocab < 2048LL * c)) c /= 2;
+    while (c > 1 && (((long long)num_seqs * c > 2LL * sms && row_bytes <= (size_t)c << 18) || vocab < 2048LL * c)) c /= 2;
     return c;
 }
 
@@ -223,7 +226,7 @@ template <typename T>
 int launch_verify(const pkv::VerifyParams &p, int num_seqs, cudaStream_t st) {
     int sms = 0;
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
-    const int c = verify_ctas(num_seqs, p.vocab, sms);
+    const int c = verify_ctas(num_seqs, p.vocab, sizeof(T) * p.vocab * (p.draft ? 2 : 1), sms);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)num_seqs * c);
     cfg.blockDim = dim3(pkv::kVerifyThreads);
