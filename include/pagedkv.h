@@ -628,6 +628,31 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
                      void *stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * Transformed scores
+ * ---------------------------------------------------------------------------
+ * paged_decode_attention for layers that change their scores before the softmax
+ * or see part of the context. With pos = context_lens[s] - 1 and t a token's
+ * position, the score of query head hq is
+ *   x = scale q . K_t;   x = softcap tanh(x / softcap)  (softcap > 0);
+ *   x = x - slopes[hq] (pos - t)  (slopes given: a bias that grows with the distance);
+ * and with window > 0 only the last `window` tokens are seen, t > pos - window.
+ * Blocks that lie wholly before the window are not read, nor are their table
+ * entries; a row before the window in its first block, or behind the context in
+ * the last, may hold anything.
+ * slopes: fp32 [num_q_heads], device, finite (NULL: none). softcap: finite, not
+ *   negative (0: none). window: tokens (0: all). Every other argument, the
+ *   workspace, an empty context and errors as for paged_decode_attention;
+ *   dtype PKV_BF16 or PKV_F32. max_context_len bounds the contexts, not the window.
+ */
+int paged_decode_attention_scored(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_tables, const int32_t *context_lens, float scale, float softcap,
+                                  int window, const float *slopes, int num_kv_heads, int num_seqs, int num_q_heads,
+                                  int head_dim, int max_blocks_per_seq, int num_blocks, int max_context_len,
+                                  pkv_dtype dtype, int partition_tokens, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/*
  * Between paged_tree_attention and kv_accept_layers: which drafts stand, and the
  * token that follows, so that the tokens are distributed as if the target
  * had drawn each by itself. Random numbers are inputs.

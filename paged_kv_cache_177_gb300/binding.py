@@ -81,6 +81,8 @@ _tree = _decl("paged_tree_attention", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp
               _i, _i, _vp, _sz, _vp)
 _tree_ws = _decl("pkv_tree_workspace_bytes", _sz, _i, _i, _i, _i, _i, _i)
 _accept = _decl("kv_accept_layers", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp)
+_scored = _decl("paged_decode_attention_scored", _i, _vp, _vp, _vp, _vp, _vp, _vp, _f, _f, _i, _vp, _i, _i, _i, _i, _i,
+                _i, _i, _i, _i, _vp, _sz, _vp)
 _verify = _decl("verify_drafts", _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _i,
                 _vp)
 _device_error = _decl("pkv_device_error", _i, ctypes.POINTER(ctypes.c_uint32), _i)
@@ -941,6 +943,61 @@ def kv_accept_layers(k_caches, v_caches, block_tables: torch.Tensor, context_len
             accepted.data_ptr() if rows[1] else None, rows[1], num_accepted.data_ptr(), new_lens.data_ptr(), S, Hkv, D,
             max(1, tables[1]), NB, dt)
     return new_lens
+
+
+def _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens) -> tuple:
+    """(S, Hq, D, NB, Hkv, maxB) of one query a sequence over bf16 or fp32 caches."""
+    if not (q.dtype == out.dtype == k_cache.dtype == v_cache.dtype):
+        raise TypeError("q, out and the caches must share one dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    shape, cache, tables = q.shape, k_cache.shape, block_tables.shape
+    if len(shape) != 3 or out.shape != shape or len(cache) != 4 or cache[2] != BLOCK_SIZE or cache[3] != shape[2] \
+            or v_cache.shape != cache:
+        raise ValueError("expected q, out [S, Hq, D] and caches [NB, Hkv, 16, D]")
+    if len(tables) != 2 or tables[0] != shape[0] or context_lens.shape != shape[:1]:
+        raise ValueError("expected block_tables [S, maxB] and context_lens [S]")
+    return (*shape, cache[0], cache[1], tables[1])
+
+
+def _slopes(slopes: Optional[torch.Tensor], num_q_heads: int, index: int):
+    if slopes is None:
+        return None
+    if slopes.dtype != torch.float32 or slopes.shape != (num_q_heads,) or _index(slopes) != index:
+        raise TypeError("slopes must be fp32 [Hq] on the caches' device")
+    return slopes.data_ptr()
+
+
+def paged_decode_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *,
+                                  softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
+                                  max_context_len: Optional[int] = None, partition_tokens: int = 0,
+                                  workspace: Optional[torch.Tensor] = None,
+                                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_decode_attention with transformed scores: capped to softcap *
+    tanh(score / softcap) (0: not), less slopes[hq] times the token's distance
+    from the query (fp32 [Hq]; None: no bias), over the last ``window`` tokens
+    only (0: all); see include/pagedkv.h.
+
+    q, out [S, Hq, D] and caches [NB, Hkv, 16, D] of one dtype, bf16 or fp32;
+    the other arguments and the workspace as for ``paged_decode_attention``."""
+    dev = _index_io((k_cache, v_cache), (out, q, block_tables, context_lens))
+    dt = _dtype_code(q)
+    S, Hq, D, NB, Hkv, max_blocks = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    max_context_len = int(max_context_len)
+    if workspace is None:
+        need = _workspace_bytes(S, Hq, Hkv, D, max_context_len, partition_tokens)
+        if need:
+            with torch.cuda.stream(stream):       # zero-filled, on the call's stream
+                workspace = torch.zeros(need, dtype=torch.uint8, device=k_cache.device)
+    keep, ws, ws_bytes = _workspace(0, workspace, dev, stream)
+    _launch(_scored, "paged_decode_attention_scored", dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale), float(softcap),
+            int(window), _slopes(slopes, Hq, dev), Hkv, S, Hq, D, max_blocks, NB, max_context_len, dt,
+            int(partition_tokens), ws, ws_bytes)
+    return out
 
 
 def _prob_rows(t: torch.Tensor, index: int, shape: Optional[tuple], dtype: Optional[torch.dtype], what: str) -> int:

@@ -41,8 +41,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    # --split-compile=0: the kernels are optimised in parallel, on all cores
-    cmd = [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "--split-compile=0", "-Xcompiler", "-fPIC", "-shared",
+    cmd = [nvcc_path(), *ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
            "-I", INCLUDE, *_sources(), "-o", tmp]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

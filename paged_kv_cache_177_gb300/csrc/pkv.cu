@@ -182,11 +182,11 @@ int max_parts_for(int max_context_len, int part_tokens) {
     return (max_context_len + part_tokens - 1) / part_tokens;
 }
 
-template <int D, int NT, typename OutT, class WA = pkv::WarpAttn<D, NT>>
+template <int D, int NT, typename OutT, class WA = pkv::WarpAttn<D, NT>, int FORM = pkv::kWhole>
 int launch_bf16(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::DecodeParams &p, dim3 grid,
                 cudaStream_t st, bool pdl = false) {
     using C = pkv::Bf16Cfg<D, NT, kNstage, kNcw>;
-    auto kern = pkv::decode_bf16_kernel<D, NT, kNstage, kNcw, OutT, WA>;
+    auto kern = pkv::decode_bf16_kernel<D, NT, kNstage, kNcw, OutT, WA, FORM>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -211,12 +211,12 @@ int launch_bf16(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::Decod
 #endif
 constexpr int kF32Stages = PKV_F32_STAGES, kF32Ncw = PKV_F32_NCW;
 
-template <int D, int GMAX>
+template <int D, int GMAX, int FORM>
 int launch_f32_staged(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::DecodeParams &p, dim3 grid,
                       cudaStream_t st, bool pdl) {
     using C = pkv::F32Cfg<D, GMAX, kF32Stages, kF32Ncw>;
     static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
-    auto kern = pkv::decode_f32_staged_kernel<D, GMAX, kF32Stages, kF32Ncw>;
+    auto kern = pkv::decode_f32_staged_kernel<D, GMAX, kF32Stages, kF32Ncw, FORM>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -244,12 +244,12 @@ int launch_f32_staged(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv:
 #endif
 constexpr bool kF32Tc = PKV_F32_TC != 0;
 
-template <int D, int GMAX>
+template <int D, int GMAX, int FORM>
 int launch_f32_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::DecodeParams &p, dim3 grid,
                   cudaStream_t st, bool pdl) {
-    using C = pkv::F32TcCfg<D, GMAX, PKV_F32_TC_STAGES, PKV_F32_TC_NCW>;
+    using C = pkv::F32TcCfg<D, GMAX, PKV_F32_TC_STAGES, PKV_F32_TC_NCW, FORM == pkv::kScored>;
     static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
-    auto kern = pkv::decode_f32_tc_kernel<D, GMAX, PKV_F32_TC_STAGES, PKV_F32_TC_NCW>;
+    auto kern = pkv::decode_f32_tc_kernel<D, GMAX, PKV_F32_TC_STAGES, PKV_F32_TC_NCW, FORM>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -264,19 +264,21 @@ int launch_f32_tc(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::Dec
 }
 
 // fp32 caches: the tensor maps of both caches, then the instance for the group size.
-template <int D>
+template <int D, int FORM>
 int launch_f32(const pkv::DecodeParams &p, dim3 grid, cudaStream_t st, bool pdl) {
     alignas(64) CUtensorMap tmk, tmv;
     int rc;
     if ((rc = encode_cache_map_f32(&tmk, p.k_cache, p.num_blocks, p.num_kv_heads, D)) != PKV_OK) return rc;
     if ((rc = encode_cache_map_f32(&tmv, p.v_cache, p.num_blocks, p.num_kv_heads, D)) != PKV_OK) return rc;
     const int g = p.group;
-    if (g == 1) return launch_f32_staged<D, 1>(tmk, tmv, p, grid, st, pdl);
-    if (g == 2) return launch_f32_staged<D, 2>(tmk, tmv, p, grid, st, pdl);
-    if (g <= 4) return launch_f32_staged<D, 4>(tmk, tmv, p, grid, st, pdl);
-    if (kF32Tc) return g <= 8 ? launch_f32_tc<D, 8>(tmk, tmv, p, grid, st, pdl) : launch_f32_tc<D, 16>(tmk, tmv, p, grid, st, pdl);
-    if (g <= 8) return launch_f32_staged<D, 8>(tmk, tmv, p, grid, st, pdl);
-    return launch_f32_staged<D, 16>(tmk, tmv, p, grid, st, pdl);
+    if (g == 1) return launch_f32_staged<D, 1, FORM>(tmk, tmv, p, grid, st, pdl);
+    if (g == 2) return launch_f32_staged<D, 2, FORM>(tmk, tmv, p, grid, st, pdl);
+    if (g <= 4) return launch_f32_staged<D, 4, FORM>(tmk, tmv, p, grid, st, pdl);
+    if (kF32Tc)
+        return g <= 8 ? launch_f32_tc<D, 8, FORM>(tmk, tmv, p, grid, st, pdl)
+                      : launch_f32_tc<D, 16, FORM>(tmk, tmv, p, grid, st, pdl);
+    if (g <= 8) return launch_f32_staged<D, 8, FORM>(tmk, tmv, p, grid, st, pdl);
+    return launch_f32_staged<D, 16, FORM>(tmk, tmv, p, grid, st, pdl);
 }
 
 template <int D, int NT>
@@ -300,15 +302,15 @@ int launch_cascade(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::De
     return check_launch();
 }
 
-template <int D>
+template <int D, int FORM>
 int launch_reduce(const pkv::DecodeParams &p, pkv_dtype dt, cudaStream_t st) {
     constexpr int PG = 512 / D;  // partition groups: 512 threads per row
     dim3 grid(p.num_q_heads, p.num_seqs);
     const size_t smem = (32 + (size_t)PG * D + (size_t)p.max_parts) * sizeof(float);
     if (dt == PKV_BF16)
-        pkv::lse_reduce_kernel<__nv_bfloat16, D, PG><<<grid, D * PG, smem, st>>>(p);
+        pkv::lse_reduce_kernel<__nv_bfloat16, D, PG, FORM><<<grid, D * PG, smem, st>>>(p);
     else
-        pkv::lse_reduce_kernel<float, D, PG><<<grid, D * PG, smem, st>>>(p);
+        pkv::lse_reduce_kernel<float, D, PG, FORM><<<grid, D * PG, smem, st>>>(p);
     return check_launch();
 }
 
@@ -375,12 +377,12 @@ int sm_count(int *n) {
     return PKV_OK;
 }
 
-template <int D, int NT, int NS, int NW, typename OutT, class WA = pkv::WarpAttn<D, NT>>
+template <int D, int NT, int NS, int NW, typename OutT, class WA = pkv::WarpAttn<D, NT>, int FORM = pkv::kWhole>
 int launch_persistent(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::DecodeParams &p, cudaStream_t st,
                       bool pdl = false) {
     using C = pkv::PersistCfg<D, NT, NS, NW>;
     static_assert(C::smem_bytes(kPersistMaxSeqs) + 64 <= kSmemLimit, "persistent kernel exceeds shared memory");
-    auto kern = pkv::decode_bf16_persistent_kernel<D, NT, NS, NW, OutT, WA>;
+    auto kern = pkv::decode_bf16_persistent_kernel<D, NT, NS, NW, OutT, WA, FORM>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -404,34 +406,39 @@ int launch_persistent(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv:
 // One query head per kv head (g = 1) takes the CUDA-core step in both
 // kernels: the block's contraction is then a matrix-vector product that
 // would fill one of the tensor cores' eight MMA columns.
-template <typename OutT, int NS128, int NS64, int NW>
+template <typename OutT, int NS128, int NS64, int NW, int FORM>
 int persistent_by_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::DecodeParams &p, cudaStream_t st,
                         bool pdl, int head_dim, int g) {
+    constexpr bool kS = FORM == pkv::kScored;
     if (head_dim == 128) {
         if (g == 1 && kMhaCudaCores)
-            return launch_persistent<128, 1, NS128, NW, OutT, pkv::WarpAttnScalar<128>>(tmk, tmv, p, st, pdl);
-        return g <= 8 ? launch_persistent<128, 1, NS128, NW, OutT>(tmk, tmv, p, st, pdl)
-                      : launch_persistent<128, 2, 2 * NS128, NW / 2, OutT>(tmk, tmv, p, st, pdl);
+            return launch_persistent<128, 1, NS128, NW, OutT, pkv::WarpAttnScalar<128>, FORM>(tmk, tmv, p, st, pdl);
+        return g <= 8
+                   ? launch_persistent<128, 1, NS128, NW, OutT, pkv::WarpAttn<128, 1, kS>, FORM>(tmk, tmv, p, st, pdl)
+                   : launch_persistent<128, 2, 2 * NS128, NW / 2, OutT, pkv::WarpAttn<128, 2, kS>, FORM>(tmk, tmv, p,
+                                                                                                        st, pdl);
     }
     if (g == 1 && kMhaCudaCores)
-        return launch_persistent<64, 1, NS64, NW, OutT, pkv::WarpAttnScalar<64>>(tmk, tmv, p, st, pdl);
-    return g <= 8 ? launch_persistent<64, 1, NS64, NW, OutT>(tmk, tmv, p, st, pdl)
-                  : launch_persistent<64, 2, 2 * NS64, NW / 2, OutT>(tmk, tmv, p, st, pdl);
+        return launch_persistent<64, 1, NS64, NW, OutT, pkv::WarpAttnScalar<64>, FORM>(tmk, tmv, p, st, pdl);
+    return g <= 8 ? launch_persistent<64, 1, NS64, NW, OutT, pkv::WarpAttn<64, 1, kS>, FORM>(tmk, tmv, p, st, pdl)
+                  : launch_persistent<64, 2, 2 * NS64, NW / 2, OutT, pkv::WarpAttn<64, 2, kS>, FORM>(tmk, tmv, p, st,
+                                                                                                    pdl);
 }
 
-template <typename OutT>
+template <typename OutT, int FORM>
 int grid_by_shape(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::DecodeParams &p, dim3 grid,
                   cudaStream_t st, bool pdl, int head_dim, int g) {
+    constexpr bool kS = FORM == pkv::kScored;
     if (head_dim == 128) {
         if (g == 1 && kMhaCudaCores)
-            return launch_bf16<128, 1, OutT, pkv::WarpAttnScalar<128>>(tmk, tmv, p, grid, st, pdl);
-        return g <= 8 ? launch_bf16<128, 1, OutT>(tmk, tmv, p, grid, st, pdl)
-                      : launch_bf16<128, 2, OutT>(tmk, tmv, p, grid, st, pdl);
+            return launch_bf16<128, 1, OutT, pkv::WarpAttnScalar<128>, FORM>(tmk, tmv, p, grid, st, pdl);
+        return g <= 8 ? launch_bf16<128, 1, OutT, pkv::WarpAttn<128, 1, kS>, FORM>(tmk, tmv, p, grid, st, pdl)
+                      : launch_bf16<128, 2, OutT, pkv::WarpAttn<128, 2, kS>, FORM>(tmk, tmv, p, grid, st, pdl);
     }
     if (g == 1 && kMhaCudaCores)
-        return launch_bf16<64, 1, OutT, pkv::WarpAttnScalar<64>>(tmk, tmv, p, grid, st, pdl);
-    return g <= 8 ? launch_bf16<64, 1, OutT>(tmk, tmv, p, grid, st, pdl)
-                  : launch_bf16<64, 2, OutT>(tmk, tmv, p, grid, st, pdl);
+        return launch_bf16<64, 1, OutT, pkv::WarpAttnScalar<64>, FORM>(tmk, tmv, p, grid, st, pdl);
+    return g <= 8 ? launch_bf16<64, 1, OutT, pkv::WarpAttn<64, 1, kS>, FORM>(tmk, tmv, p, grid, st, pdl)
+                  : launch_bf16<64, 2, OutT, pkv::WarpAttn<64, 2, kS>, FORM>(tmk, tmv, p, grid, st, pdl);
 }
 
 // The persistent balanced kernel is chosen for bf16 when asked for
@@ -455,11 +462,34 @@ bool use_persistent(pkv_dtype dtype, int partition_tokens, int num_seqs, int num
 // set-up overlaps the append, cache reads wait for it); or only check.
 constexpr int kLaunch = 0, kLaunchAfterAppend = 1, kCheckOnly = 2;
 
+// How a call transforms its scores.
+struct ScoreArgs {
+    float softcap;
+    int window;
+    const float *slopes;
+};
+
+// The checked arguments of a transformation, into p.
+int score_params(pkv::DecodeParams &p, const ScoreArgs &a, float scale) {
+    if (!(a.softcap >= 0.f) || !std::isfinite(a.softcap) || a.window < 0) return PKV_ERR_ARG;
+    if ((reinterpret_cast<uintptr_t>(a.slopes) & 3) != 0) return PKV_ERR_ALIGN;
+    p.window = a.window;
+    p.slopes = a.slopes;
+    p.cap_log2 = p.cap_in = 0.f;
+    if (a.softcap > 0.f) {
+        p.cap_log2 = (float)((double)a.softcap * 1.4426950408889634);
+        p.cap_in = (float)((double)scale / (double)a.softcap);
+        if (p.cap_log2 == 0.f || !std::isfinite(p.cap_log2) || !std::isfinite(p.cap_in)) return PKV_ERR_ARG;
+    }
+    return PKV_OK;
+}
+
 // Shared by the decode entry points once the workspace is known.
 int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
                     const int32_t *context_lens, float scale, int num_kv_heads, int num_seqs, int num_q_heads,
                     int head_dim, int max_blocks_per_seq, int num_blocks, int max_context_len, pkv_dtype dtype,
-                    int partition_tokens, void *workspace, size_t workspace_bytes, void *stream, int mode = kLaunch);
+                    int partition_tokens, void *workspace, size_t workspace_bytes, void *stream, int mode = kLaunch,
+                    const ScoreArgs *scores = nullptr);
 }  // namespace
 
 extern "C" {
@@ -887,7 +917,8 @@ namespace {
 int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
                     const int32_t *context_lens, float scale, int num_kv_heads, int num_seqs, int num_q_heads,
                     int head_dim, int max_blocks_per_seq, int num_blocks, int max_context_len, pkv_dtype dtype,
-                    int partition_tokens, void *workspace, size_t workspace_bytes, void *stream, int mode) {
+                    int partition_tokens, void *workspace, size_t workspace_bytes, void *stream, int mode,
+                    const ScoreArgs *scores) {
     if (num_seqs < 0 || num_kv_heads <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
         max_context_len < 0 || partition_tokens < PKV_PARTITION_BALANCED)
         return PKV_ERR_ARG;
@@ -899,6 +930,12 @@ int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v
     const int g = num_q_heads / num_kv_heads;
     if (g > 16) return PKV_ERR_UNSUPPORTED;
     if (!std::isfinite(scale)) return PKV_ERR_ARG;
+    pkv::DecodeParams p{};
+    if (scores) {
+        const int rc = score_params(p, *scores, scale);
+        if (rc != PKV_OK) return rc;
+        if (f32_out) return PKV_ERR_UNSUPPORTED;
+    }
     if (num_seqs > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
     if ((int64_t)num_blocks * num_kv_heads * 16 >= (int64_t(1) << 31)) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
@@ -915,7 +952,6 @@ int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v
     if (mode == kCheckOnly) return PKV_OK;
     const bool pdl = mode == kLaunchAfterAppend;
 
-    pkv::DecodeParams p{};
     p.out = out;
     p.q = q;
     p.k_cache = k_cache;
@@ -942,28 +978,41 @@ int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v
         if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
         if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
         constexpr int ns128 = PKV_PERSIST_STAGES_D128, ns64 = PKV_PERSIST_STAGES_D64, nw = kPersistWarps;
-        return f32_out ? persistent_by_shape<float, ns128, ns64, nw>(tmk, tmv, p, st, pdl, head_dim, g)
-                       : persistent_by_shape<__nv_bfloat16, ns128, ns64, nw>(tmk, tmv, p, st, pdl, head_dim, g);
+        if (scores)
+            return persistent_by_shape<__nv_bfloat16, ns128, ns64, nw, pkv::kScored>(tmk, tmv, p, st, pdl, head_dim, g);
+        return f32_out
+                   ? persistent_by_shape<float, ns128, ns64, nw, pkv::kWhole>(tmk, tmv, p, st, pdl, head_dim, g)
+                   : persistent_by_shape<__nv_bfloat16, ns128, ns64, nw, pkv::kWhole>(tmk, tmv, p, st, pdl, head_dim, g);
     }
 
     const size_t grid_ws = grid_workspace_bytes(num_seqs, num_q_heads, head_dim, max_context_len, pt);
     p.ws_ml = grid_ws ? reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes) : nullptr;
     p.ws_o = grid_ws ? p.ws_ml + (size_t)num_seqs * num_q_heads * mp * 2 : nullptr;
-    dim3 grid(mp, num_kv_heads, num_seqs);
+    int parts = mp;  // that a sequence can have: a window of W tokens touches at most (W - 2) / 16 + 2 blocks
+    if (scores && scores->window > 0)
+        parts = (int)std::min<long long>(mp, ((scores->window - 1LL) / 16 + 2 + p.part_blocks - 1) / p.part_blocks);
+    dim3 grid(parts, num_kv_heads, num_seqs);
     int rc;
     if (dtype == PKV_BF16) {
         alignas(64) CUtensorMap tmk, tmv;
         if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
         if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
-        rc = f32_out ? grid_by_shape<float>(tmk, tmv, p, grid, st, pdl, head_dim, g)
-                     : grid_by_shape<__nv_bfloat16>(tmk, tmv, p, grid, st, pdl, head_dim, g);
+        rc = scores    ? grid_by_shape<__nv_bfloat16, pkv::kScored>(tmk, tmv, p, grid, st, pdl, head_dim, g)
+             : f32_out ? grid_by_shape<float, pkv::kWhole>(tmk, tmv, p, grid, st, pdl, head_dim, g)
+                       : grid_by_shape<__nv_bfloat16, pkv::kWhole>(tmk, tmv, p, grid, st, pdl, head_dim, g);
+    } else if (scores) {
+        rc = head_dim == 128 ? launch_f32<128, pkv::kScored>(p, grid, st, pdl)
+                             : launch_f32<64, pkv::kScored>(p, grid, st, pdl);
     } else {
-        rc = head_dim == 128 ? launch_f32<128>(p, grid, st, pdl) : launch_f32<64>(p, grid, st, pdl);
+        rc = head_dim == 128 ? launch_f32<128, pkv::kWhole>(p, grid, st, pdl)
+                             : launch_f32<64, pkv::kWhole>(p, grid, st, pdl);
     }
-    if (rc != PKV_OK) return rc;
+    if (rc != PKV_OK || parts <= 1) return rc;
     const pkv_dtype out_dt = f32_out ? PKV_F32 : dtype;
-    if (mp > 1) rc = head_dim == 128 ? launch_reduce<128>(p, out_dt, st) : launch_reduce<64>(p, out_dt, st);
-    return rc;
+    if (scores)
+        return head_dim == 128 ? launch_reduce<128, pkv::kScored>(p, out_dt, st)
+                               : launch_reduce<64, pkv::kScored>(p, out_dt, st);
+    return head_dim == 128 ? launch_reduce<128, pkv::kWhole>(p, out_dt, st) : launch_reduce<64, pkv::kWhole>(p, out_dt, st);
 }
 
 }  // namespace

@@ -73,6 +73,14 @@ struct DecodeParams {
     const int32_t *shared_blocks; // [num_groups] leading blocks the members share
     int num_groups, group_size;
     int pre_parts;                // workspace slots per row reserved for the prefix parts
+    // transformed scores (ScoredRows)
+    const float *slopes;          // [Hq] or null
+    float cap_log2, cap_in;       // cap log2(e) and scale / cap; cap_log2 0: no cap
+    int window;                   // tokens a query sees, itself included; 0: all
+    // decode behind a prefix that was attended before (kBehindPrefix)
+    const int32_t *first_blocks;  // [S] blocks of the prefix
+    const float *prefix_ml;       // [S][Hq][2]: its max (log2 domain) and sum, ...
+    const float *prefix_o;        // [S][Hq][D]: ... and unnormalised output
 };
 
 
@@ -106,6 +114,81 @@ __device__ __forceinline__ float block_reduce(float v, bool is_max, float *scrat
 
 
 
+// How a staged block's raw products become scores in the log2 domain; -inf where a row is no token that the query sees.
+// Plain: rows below `lo` are not tokens of the sequence (its last block is loaded that many rows early, zero-filled).
+struct PlainRows {
+    static constexpr bool kScored = false;
+    int lo;
+    float scale_log2;
+    __device__ __forceinline__ float score(float raw, int row, float) const {
+        return row >= lo ? raw * scale_log2 : -INFINITY;
+    }
+    __device__ __forceinline__ bool seen(int) const { return true; }
+};
+
+// cap log2(e) tanh(y), y = raw scale / cap. 1 - 2 / (1 + e^2y) takes three instructions on the special-function unit and
+// is off by 2^-22 of the cap, which is 2^-20 of the score from y = 1/4 on; below that the Taylor series to y^7 is as near
+// (the next term is 62/2835 y^8 < 2^-21 of it), so a cap far above the scores costs them nothing.
+__device__ __forceinline__ float capped(float raw, float cap_in, float cap_log2) {
+    const float y = raw * cap_in, y2 = y * y;
+    const float near = fmaf(fmaf(fmaf(-17.f / 315.f, y2, 2.f / 15.f), y2, -1.f / 3.f), y2, 1.f) * y;
+    const float far = 1.f - __fdividef(2.f, ex2_approx(y * 2.885390082f) + 1.f);
+    return cap_log2 * (y2 < 0.0625f ? near : far);
+}
+// The same for fp32 caches, whose outputs are held to 1e-5: tanhf is within 2 units in its last place.
+__device__ __forceinline__ float capped_exact(float raw, float cap_in, float cap_log2) {
+    return cap_log2 * tanhf(raw * cap_in);
+}
+
+// Transformed: capped, less slope times the distance, cut to rows lo .. hi - 1 (tokens within the window). The rows are
+// not shifted or zero-filled, so what other rows hold must not meet a weight of zero: see seen().
+template <bool kExact>
+struct ScoredRowsOf {
+    static constexpr bool kScored = true;
+    int lo, hi;
+    float dist;  // of row 0 from the query
+    float scale_log2, cap_in, cap_log2;
+    __device__ __forceinline__ float score(float raw, int row, float slope) const {
+        float x = raw * scale_log2;
+        if (cap_log2 != 0.f)
+            x = kExact ? capped_exact(raw, cap_in, cap_log2) : capped(raw, cap_in, cap_log2);
+        x = fmaf(-slope, dist - row, x);
+        return seen(row) ? x : -INFINITY;
+    }
+    __device__ __forceinline__ bool seen(int row) const { return row >= lo && row < hi; }
+};
+using ScoredRows = ScoredRowsOf<false>;
+
+// What of its context a unit attends: all of it; the window, with transformed scores; or what lies behind a
+// prefix that was attended before, starting from that state.
+constexpr int kWhole = 0, kScored = 1, kBehindPrefix = 2;
+
+// The first block that a sequence of len tokens reads.
+template <int FORM>
+__device__ __forceinline__ int first_block(const DecodeParams &p, int s, int len) {
+    if constexpr (FORM == kScored) return p.window > 0 && len > p.window ? (len - p.window) / kBlock : 0;
+    else if constexpr (FORM == kBehindPrefix) return min(max(__ldg(p.first_blocks + s), 0), len / kBlock);
+    else return 0;
+}
+
+// The rows of block b of a sequence of len tokens, whose last token is the query.
+template <bool kExact>
+__device__ __forceinline__ ScoredRowsOf<kExact> scored_rows(const DecodeParams &p, int b, int len) {
+    const int t0 = b * kBlock, start = p.window > 0 ? max(0, len - p.window) : 0;
+    return {max(start - t0, 0), min(len - t0, kBlock), (float)(len - 1 - t0), p.scale_log2, p.cap_in, p.cap_log2};
+}
+
+// The slope of query head `head` of the group whose slopes these are, in the log2 domain.
+__device__ __forceinline__ float slope_log2(const float *slopes, int head, int g) {
+    return slopes && head < g ? __ldg(slopes + head) * 1.4426950408889634f : 0.f;
+}
+
+// Weights of a block also enter as their rounding remainders (kSplitBlocks): in a unit's first blocks, and where
+// scores fall off with distance in its last ones, whose few tokens may then carry all the weight.
+__device__ __forceinline__ bool split_scored(const DecodeParams &p, int j, int n) {
+    return j < kSplitBlocks || (p.slopes && j >= n - kSplitBlocks);
+}
+
 // =====================================================================================
 // The per-block step shared by both bf16 decode kernels. One warp attends a
 // (block, kv head) tile already staged in shared memory (K and V, [16][D]
@@ -118,7 +201,7 @@ __device__ __forceinline__ float block_reduce(float v, bool is_max, float *scrat
 // the log2 domain (scale_log2 = scale log2 e). Lane (gq = lane/4, t4 = lane%4)
 // holds heads 2 t4, 2 t4 + 1 of each 8-wide n-tile.
 // =====================================================================================
-template <int D, int NT>
+template <int D, int NT, bool kSlopes = false>
 struct WarpAttn {
     static constexpr int kSteps = D / 16;
     static constexpr int kSubBytes = kBlock * 128;      // 2 KiB: 16 rows of 64 bf16
@@ -128,6 +211,33 @@ struct WarpAttn {
     float m[NT][2], l[NT][2];
     float acc[kSteps][NT][4];
     QFrag qf;                                            // Q^T as the MMA B operand
+    float slope[kSlopes ? NT : 1][2];                    // of the lane's two columns of each n-tile
+
+    __device__ __forceinline__ void load_slopes(const float *slopes, int g, int lane) {
+#pragma unroll
+        for (int nt = 0; nt < (kSlopes ? NT : 1); ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) slope[nt][c] = slope_log2(slopes, nt * 8 + 2 * (lane & 3) + c, g);
+    }
+
+    // Starts from an earlier state of the g heads: ml [g][2] (max in the log2 domain, sum), o [g][D].
+    __device__ __forceinline__ void load_state(const float *ml, const float *o, int g, int lane) {
+        const int gq = lane >> 2, t4 = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int head = nt * 8 + 2 * t4 + c;
+                const bool on = head < g;
+                m[nt][c] = on ? __ldcg(ml + 2 * head) : -INFINITY;
+                l[nt][c] = on && gq == 0 ? __ldcg(ml + 2 * head + 1) : 0.f;
+#pragma unroll
+                for (int mt = 0; mt < kSteps; ++mt) {
+                    acc[mt][nt][c] = on ? __ldcg(o + (size_t)head * D + 16 * mt + gq) : 0.f;
+                    acc[mt][nt][c + 2] = on ? __ldcg(o + (size_t)head * D + 16 * mt + gq + 8) : 0.f;
+                }
+            }
+    }
 
     __device__ __forceinline__ void set_q(const QFrag &f) {
 #pragma unroll
@@ -262,11 +372,12 @@ struct WarpAttn {
     // col_lo, col_hi: the MMA columns this block is attended for (columns
     // outside get no weight from it; a shared-prefix unit attends each
     // member's own blocks for that member's columns only).
-    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, int lo, float scale_log2, int lane,
-                                          int col_lo = 0, int col_hi = 8 * NT, bool split = false) {
+    template <class Rows>
+    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, const Rows &rows, int lane, int col_lo = 0,
+                                          int col_hi = 8 * NT, bool split = false) {
         float sc[NT][4];
         scores(sk, sc, lane);
-        softmax_pv(sc, sv, lo, scale_log2, lane, col_lo, col_hi, split);
+        softmax_pv(sc, sv, rows, lane, col_lo, col_hi, split);
     }
 
     // S^T = K . Q^T for the 16 tokens of the staged K tile (two independent
@@ -303,20 +414,21 @@ struct WarpAttn {
     // from the staged V tile. With `split` the weights enter the product as
     // the sum of two bf16 values (the rounded weight and its rounding
     // remainder), 16 significant bits instead of 8 (see kSplitBlocks).
-    __device__ __forceinline__ void softmax_pv(const float (&sc)[NT][4], uint32_t sv, int lo, float scale_log2,
-                                               int lane, int col_lo = 0, int col_hi = 8 * NT, bool split = false) {
+    template <class Rows>
+    __device__ __forceinline__ void softmax_pv(const float (&sc)[NT][4], uint32_t sv, const Rows &rows, int lane,
+                                               int col_lo = 0, int col_hi = 8 * NT, bool split = false) {
         const int gq = lane >> 2, t4 = lane & 3;
         const int mi = lane >> 3, r8 = lane & 7;
-        const bool v0 = gq >= lo, v1 = gq + 8 >= lo;
         uint32_t pb0[NT], pb1[NT], pl0[NT], pl1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int c0 = nt * 8 + 2 * t4;
             const bool k0 = c0 >= col_lo && c0 < col_hi, k1 = c0 + 1 >= col_lo && c0 + 1 < col_hi;
-            const float x0 = (v0 && k0) ? sc[nt][0] * scale_log2 : -INFINITY;
-            const float x1 = (v0 && k1) ? sc[nt][1] * scale_log2 : -INFINITY;
-            const float x2 = (v1 && k0) ? sc[nt][2] * scale_log2 : -INFINITY;
-            const float x3 = (v1 && k1) ? sc[nt][3] * scale_log2 : -INFINITY;
+            const float s0 = Rows::kScored ? slope[kSlopes ? nt : 0][0] : 0.f, s1 = Rows::kScored ? slope[kSlopes ? nt : 0][1] : 0.f;
+            const float x0 = k0 ? rows.score(sc[nt][0], gq, s0) : -INFINITY;
+            const float x1 = k1 ? rows.score(sc[nt][1], gq, s1) : -INFINITY;
+            const float x2 = k0 ? rows.score(sc[nt][2], gq + 8, s0) : -INFINITY;
+            const float x3 = k1 ? rows.score(sc[nt][3], gq + 8, s1) : -INFINITY;
             float mx0 = fmaxf(x0, x2), mx1 = fmaxf(x1, x3);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -359,6 +471,9 @@ struct WarpAttn {
             pb0[nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&plo));
             pb1[nt] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&phi));
         }
+        // V^T fragments hold tokens 2 t4, 2 t4 + 1 (and + 8): those of rows that are not seen become zeros
+        auto keep = [&](int row) { return (rows.seen(row) ? 0xffffu : 0u) | (rows.seen(row + 1) ? 0xffff0000u : 0u); };
+        const uint32_t keep0 = Rows::kScored ? keep(2 * t4) : 0u, keep1 = Rows::kScored ? keep(2 * t4 + 8) : 0u;
 
 #pragma unroll
         for (int mt = 0; mt < kSteps; ++mt) {
@@ -367,6 +482,12 @@ struct WarpAttn {
             const int chunk = (mt & 3) * 2 + (mi & 1);
             uint32_t a[4];
             ldsm_x4_trans(sv + u * kSubBytes + row * 128 + ((chunk ^ (row & 7)) << 4), a);
+            if constexpr (Rows::kScored) {
+                a[0] &= keep0;
+                a[1] &= keep0;
+                a[2] &= keep1;
+                a[3] &= keep1;
+            }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_bf16_16816(acc[mt][nt], a, pb0[nt], pb1[nt]);
             if (split) {
@@ -417,6 +538,19 @@ struct WarpAttnScalar {
     float m, l;
     uint64_t acc[kDims / 2];                            // packed fp32 pairs: elements kDims*lane ..
     QFrag qw;                                           // widened to fp32 where used
+    float slope;
+
+    __device__ __forceinline__ void load_slopes(const float *slopes, int g, int) { slope = slope_log2(slopes, 0, g); }
+
+    __device__ __forceinline__ void load_state(const float *ml, const float *o, int, int lane) {
+        m = __ldcg(ml);
+        l = lane == 0 ? __ldcg(ml + 1) : 0.f;
+#pragma unroll
+        for (int i = 0; i < kDims / 2; ++i) {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(o + kDims * lane) + i);
+            acc[i] = pack_f2(v.x, v.y);
+        }
+    }
 
     static __device__ __forceinline__ void load_q_frags(QFrag &f, const __nv_bfloat16 *q_group, int, int lane) {
         const uint4 *src = reinterpret_cast<const uint4 *>(q_group + (lane >> 3) * kQuarter);
@@ -481,12 +615,13 @@ struct WarpAttnScalar {
     }
 
     // Online-softmax update with the block's scores, then acc += V^T p.
-    // Rows below `lo` are not tokens of the sequence (zero-filled by TMA).
-    __device__ __forceinline__ void softmax_pv(const Scores &s, uint32_t sv, int lo, float scale_log2, int lane,
-                                               int = 0, int = 0, bool = false) {
+    template <class Rows>
+    __device__ __forceinline__ void softmax_pv(const Scores &s, uint32_t sv, const Rows &rows, int lane, int = 0,
+                                               int = 0, bool = false) {
         const int h4 = lane >> 3, t8 = lane & 7;
-        const float x0 = t8 >= lo ? s[0] * scale_log2 : -INFINITY;
-        const float x1 = t8 + 8 >= lo ? s[1] * scale_log2 : -INFINITY;
+        const float sl = Rows::kScored ? slope : 0.f;
+        const float x0 = rows.score(s[0], t8, sl);
+        const float x1 = rows.score(s[1], t8 + 8, sl);
         float mx = fmaxf(x0, x1);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -521,6 +656,10 @@ struct WarpAttnScalar {
                 uint32_t we[2], wo[2];
                 ld_shared_v2(ae, we);
                 ld_shared_v2(ao, wo);
+                if constexpr (Rows::kScored) {  // (the same rows in all lanes)
+                    if (!rows.seen(t)) we[0] = we[1] = 0;
+                    if (!rows.seen(t + 1)) wo[0] = wo[1] = 0;
+                }
                 acc[0] = fma_f2(bf16x2_to_f2(we[0]), pe2, acc[0]);
                 acc[1] = fma_f2(bf16x2_to_f2(we[1]), pe2, acc[1]);
                 a2[0] = fma_f2(bf16x2_to_f2(wo[0]), po2, a2[0]);
@@ -529,6 +668,10 @@ struct WarpAttnScalar {
                 uint32_t we, wo;
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(we) : "r"(ae));
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(wo) : "r"(ao));
+                if constexpr (Rows::kScored) {
+                    if (!rows.seen(t)) we = 0;
+                    if (!rows.seen(t + 1)) wo = 0;
+                }
                 acc[0] = fma_f2(bf16x2_to_f2(we), pe2, acc[0]);
                 a2[0] = fma_f2(bf16x2_to_f2(wo), po2, a2[0]);
             }
@@ -554,11 +697,12 @@ struct WarpAttnScalar {
         }
     }
 
-    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, int lo, float scale_log2, int lane, int = 0,
-                                          int = 0, bool = false) {
+    template <class Rows>
+    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, const Rows &rows, int lane, int = 0, int = 0,
+                                          bool = false) {
         Scores sc;
         scores(sk, sc, lane);
-        softmax_pv(sc, sv, lo, scale_log2, lane);
+        softmax_pv(sc, sv, rows, lane);
     }
 
     __device__ __forceinline__ void store_merge(float *ml, float *acc_rows, int, int lane) const {
@@ -667,12 +811,12 @@ __device__ __forceinline__ void grid_produce(const CUtensorMap &tmk, const CUten
 
 // Consumer warps of the grid kernels: blocks j = warp, warp + NCW, ... of the
 // staged range (block_args(j, stage) gives each block's early-loaded rows and
-// column range), then the warps' states merged through shared memory. For
+// column range, rows_of(j, early) its rows' view), then the warps' states merged through shared memory. For
 // each column c < ncols (an MMA column: a query head of a query sequence)
 // and head-dim index d, emit(c, d, o, M, L) receives the column's output
 // o = O / L and its (max, sum) in the log2 domain.
-template <class C, int D, int NSTAGE, int NCW, class WA, class BlockArgs, class Emit>
-__device__ __forceinline__ void grid_consume(WA &wa, int nb, BlockArgs block_args, float scale_log2, uint8_t *base,
+template <class C, int D, int NSTAGE, int NCW, class WA, class BlockArgs, class RowsOf, class Emit>
+__device__ __forceinline__ void grid_consume(WA &wa, int nb, BlockArgs block_args, RowsOf rows_of, uint8_t *base,
                                              uint64_t *full, uint64_t *empty, int ncols, int warp, int lane, int tid,
                                              Emit emit) {
     for (int j = warp; j < nb; j += NCW) {
@@ -683,7 +827,7 @@ __device__ __forceinline__ void grid_consume(WA &wa, int nb, BlockArgs block_arg
         }
         const uint32_t sk = smem_u32(base + st * C::kStage);
         const int4 a = block_args(j, st);  // (rows loaded early, first column, column end, split)
-        wa.block(sk, sk + C::kTile, a.x, scale_log2, lane, a.y, a.z, a.w != 0);
+        wa.block(sk, sk + C::kTile, rows_of(j, a.x), lane, a.y, a.z, a.w != 0);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
     }
@@ -710,7 +854,8 @@ __device__ __forceinline__ void grid_consume(WA &wa, int nb, BlockArgs block_arg
     }
 }
 
-template <int D, int NT, int NSTAGE, int NCW, typename OutT = __nv_bfloat16, class WA = WarpAttn<D, NT>>
+template <int D, int NT, int NSTAGE, int NCW, typename OutT = __nv_bfloat16, class WA = WarpAttn<D, NT>,
+          int FORM = kWhole>
 __global__ void __launch_bounds__((NCW + 1) * 32)
     decode_bf16_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                        const DecodeParams p) {
@@ -721,8 +866,8 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = p.group;
     const int len = seq_len(p, s, tid == 0 && part == 0 && h == 0);
-    const int nblk = (len + kBlock - 1) / kBlock;
-    const int npart = (nblk + p.part_blocks - 1) / p.part_blocks;
+    const int nblk = (len + kBlock - 1) / kBlock, first = first_block<FORM>(p, s, len);
+    const int npart = (nblk - first + p.part_blocks - 1) / p.part_blocks;
     OutT *out = static_cast<OutT *>(p.out);
 
     if (len == 0) {  // empty context: zero output rows
@@ -734,9 +879,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
     }
     if (part >= npart) return;
 
-    const int b_begin = part * p.part_blocks;
+    const int b_begin = first + part * p.part_blocks;
     const int nb = min(nblk - b_begin, p.part_blocks);
-    const int last_valid = len - (nblk - 1) * kBlock;  // tokens in the sequence's last block
+    // tokens in the sequence's last block, which is loaded early (with transformed scores in place: all its rows)
+    const int last_valid = FORM == kScored ? kBlock : len - (nblk - 1) * kBlock;
 
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(base + C::kBarOffset);
@@ -760,14 +906,20 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
     WA wa;
     wa.load_q(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)s * p.num_q_heads + (size_t)h * g) * D, g, lane);
     wa.reset();
+    if constexpr (FORM == kScored) wa.load_slopes(p.slopes ? p.slopes + h * g : nullptr, g, lane);
     const size_t orow0 = (size_t)s * p.num_q_heads + (size_t)h * g;
     const int last_in_range = (b_begin + nb - 1 == nblk - 1) ? nb - 1 : -1;
     grid_consume<C, D, NSTAGE, NCW>(
         wa, nb,
         [&](int j, int) {
-            return make_int4(j == last_in_range ? kBlock - last_valid : 0, 0, C::kHeads, b_begin + j < kSplitBlocks);
+            const bool split = FORM == kScored ? split_scored(p, b_begin - first + j, nblk - first) : b_begin + j < kSplitBlocks;
+            return make_int4(j == last_in_range ? kBlock - last_valid : 0, 0, C::kHeads, split);
         },
-        p.scale_log2, base, full, empty, g, warp, lane, tid, [&](int col, int d, float o, float M, float L) {
+        [&](int j, int early) {
+            if constexpr (FORM == kScored) return scored_rows<false>(p, b_begin + j, len);
+            else return PlainRows{early, p.scale_log2};
+        },
+        base, full, empty, g, warp, lane, tid, [&](int col, int d, float o, float M, float L) {
             if (npart == 1) {
                 out[(orow0 + col) * D + d] = to_out<OutT>(o);
             } else {
@@ -906,7 +1058,7 @@ __device__ __forceinline__ void merge_segments(const float *partials, size_t slo
 
 // WA: the per-block step -- WarpAttn (tensor cores, any group up to 8 NT) or
 // WarpAttnScalar (CUDA cores, one query head per kv head).
-template <int D, int NT, int NS, int NW, typename OutT = __nv_bfloat16, class WA = WarpAttn<D, NT>>
+template <int D, int NT, int NS, int NW, typename OutT = __nv_bfloat16, class WA = WarpAttn<D, NT>, int FORM = kWhole>
 __global__ void __launch_bounds__(NW * 32, 1)
     decode_bf16_persistent_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                   const DecodeParams p) {
@@ -929,10 +1081,14 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
 
     // ---- block-count prefix sums over the batch (every CTA computes its own copy) ----
+    auto blocks_of = [&](int s, bool flag) {
+        const int len = seq_len(p, s, flag);
+        return (len + kBlock - 1) / kBlock - first_block<FORM>(p, s, len);
+    };
     const int per = (S + C::kThreads - 1) / C::kThreads;
     const int s_lo = min(S, tid * per), s_hi = min(S, s_lo + per);
     int local = 0;
-    for (int s = s_lo; s < s_hi; ++s) local += (seq_len(p, s, blockIdx.x == 0) + kBlock - 1) / kBlock;
+    for (int s = s_lo; s < s_hi; ++s) local += blocks_of(s, blockIdx.x == 0);
     int incl = local;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -945,7 +1101,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     for (int w = 0; w < warp; ++w) run += warp_total[w];
     for (int s = s_lo; s < s_hi; ++s) {
         prefix[s] = run;
-        run += (seq_len(p, s, false) + kBlock - 1) / kBlock;
+        run += blocks_of(s, false);
     }
     if (tid == 0) {
         int tot = 0;
@@ -954,11 +1110,20 @@ __global__ void __launch_bounds__(NW * 32, 1)
     }
     __syncthreads();
 
-    // ---- empty contexts: zero output rows (spread over the CTAs) ----
+    // ---- empty contexts: zero output rows (spread over the CTAs); nothing behind a prefix: the prefix's output ----
+    if constexpr (FORM == kBehindPrefix) pdl_wait();  // (written by the kernel before)
     for (int s = blockIdx.x; s < S; s += gridDim.x) {
         if (prefix[s + 1] == prefix[s]) {
             OutT *o = out + (size_t)s * p.num_q_heads * D;
-            for (int i = tid; i < p.num_q_heads * D; i += C::kThreads) o[i] = to_out<OutT>(0.f);
+            for (int i = tid; i < p.num_q_heads * D; i += C::kThreads) {
+                float v = 0.f;
+                if constexpr (FORM == kBehindPrefix) {
+                    const size_t row = (size_t)s * p.num_q_heads + i / D;
+                    const float l = __ldcg(p.prefix_ml + 2 * row + 1);
+                    if (l != 0.f) v = __ldcg(p.prefix_o + row * D + i % D) / l;
+                }
+                o[i] = to_out<OutT>(v);
+            }
         }
     }
 
@@ -997,8 +1162,15 @@ __global__ void __launch_bounds__(NW * 32, 1)
         Batch r{0, 0};
         if (lane < count) {
             cursor_advance(b, lane, prefix, Hkv);
-            r.pb = __ldg(p.block_tables + (size_t)b.s * p.max_blocks_per_seq + b.j);
-            const int shift = (b.j == b.n - 1) ? kBlock * b.n - seq_len(p, b.s, false) : 0;
+            int first = 0, shift = 0;
+            if constexpr (FORM == kWhole) {
+                shift = (b.j == b.n - 1) ? kBlock * b.n - seq_len(p, b.s, false) : 0;
+            } else {
+                const int len = seq_len(p, b.s, false);
+                first = first_block<FORM>(p, b.s, len);
+                if (FORM == kBehindPrefix && b.j == b.n - 1) shift = kBlock * (first + b.n) - len;
+            }
+            r.pb = __ldg(p.block_tables + (size_t)b.s * p.max_blocks_per_seq + first + b.j);
             r.hs = b.h * 16 + shift;
         }
         return r;
@@ -1061,8 +1233,21 @@ __global__ void __launch_bounds__(NW * 32, 1)
     WA wa;
     int seg_j0 = c.j;
     int len = seq_len(p, c.s, false);
+    int first = first_block<FORM>(p, c.s, len);
     wa.load_q(static_cast<const __nv_bfloat16 *>(p.q) + ((size_t)c.s * p.num_q_heads + (size_t)c.h * g) * D, g, lane);
-    wa.reset();
+    // a segment's state: nothing yet, or where it begins its unit what the prefix left
+    auto begin = [&]() {
+        if constexpr (FORM == kScored) wa.load_slopes(p.slopes ? p.slopes + c.h * g : nullptr, g, lane);
+        if constexpr (FORM == kBehindPrefix) {
+            if (seg_j0 == 0) {
+                const size_t row = (size_t)c.s * p.num_q_heads + (size_t)c.h * g;
+                wa.load_state(p.prefix_ml + 2 * row, p.prefix_o + row * D, g, lane);
+                return;
+            }
+        }
+        wa.reset();
+    };
+    begin();
 
     const __nv_bfloat16 *qbase = static_cast<const __nv_bfloat16 *>(p.q);
     typename WA::QFrag qnext;
@@ -1092,8 +1277,12 @@ __global__ void __launch_bounds__(NW * 32, 1)
             raise_error(PKV_DEVERR_TIMEOUT);
             break;
         }
-        wa.softmax_pv(sc, sk + C::kTile, unit_end ? kBlock * c.n - len : 0, p.scale_log2, lane, 0, 8 * NT,
-                      c.j < kSplitBlocks);
+        if constexpr (FORM == kScored)
+            wa.softmax_pv(sc, sk + C::kTile, scored_rows<false>(p, first + c.j, len), lane, 0, 8 * NT,
+                          split_scored(p, c.j, c.n));
+        else
+            wa.softmax_pv(sc, sk + C::kTile, PlainRows{unit_end ? kBlock * (first + c.n) - len : 0, p.scale_log2}, lane,
+                          0, 8 * NT, first + c.j < kSplitBlocks);
         __syncwarp();  // ... and its V fragment loads before the V refill
         if (refill) issue_v();
 
@@ -1132,8 +1321,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         c = cn;
         seg_j0 = 0;
         len = len_next;
+        first = first_block<FORM>(p, c.s, len);
         wa.set_q(qnext);
-        wa.reset();
+        begin();
     }
 }
 
@@ -1303,7 +1493,8 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
             const int early = info.y & 0xff, split = info.y >> 8;
             return info.x < 0 ? make_int4(early, 0, ncols, split) : make_int4(early, info.x * g, info.x * g + g, split);
         },
-        p.scale_log2, base, full, empty, ncols, warp, lane, tid, [&](int col, int d, float o, float Mx, float L) {
+        [&](int, int early) { return PlainRows{early, p.scale_log2}; }, base, full, empty, ncols, warp, lane, tid,
+        [&](int col, int d, float o, float Mx, float L) {
             const int r0 = row_of(col);
             if (r0 < 0) return;
             const size_t r = (size_t)r0 * p.max_parts + part;
@@ -1445,7 +1636,7 @@ struct F32Cfg {
 // shared-memory slot so that P V can take four tokens' weights of a head in one
 // broadcast load; lane l accumulates head-dim elements kDims l .. kDims l + kDims - 1 of
 // every head.
-template <int D, int GMAX>
+template <int D, int GMAX, bool kSlopes = false>
 struct WarpAttnF32 {
     static constexpr int kSubBytes = kBlock * 128;  // 2 KiB: 16 rows of 32 fp32
     static constexpr int kQC = D / 16;        // 16-byte chunks in a quarter row
@@ -1457,6 +1648,12 @@ struct WarpAttnF32 {
     uint64_t acc[GMAX][kDims / 2];
     uint32_t q_s, p_s;  // shared addresses: staged query rows, this warp's weights
     int g;
+    float slope[kSlopes ? GMAX : 1];
+
+    __device__ __forceinline__ void load_slopes(const float *slopes) {
+#pragma unroll
+        for (int h = 0; h < (kSlopes ? GMAX : 1); ++h) slope[h] = slope_log2(slopes, h, g);
+    }
 
     __device__ __forceinline__ void init(uint32_t q_smem, uint32_t p_smem, int group) {
         q_s = q_smem;
@@ -1474,11 +1671,11 @@ struct WarpAttnF32 {
         }
     }
 
-    // Rows below `lo` of the staged tiles are not tokens of the sequence (zero-filled by TMA).
     // Heads go in groups of kHG (scores, softmax, then P V per group): fewer registers at
     // the price of reading the block's K and V tiles from shared memory once per group.
-    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, int lo, float scale_log2, int lane, int = 0,
-                                          int = 0, bool = false) {
+    template <class Rows>
+    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, const Rows &rows, int lane, int = 0, int = 0,
+                                          bool = false) {
         const int h4 = lane >> 3, t8 = lane & 7;
         constexpr int kLaneBytes = kDims * 4;
         const int ci_v = (lane * kLaneBytes) >> 4;
@@ -1526,8 +1723,9 @@ struct WarpAttnF32 {
                     s1 += __shfl_xor_sync(0xffffffffu, s1, 8);
                     s0 += __shfl_xor_sync(0xffffffffu, s0, 16);
                     s1 += __shfl_xor_sync(0xffffffffu, s1, 16);
-                    const float x0 = t8 >= lo ? s0 * scale_log2 : -INFINITY;
-                    const float x1 = t8 + 8 >= lo ? s1 * scale_log2 : -INFINITY;
+                    const float sl = Rows::kScored ? slope[kSlopes ? h : 0] : 0.f;
+                    const float x0 = rows.score(s0, t8, sl);
+                    const float x1 = rows.score(s1, t8 + 8, sl);
                     float mx = fmaxf(x0, x1);
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -1579,6 +1777,9 @@ struct WarpAttnF32 {
                         ld_shared_v2(at, w);
                         v2[0] = pack_f2(__uint_as_float(w[0]), __uint_as_float(w[1]));
                     }
+                    if constexpr (Rows::kScored) {
+                        if (!rows.seen(t)) v2[0] = v2[kDims / 2 - 1] = 0;
+                    }
 #pragma unroll
                     for (int k = 0; k < kHG; ++k) {
                         if (hg + k < g) {
@@ -1623,7 +1824,7 @@ struct WarpAttnF32 {
 // warps of a team (each takes half the heads on the same staged tiles): a block's
 // CUDA-core work is halved, and each team alternates between two stages, so a warp's
 // next block is in flight while it computes.
-template <int D, int GMAX, int NSTAGE, int NCW>
+template <int D, int GMAX, int NSTAGE, int NCW, int FORM = kWhole>
 __global__ void __launch_bounds__((NCW + 1) * 32, GMAX >= 16 ? 1 : (GMAX >= 8 ? 2 : 3))
     decode_f32_staged_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                              const DecodeParams p) {
@@ -1635,8 +1836,8 @@ __global__ void __launch_bounds__((NCW + 1) * 32, GMAX >= 16 ? 1 : (GMAX >= 8 ? 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = p.group;
     const int len = seq_len(p, s, tid == 0 && part == 0 && h == 0);
-    const int nblk = (len + kBlock - 1) / kBlock;
-    const int npart = (nblk + p.part_blocks - 1) / p.part_blocks;
+    const int nblk = (len + kBlock - 1) / kBlock, first = first_block<FORM>(p, s, len);
+    const int npart = (nblk - first + p.part_blocks - 1) / p.part_blocks;
     float *out = static_cast<float *>(p.out);
 
     if (len == 0) {  // empty context: zero output rows
@@ -1648,9 +1849,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32, GMAX >= 16 ? 1 : (GMAX >= 8 ? 
     }
     if (part >= npart) return;
 
-    const int b_begin = part * p.part_blocks;
+    const int b_begin = first + part * p.part_blocks;
     const int nb = min(nblk - b_begin, p.part_blocks);
-    const int last_valid = len - (nblk - 1) * kBlock;  // tokens in the sequence's last block
+    // tokens in the sequence's last block, which is loaded early (with transformed scores in place: all its rows)
+    const int last_valid = FORM == kScored ? kBlock : len - (nblk - 1) * kBlock;
 
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(base + C::kBarOffset);
@@ -1684,9 +1886,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32, GMAX >= 16 ? 1 : (GMAX >= 8 ? 
     const int team = warp / C::kSplit, mem = warp % C::kSplit;
     const int h0 = mem * GW;
     const int nh = min(GW, g - h0);
-    WarpAttnF32<D, GW> wa;
+    WarpAttnF32<D, GW, FORM == kScored> wa;
     wa.init(smem_u32(base + C::kQOffset + h0 * C::kQRow), smem_u32(base + C::kPOffset + warp * C::kPBytes), nh);
     wa.reset();
+    if constexpr (FORM == kScored) wa.load_slopes(p.slopes ? p.slopes + h * g + h0 : nullptr);
     const int last_in_range = (b_begin + nb - 1 == nblk - 1) ? nb - 1 : -1;
     for (int j = team; j < nb; j += C::kTeams) {
         const int st = j % NSTAGE;
@@ -1695,7 +1898,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32, GMAX >= 16 ? 1 : (GMAX >= 8 ? 
             break;
         }
         const uint32_t sk = smem_u32(base + st * C::kStage);
-        wa.block(sk, sk + C::kTile, j == last_in_range ? kBlock - last_valid : 0, p.scale_log2, lane);
+        if constexpr (FORM == kScored)
+            wa.block(sk, sk + C::kTile, scored_rows<true>(p, b_begin + j, len), lane);
+        else
+            wa.block(sk, sk + C::kTile, PlainRows{j == last_in_range ? kBlock - last_valid : 0, p.scale_log2}, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
     }
@@ -1774,7 +1980,7 @@ __device__ __forceinline__ void mma_tf32x3(float (&d)[4], const uint32_t (&ah)[4
 // fragments split once per CTA into shared memory; the softmax on the S^T fragments;
 // the weights through the warp's shared-memory slot into P^T fragments; then
 // O^T (D x 8 per n-tile) += V^T P^T with V^T fragments read element by element.
-template <int D, int GMAX>
+template <int D, int GMAX, bool kSlopes = false>
 struct WarpAttnTF32 {
     static constexpr int kNT = GMAX / 8;          // n-tiles of 8 query heads
     static constexpr int kKS = D / 8;             // k-steps of S^T = K Q^T
@@ -1786,6 +1992,14 @@ struct WarpAttnTF32 {
     float m[kNT][2], l[kNT][2];   // columns nt 8 + 2 t and + 1 (t = lane % 4); l over this lane's tokens
     float acc[kNT][kMT][4];       // O^T fragments: rows (dims) 16 mi + lane / 4 (+ 8), columns 2 t (+ 1)
     uint32_t q_s, p_s;
+    float slope[kSlopes ? kNT : 1][2];
+
+    __device__ __forceinline__ void load_slopes(const float *slopes, int g, int lane) {
+#pragma unroll
+        for (int nt = 0; nt < (kSlopes ? kNT : 1); ++nt)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) slope[nt][hh] = slope_log2(slopes, nt * 8 + 2 * (lane & 3) + hh, g);
+    }
 
     // All threads of the CTA: the group's q (g heads at qg, D floats each) as split B
     // fragments of S^T = K Q^T: entry (nt, ks, lane) holds hi and lo of q[head][8 ks + t]
@@ -1823,8 +2037,8 @@ struct WarpAttnTF32 {
         }
     }
 
-    // Rows below `lo` of the staged tiles are not tokens of the sequence (zero-filled by TMA).
-    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, int lo, float scale_log2, int lane) {
+    template <class Rows>
+    __device__ __forceinline__ void block(uint32_t sk, uint32_t sv, const Rows &rows, int lane) {
         const int gq = lane >> 2, t = lane & 3;
         // S^T = K Q^T
         float sacc[kNT][4];
@@ -1852,10 +2066,10 @@ struct WarpAttnTF32 {
         // online softmax per column; lane holds tokens gq, gq + 8 of columns 2 t, 2 t + 1
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
-            const float x00 = gq >= lo ? sacc[nt][0] * scale_log2 : -INFINITY;
-            const float x01 = gq >= lo ? sacc[nt][1] * scale_log2 : -INFINITY;
-            const float x10 = gq + 8 >= lo ? sacc[nt][2] * scale_log2 : -INFINITY;
-            const float x11 = gq + 8 >= lo ? sacc[nt][3] * scale_log2 : -INFINITY;
+            const float sl0 = Rows::kScored ? slope[kSlopes ? nt : 0][0] : 0.f;
+            const float sl1 = Rows::kScored ? slope[kSlopes ? nt : 0][1] : 0.f;
+            const float x00 = rows.score(sacc[nt][0], gq, sl0), x01 = rows.score(sacc[nt][1], gq, sl1);
+            const float x10 = rows.score(sacc[nt][2], gq + 8, sl0), x11 = rows.score(sacc[nt][3], gq + 8, sl1);
             float mx0 = fmaxf(x00, x10), mx1 = fmaxf(x01, x11);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
@@ -1915,6 +2129,10 @@ struct WarpAttnTF32 {
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[1]) : "r"(a1));
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[2]) : "r"(a2));
                 asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v[3]) : "r"(a3));
+                if constexpr (Rows::kScored) {
+                    if (!rows.seen(t0)) v[0] = v[1] = 0.f;
+                    if (!rows.seen(t1)) v[2] = v[3] = 0.f;
+                }
                 uint32_t ah[4], al[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) tf32_split(v[i], ah[i], al[i]);
@@ -1956,9 +2174,9 @@ struct WarpAttnTF32 {
     }
 };
 
-template <int D, int GMAX, int NSTAGE, int NCW>
+template <int D, int GMAX, int NSTAGE, int NCW, bool kSlopes = false>
 struct F32TcCfg {
-    using WA = WarpAttnTF32<D, GMAX>;
+    using WA = WarpAttnTF32<D, GMAX, kSlopes>;
     static constexpr int kTile = kBlock * D * 4;
     static constexpr int kStage = 2 * kTile;
     static constexpr int kThreads = (NCW + 1) * 32;
@@ -1973,19 +2191,19 @@ struct F32TcCfg {
     static_assert(kQOffset % 16 == 0 && WA::kPBytes % 16 == 0, "16-byte aligned areas");
 };
 
-template <int D, int GMAX, int NSTAGE, int NCW>
+template <int D, int GMAX, int NSTAGE, int NCW, int FORM = kWhole>
 __global__ void __launch_bounds__((NCW + 1) * 32)
     decode_f32_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                          const DecodeParams p) {
-    using C = F32TcCfg<D, GMAX, NSTAGE, NCW>;
+    using C = F32TcCfg<D, GMAX, NSTAGE, NCW, FORM == kScored>;
     extern __shared__ uint8_t smem_raw[];
 
     const int part = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = p.group;
     const int len = seq_len(p, s, tid == 0 && part == 0 && h == 0);
-    const int nblk = (len + kBlock - 1) / kBlock;
-    const int npart = (nblk + p.part_blocks - 1) / p.part_blocks;
+    const int nblk = (len + kBlock - 1) / kBlock, first = first_block<FORM>(p, s, len);
+    const int npart = (nblk - first + p.part_blocks - 1) / p.part_blocks;
     float *out = static_cast<float *>(p.out);
 
     if (len == 0) {  // empty context: zero output rows
@@ -1997,9 +2215,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
     }
     if (part >= npart) return;
 
-    const int b_begin = part * p.part_blocks;
+    const int b_begin = first + part * p.part_blocks;
     const int nb = min(nblk - b_begin, p.part_blocks);
-    const int last_valid = len - (nblk - 1) * kBlock;  // tokens in the sequence's last block
+    // tokens in the sequence's last block, which is loaded early (with transformed scores in place: all its rows)
+    const int last_valid = FORM == kScored ? kBlock : len - (nblk - 1) * kBlock;
 
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(base + C::kBarOffset);
@@ -2025,6 +2244,7 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
     typename C::WA wa;
     wa.init(smem_u32(base + C::kQOffset), smem_u32(base + C::kPOffset + warp * C::WA::kPBytes));
     wa.reset();
+    if constexpr (FORM == kScored) wa.load_slopes(p.slopes ? p.slopes + h * g : nullptr, g, lane);
     const int last_in_range = (b_begin + nb - 1 == nblk - 1) ? nb - 1 : -1;
     for (int j = warp; j < nb; j += NCW) {
         const int st = j % NSTAGE;
@@ -2033,7 +2253,10 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
             break;
         }
         const uint32_t sk = smem_u32(base + st * C::kStage);
-        wa.block(sk, sk + C::kTile, j == last_in_range ? kBlock - last_valid : 0, p.scale_log2, lane);
+        if constexpr (FORM == kScored)
+            wa.block(sk, sk + C::kTile, scored_rows<true>(p, b_begin + j, len), lane);
+        else
+            wa.block(sk, sk + C::kTile, PlainRows{j == last_in_range ? kBlock - last_valid : 0, p.scale_log2}, lane);
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[st]);
     }
@@ -2078,14 +2301,14 @@ __global__ void __launch_bounds__((NCW + 1) * 32)
 // Sequences with a single partition were written by K1 and are skipped.
 // =====================================================================================
 
-template <typename OutT, int D, int PG>
+template <typename OutT, int D, int PG, int FORM = kWhole>
 __global__ void __launch_bounds__(D *PG) lse_reduce_kernel(const DecodeParams p) {
     // PG groups of D threads: group k sums partitions k, k + PG, ...
     extern __shared__ float rsm[];  // [32] scratch, [PG][D] group sums, [max_parts] weights
     const int hq = blockIdx.x, s = blockIdx.y, tid = threadIdx.x;
     const int d = tid % D, grp = tid / D;
     const int len = seq_len(p, s, false);
-    const int nblk = (len + kBlock - 1) / kBlock;
+    const int nblk = (len + kBlock - 1) / kBlock - first_block<FORM>(p, s, len);
     const int npart = (nblk + p.part_blocks - 1) / p.part_blocks;
     if (npart <= 1) return;
     const size_t row = (size_t)s * p.num_q_heads + hq;

@@ -502,6 +502,18 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
     return check_launch();
 }
 
+int paged_decode_attention_scored(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                  const int32_t *block_tables, const int32_t *context_lens, float scale, float softcap,
+                                  int window, const float *slopes, int num_kv_heads, int num_seqs, int num_q_heads,
+                                  int head_dim, int max_blocks_per_seq, int num_blocks, int max_context_len,
+                                  pkv_dtype dtype, int partition_tokens, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    const ScoreArgs scores{softcap, window, slopes};
+    return decode_dispatch(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, num_seqs,
+                           num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len, dtype,
+                           partition_tokens, workspace, workspace_bytes, stream, kLaunch, &scores);
+}
+
 int verify_drafts(int32_t *accepted, int max_accepted, int32_t *num_accepted, int64_t *next_tokens,
                   const int64_t *tokens, const int32_t *parents, const int32_t *query_start, const void *target_probs,
                   int64_t target_stride, const void *draft_probs, int64_t draft_stride, const float *uniforms,
