@@ -653,6 +653,31 @@ int paged_decode_attention_scored(void *out, const void *q, const void *k_cache,
                                   void *stream);
 
 /*
+ * paged_prefill_attention with transformed scores, for a prompt or a chunk: the
+ * row at position pos sees position t of its sequence if
+ *   t <= pos, or t < prefix_lens[s] (a prefix that is seen from both sides),
+ *   and, with window > 0, |pos - t| < window;
+ * scores are capped as by paged_decode_attention_scored, then biased by
+ * -slopes[hq] |pos - t|. A chain of drafts behind a context is such a chunk.
+ * prefix_lens: int32 [num_seqs], device (NULL: none); at most the context counts,
+ *   a negative one counts as 0 and raises PKV_DEVERR_LENGTH. The prefix' keys
+ *   have to be in the cache when a row that sees them is attended: put a prefix
+ *   into one chunk.
+ * Blocks that lie wholly before what a sequence's first row of a call sees are
+ * not read. A key or value that is not finite shows in the rows that see it, and in no other.
+ * Weights are rounded to bf16 for the tensor cores, to 16 bits in tiles of rows
+ * with one that sees less than 64 keys, and with slopes around the rows' positions.
+ * Every other argument and error as for paged_prefill_attention.
+ */
+int paged_prefill_attention_scored(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_tables, const int32_t *context_lens,
+                                   const int32_t *query_start, float scale, float softcap, int window,
+                                   const float *slopes, const int32_t *prefix_lens, int num_kv_heads, int num_seqs,
+                                   int num_q_heads, int head_dim, int max_blocks_per_seq, int num_blocks,
+                                   int num_queries, int max_query_len, int max_context_len, pkv_dtype dtype,
+                                   void *stream);
+
+/*
  * Between paged_tree_attention and kv_accept_layers: which drafts stand, and the
  * token that follows, so that the tokens are distributed as if the target
  * had drawn each by itself. Random numbers are inputs.

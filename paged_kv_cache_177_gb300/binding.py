@@ -83,6 +83,8 @@ _tree_ws = _decl("pkv_tree_workspace_bytes", _sz, _i, _i, _i, _i, _i, _i)
 _accept = _decl("kv_accept_layers", _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp)
 _scored = _decl("paged_decode_attention_scored", _i, _vp, _vp, _vp, _vp, _vp, _vp, _f, _f, _i, _vp, _i, _i, _i, _i, _i,
                 _i, _i, _i, _i, _vp, _sz, _vp)
+_prefill_scored = _decl("paged_prefill_attention_scored", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _f, _i, _vp, _vp, _i,
+                        _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp)
 _verify = _decl("verify_drafts", _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _i,
                 _vp)
 _device_error = _decl("pkv_device_error", _i, ctypes.POINTER(ctypes.c_uint32), _i)
@@ -997,6 +999,51 @@ def paged_decode_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: t
             v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale), float(softcap),
             int(window), _slopes(slopes, Hq, dev), Hkv, S, Hq, D, max_blocks, NB, max_context_len, dt,
             int(partition_tokens), ws, ws_bytes)
+    return out
+
+
+def paged_prefill_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                   block_tables: torch.Tensor, context_lens: torch.Tensor, query_start: torch.Tensor,
+                                   scale: float, *, softcap: float = 0.0, window: int = 0,
+                                   slopes: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None,
+                                   max_query_len: Optional[int] = None, max_context_len: Optional[int] = None,
+                                   stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_prefill_attention with transformed scores (as for
+    ``paged_decode_attention_scored``): the row at position p sees t <= p, and
+    t < prefix_lens[s] (int32 [S]; None: no prefix) from either side, both
+    within ``window`` (|p - t| < window; 0: all); see include/pagedkv.h.
+
+    bf16; q, out [T, Hq, D], sequence s owning rows query_start[s] ..
+    query_start[s+1]-1, its last tokens, already in the cache.
+    ``max_query_len`` and ``max_context_len`` default to the maxima of the
+    device arrays (a sync)."""
+    dev = _index(out, q, k_cache, v_cache, block_tables, context_lens, query_start)
+    if q.dtype != torch.bfloat16 or not (out.dtype == k_cache.dtype == v_cache.dtype == torch.bfloat16):
+        raise TypeError("prefill attention is bf16")
+    if not (query_start.dtype == context_lens.dtype == block_tables.dtype == torch.int32):
+        raise TypeError("query_start, context_lens and block_tables are int32")
+    shape, cache, tables = q.shape, k_cache.shape, block_tables.shape
+    if len(shape) != 3 or out.shape != shape or len(cache) != 4 or cache[2] != BLOCK_SIZE or cache[3] != shape[2] \
+            or v_cache.shape != cache:
+        raise ValueError("expected q, out [T, Hq, D] and caches [NB, Hkv, 16, D]")
+    if context_lens.dim() != 1:
+        raise ValueError("context_lens must be [S]")
+    S = context_lens.shape[0]
+    if query_start.shape != (S + 1,) or len(tables) != 2 or tables[0] != S:
+        raise ValueError("query_start must be [S + 1] and block_tables [S, maxB]")
+    if prefix_lens is not None and (prefix_lens.dtype != torch.int32 or prefix_lens.shape != (S,)
+                                    or _index(prefix_lens) != dev):
+        raise TypeError("prefix_lens must be int32 [S] on the caches' device")
+    T, Hq, D = shape
+    if max_query_len is None:
+        max_query_len = int((query_start[1:] - query_start[:-1]).max().item()) if S else 0
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    _launch(_prefill_scored, "paged_prefill_attention_scored", dev, stream, out.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
+            query_start.data_ptr(), float(scale), float(softcap), int(window), _slopes(slopes, Hq, dev),
+            _p(prefix_lens), cache[1], S, Hq, D, tables[1] if S else 1, cache[0], T, int(max_query_len),
+            int(max_context_len), PKV_BF16)
     return out
 
 

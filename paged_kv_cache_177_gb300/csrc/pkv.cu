@@ -19,6 +19,7 @@
 #include "pkv_e4m3.cuh"
 #include "pkv_rope.cuh"
 #include "pkv_tree.cuh"
+#include "pkv_prefill_scored.cuh"
 #include "pkv_verify.cuh"
 
 namespace {

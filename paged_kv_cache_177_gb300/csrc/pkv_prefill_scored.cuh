@@ -1,0 +1,565 @@
+// pkv_prefill_scored.cuh -- prefill attention with transformed scores on the
+// 5th-generation tensor cores: scores capped by a tanh, biased by distance, cut
+// to a window, over a prefix that is seen from both sides.
+#pragma once
+
+#include "pkv_prefill_tc.cuh"
+
+namespace pkv {
+
+struct ScoredPrefillParams {
+    PrefillParams pp;
+    const int32_t *prefix_lens;  // [num_seqs] or null
+};
+
+// =====================================================================================
+// The query at position pos sees t if (t <= pos or t < prefix) and |pos - t| < window: one interval
+// [lo, hi] that holds pos and moves up with it, so a 128-row tile needs the chunks of 128 keys from its first row's
+// lo to its last row's hi, and a chunk that lies within all rows' intervals needs no mask.
+//
+// Roles and pipelines are those of prefill_tc_kernel (a CTA per pair of 128-row tiles, K and V chunks in two-stage
+// rings, S and P in the same tensor-memory columns, warpgroups of 128 threads for a tile's softmax). What differs:
+//  - each tile has its own first and last chunk; the pair walks their union, in which there is no gap;
+//  - a warp cleans values: a row that does not see a key must not meet its NaN or infinity (0 times either is NaN),
+//    so in chunks that not every row sees whole such elements are zeroed before P V, and added at the end,
+//    element by element, to the rows that see them;
+//  - the scores are transformed between S and the softmax:
+//    chunks without a mask in registers, S' = raw Q(raw^2) with Q the polynomial of cap tanh(y) / raw (y = raw scale /
+//    cap) for |y| <= 3/4, 5.7e-7 of the score off. tanh by exponentials takes two more instructions a score on the
+//    special-function unit, where a chunk's exponentials alone take as long as its products; so only where a warp
+//    holds a larger score, and in masked chunks, are the scores taken that way, rewritten in tensor memory by a
+//    rolled loop.
+//  - Weights come with their rounding remainders (a second P V) where a row may see few keys or give few all of
+//    its weight: tiles with rows that see less than 64 keys, and with a bias by distance the chunks next to the tile's
+//    positions and the first.
+// =====================================================================================
+constexpr float kCapNear = 0.75f;
+// tanh(y) / y = sum c_k y^2k, fitted on [0, kCapNear] (relative error 5.7e-7)
+constexpr float kTanh0 = 0.999999435f, kTanh1 = -0.333282515f, kTanh2 = 0.132589832f, kTanh3 = -0.0500563012f,
+                kTanh4 = 0.0129296311f;
+
+struct ScoredBars {
+    uint64_t q_full;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2];
+    uint64_t s_full[2], p_full[2], o_done[2];  // per query tile
+    uint64_t drain;
+    uint32_t tmem_base;
+    int any_bad;  // a value was not finite, and was zeroed
+};
+static_assert(sizeof(ScoredBars) <= 256, "barrier area");
+
+// What a sequence's rows see.
+struct Sight {
+    int window, prefix;
+    __device__ __forceinline__ int lo(int pos) const { return max(0, pos - window + 1); }
+    __device__ __forceinline__ int hi(int pos) const {
+        return min(max(pos, prefix - 1), pos - 1 + min(window, INT_MAX - pos));
+    }
+};
+
+// One query tile: tokens t0 .. t_end - 1, chunks c0 .. c1 - 1, positions first .. last.
+struct ScoredTile {
+    int t0, t_end, c0, c1, first, last;
+    // whether all rows see all of chunk j (128 keys), which lies before the sequence's last block
+    __device__ __forceinline__ bool whole(const Sight &see, int j, int nblk) const {
+        return (j + 1) * 8 < nblk && j * 128 >= see.lo(last) && j * 128 + 127 <= see.hi(first);
+    }
+    // whether its weights come with their remainders
+    __device__ __forceinline__ bool split(const Sight &see, bool bias, int j) const {
+        // (what a row sees grows with its position up to the window, and falls where the prefix' end stays ahead of it)
+        const bool few = min(see.hi(first) - see.lo(first), see.hi(last) - see.lo(last)) < 63;
+        return few || (bias && (j == c0 || (j >= first / 128 - 1 && j <= last / 128 + 1)));
+    }
+};
+
+// Adds the values at positions [from, to] of a sequence that are not finite to a row that this thread has written. Not in
+// line: it is seldom called.
+__device__ __noinline__ void scored_add_zeroed(const DecodeParams &p, int s, int h, int from, int to, int head_dim,
+                                               __nv_bfloat16 *dst) {
+#pragma unroll 1
+    for (int ps = from; ps <= to; ++ps) {
+        const int pb = __ldg(p.block_tables + (size_t)s * p.max_blocks_per_seq + ps / kBlock);
+        if (pb < 0 || pb >= p.num_blocks) continue;
+        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(p.v_cache) +
+                                 (((size_t)pb * p.num_kv_heads + h) * kBlock + ps % kBlock) * head_dim;
+#pragma unroll 1
+        for (int c = 0; c < head_dim; ++c) {
+            const float x = __bfloat162float(v[c]);
+            if (!(fabsf(x) < INFINITY)) dst[c] = __float2bfloat16_rn(__bfloat162float(dst[c]) + x);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
+    prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                          const __grid_constant__ CUtensorMap tmv, const ScoredPrefillParams sp) {
+    using C = TcCfg<D>;
+    const PrefillParams &pp = sp.pp;
+    const DecodeParams &p = pp.d;
+    extern __shared__ uint8_t smem_raw[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x;
+    int s, pair;
+    if (pp.seq_major) {
+        pair = gridDim.y - 1 - blockIdx.y;
+        s = prefill_sequence_by_rank(pp, blockIdx.z, tid);
+    } else {
+        s = blockIdx.y;
+        pair = gridDim.z - 1 - blockIdx.z;
+    }
+    const bool flagger = h == 0 && pair == 0;  // one CTA per sequence reports bad lengths
+    const int g = p.group;
+    const int q0 = __ldg(pp.query_start + s);
+    const long long nn = (long long)__ldg(pp.query_start + s + 1) - q0;
+    const int len = seq_len(p, s, tid == 0 && flagger);
+    const int tt = pp.tile_tokens;
+    Sight see{p.window, sp.prefix_lens ? __ldg(sp.prefix_lens + s) : 0};
+    if (see.prefix < 0 && tid == 0 && flagger) raise_error(PKV_DEVERR_LENGTH);
+    see.prefix = min(max(see.prefix, 0), len);
+    if (nn < 0 || nn > len || nn > pp.max_query_len || q0 < 0 || q0 + nn > pp.num_queries) {
+        if (tid == 0 && flagger) raise_error(PKV_DEVERR_LENGTH);
+        return;
+    }
+    const int n = (int)nn;
+    if (pair * C::kTiles * tt >= n) return;
+    const int first_pos = len - n;  // position of new token 0
+    ScoredTile tl[C::kTiles];
+#pragma unroll
+    for (int t = 0; t < C::kTiles; ++t) {
+        ScoredTile &x = tl[t];
+        x.t0 = (pair * C::kTiles + t) * tt;
+        x.t_end = min(n, x.t0 + tt);
+        x.first = first_pos + x.t0;
+        x.last = first_pos + x.t_end - 1;
+        if (x.t0 < n) {
+            x.c0 = see.lo(x.first) / C::kKeys;
+            x.c1 = see.hi(x.last) / C::kKeys + 1;
+        } else {
+            x.c0 = x.c1 = tl[0].c1;  // (an empty second tile)
+        }
+    }
+    const int j0 = tl[0].c0, j1 = max(tl[0].c1, tl[1].c1);
+    const int nblk = (len + kBlock - 1) / kBlock;
+    const int last_valid = len - (nblk - 1) * kBlock;
+    const int first_blk = see.lo(tl[0].first) / kBlock;  // blocks before it are not read
+
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    ScoredBars &b = *reinterpret_cast<ScoredBars *>(base + C::kBarOff);
+    if (tid == 0) {
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+        mbar_init(&b.q_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.k_full[i], 1);
+            mbar_init(&b.k_empty[i], 1);
+            mbar_init(&b.v_full[i], 1);
+            mbar_init(&b.v_empty[i], 1);
+            mbar_init(&b.v_clean[i], 1);
+            mbar_init(&b.s_full[i], 1);
+            mbar_init(&b.p_full[i], 4);
+            mbar_init(&b.o_done[i], 1);
+        }
+        mbar_init(&b.drain, 1);
+        b.any_bad = 0;
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&b.tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem_base;
+    const uint32_t q_s = smem_u32(base + C::kQOff), k_s = smem_u32(base + C::kKOff);
+    const uint32_t v_s = smem_u32(base + C::kVOff);
+    auto active = [&](int t, int j) { return j >= tl[t].c0 && j < tl[t].c1; };
+    const bool bias = p.slopes != nullptr;
+
+    if (warp < 4) {
+      setmaxnreg_dec<C::kLowRegs>();
+      if (warp == 0) {
+        // ------------------------------ TMA producer ------------------------------
+        if (lane == 0) {
+            bool ok = true;
+            int qbytes = 0;
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t) qbytes += tl[t].t0 < n ? C::kHalves * 128 * g * tt : 0;
+            mbar_arrive_expect_tx(&b.q_full, qbytes);
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t)
+                if (tl[t].t0 < n)
+                    for (int u = 0; u < C::kHalves; ++u)
+                        tma_load_4d(base + C::kQOff + t * C::kQBytes + u * C::kHalfRows, &tmq, 0, u, h * g,
+                                    q0 + tl[t].t0, &b.q_full);
+            const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+            int issued_k = 0, issued_v = 0;  // chunks whose K / V copies were issued
+            for (int j = j0; j < j1 && ok; ++j) {
+                const int r = j - j0, st = r & 1;
+                if (r >= 2 && !mbar_wait(&b.k_empty[st], ((r - 2) >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                // the chunk's blocks: tile row z of the cache view (-1, outside the tensor, reads as zeros: not
+                // seen by any row, past the sequence, or a bad id) and first slot y
+                int z[C::kChunkBlocks], y[C::kChunkBlocks];
+#pragma unroll
+                for (int bi = 0; bi < C::kChunkBlocks; ++bi) {
+                    const int blk = j * C::kChunkBlocks + bi;
+                    z[bi] = blk >= first_blk && blk < nblk ? __ldg(table + blk) : -1;
+                }
+#pragma unroll
+                for (int bi = 0; bi < C::kChunkBlocks; ++bi) {
+                    const int blk = j * C::kChunkBlocks + bi;
+                    y[bi] = blk == nblk - 1 ? last_valid - kBlock : 0;
+                    if (blk >= first_blk && blk < nblk) {
+                        if (z[bi] < 0 || z[bi] >= p.num_blocks) {
+                            raise_error(PKV_DEVERR_BLOCK_ID);
+                            z[bi] = -1;
+                        } else {
+                            z[bi] = z[bi] * p.num_kv_heads + h;
+                        }
+                    }
+                }
+                // K chunk as [half][128 keys][64]: 8-row groups 1024 bytes apart along the keys
+                mbar_arrive_expect_tx(&b.k_full[st], C::kStage);
+#pragma unroll
+                for (int bi = 0; bi < C::kChunkBlocks; ++bi)
+#pragma unroll
+                    for (int u = 0; u < C::kHalves; ++u)
+                        tma_load_4d(base + C::kKOff + st * C::kStage + u * C::kHalfRows + bi * (kBlock * 128), &tmk,
+                                    0, y[bi], u, z[bi], &b.k_full[st]);
+                issued_k = r + 1;
+                if (r >= 2 && !mbar_wait(&b.v_empty[st], ((r - 2) >> 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                // V chunk as [block][half][16 keys][64]
+                mbar_arrive_expect_tx(&b.v_full[st], C::kStage);
+#pragma unroll
+                for (int bi = 0; bi < C::kChunkBlocks; ++bi)
+                    tma_load_4d(base + C::kVOff + st * C::kStage + bi * C::kBlockBytes, &tmv, 0, y[bi], 0, z[bi],
+                                &b.v_full[st]);
+                issued_v = r + 1;
+            }
+            if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+            // no copy may land after the CTA is gone: wait (bounded) for the last one of each stage
+            for (int r = max(0, issued_k - 2); r < issued_k; ++r) mbar_wait(&b.k_full[r & 1], (r >> 1) & 1);
+            for (int r = max(0, issued_v - 2); r < issued_v; ++r) mbar_wait(&b.v_full[r & 1], (r >> 1) & 1);
+            mbar_wait(&b.q_full, 0);
+        }
+      } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16_f32(C::kRows, C::kKeys, false, false);
+            constexpr uint32_t idesc_o = idesc_bf16_f32(C::kRows, D, false, true);
+            auto issue_s = [&](int t, int r) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {  // 16 head-dim elements per step
+                    const uint32_t off = (kk >> 2) * C::kHalfRows + (kk & 3) * 32;
+                    umma_bf16(tmem + t * C::kTileCols, smem_desc_sw128(q_s + t * C::kQBytes + off, 16, 1024),
+                              smem_desc_sw128(k_s + (r & 1) * C::kStage + off, 16, 1024), idesc_s, kk > 0);
+                }
+            };
+            auto issue_pv = [&](int t, int r, bool start, bool split) {
+#pragma unroll
+                for (int kk = 0; kk < C::kChunkBlocks; ++kk) {  // 16 keys (one block) per step
+                    const uint64_t vd =
+                        smem_desc_sw128(v_s + (r & 1) * C::kStage + kk * C::kBlockBytes, kBlock * 128, 1024);
+                    // P of keys 16 kk .. 16 kk + 15: columns 32 (kk / 2) + 8 (kk % 2); remainder 16 further
+                    const uint32_t pa = tmem + t * C::kTileCols + (kk >> 1) * 32 + (kk & 1) * 8;
+                    umma_bf16_tmem_a(tmem + t * C::kTileCols + C::kOCol, pa, vd, idesc_o, !start || kk > 0);
+                    if (split) umma_bf16_tmem_a(tmem + t * C::kTileCols + C::kOCol, pa + 16, vd, idesc_o, true);
+                }
+            };
+            bool ok = mbar_wait(&b.q_full, 0) && mbar_wait(&b.k_full[0], 0);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t)
+                    if (active(t, j0)) {
+                        issue_s(t, 0);
+                        umma_commit(&b.s_full[t]);
+                    }
+                umma_commit(&b.k_empty[0]);
+            }
+            for (int j = j0; ok && j < j1; ++j) {
+                const int r = j - j0;
+                ok = mbar_wait(&b.v_clean[r & 1], (r >> 1) & 1);
+                if (ok && j + 1 < j1) ok = mbar_wait(&b.k_full[(r + 1) & 1], ((r + 1) >> 1) & 1);
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < C::kTiles; ++t) {
+                    const bool now = active(t, j), next = active(t, j + 1);
+                    if (now) {
+                        if (!(ok = mbar_wait(&b.p_full[t], (j - tl[t].c0) & 1))) break;
+                        tc_fence_after();
+                        issue_pv(t, r, j == tl[t].c0, tl[t].split(see, bias, j));
+                        if (!next) umma_commit(&b.o_done[t]);
+                    }
+                    if (next) {
+                        tc_fence_after();
+                        issue_s(t, r + 1);
+                        umma_commit(&b.s_full[t]);
+                    }
+                }
+                if (!ok) break;
+                umma_commit(&b.v_empty[r & 1]);
+                if (j + 1 < j1) umma_commit(&b.k_empty[(r + 1) & 1]);
+            }
+            if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+            // every MMA issued has finished before the tensor memory is released
+            umma_commit(&b.drain);
+            mbar_wait(&b.drain, 0);
+        }
+        __syncwarp();
+      } else if (warp == 2) {
+        // ------------------------------ values that not every row sees ------------------------------
+        bool ok = true;
+        for (int j = j0; j < j1 && ok; ++j) {
+            const int r = j - j0, st = r & 1;
+            if (!(ok = warp_wait(&b.v_full[st], (r >> 1) & 1))) break;
+            bool clean = false;
+#pragma unroll
+            for (int t = 0; t < C::kTiles; ++t)
+                clean |= active(t, j) && (!tl[t].whole(see, j, nblk) || tl[t].split(see, bias, j));
+            if (clean) {
+                uint8_t *vst = base + C::kVOff + st * C::kStage;
+                for (int i = lane; i < C::kStage / 16; i += 32) {
+                    const uint4 v = reinterpret_cast<const uint4 *>(vst)[i];
+                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t keep[4];
+                    bool bad = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        keep[e] = ((x[e] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
+                                  ((x[e] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
+                        bad |= keep[e] != ~0u;
+                    }
+                    if (bad) {
+                        reinterpret_cast<uint4 *>(vst)[i] =
+                            make_uint4(x[0] & keep[0], x[1] & keep[1], x[2] & keep[2], x[3] & keep[3]);
+                        *reinterpret_cast<volatile int *>(&b.any_bad) = 1;
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.v_clean[st]);
+        }
+        if (!ok && lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
+      }
+    } else {
+        setmaxnreg_inc<C::kHighRegs>();
+        // ------------------------------ softmax ------------------------------
+        const int t = (warp - 4) >> 2;  // query tile
+        const int quad = warp & 3;       // tensor-memory lanes 32 quad .. 32 quad + 31
+        const int row = quad * 32 + lane;
+        static_assert(C::kTiles == 2, "tile selection below");
+        const ScoredTile me = {t ? tl[1].t0 : tl[0].t0, t ? tl[1].t_end : tl[0].t_end, t ? tl[1].c0 : tl[0].c0,
+                               t ? tl[1].c1 : tl[0].c1, t ? tl[1].first : tl[0].first, t ? tl[1].last : tl[0].last};
+        const int rows = me.t0 < n ? (me.t_end - me.t0) * g : 0;
+        const bool row_ok = row < rows;
+        const int row_token = row / g, row_head = row - row_token * g;
+        const int pos = me.first + (row_ok ? row_token : 0);
+        const int lo_t = see.lo(pos), hi_t = see.hi(pos);  // (rows past the tile's end see what its first does)
+        const uint32_t cols = tmem + ((uint32_t)(quad * 32) << 16) + t * C::kTileCols;
+        const float slope = slope_log2(p.slopes, h * g + row_head, p.num_q_heads);
+        const bool cap = p.cap_log2 != 0.f;
+        // the polynomial's coefficients in powers of the raw score, and up to where it holds
+        const float ci2 = p.cap_in * p.cap_in;
+        const float near_max = cap ? kCapNear / fabsf(p.cap_in) : INFINITY;
+        const float k0 = cap ? p.scale_log2 * kTanh0 : p.scale_log2, k1 = p.scale_log2 * kTanh1 * ci2;
+        const float k2 = p.scale_log2 * kTanh2 * ci2 * ci2, k3 = p.scale_log2 * kTanh3 * ci2 * ci2 * ci2;
+        const float k4 = p.scale_log2 * kTanh4 * ci2 * ci2 * ci2 * ci2;
+        // (constants past fp32 where the cap is tiny: every score is taken the long way)
+        const bool poly = !cap || fabsf(k4) < INFINITY;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = me.c0; j < me.c1; ++j) {
+            if (!(ok = warp_wait(&b.s_full[t], (j - me.c0) & 1))) break;
+            tc_fence_after();
+            const bool whole = me.whole(see, j, nblk);
+            // the whole row of S_t in registers (one tensor-memory round trip)
+            float x[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(cols + q * 32, x[q]);
+            tmem_wait_ld();
+            bool far = !whole || !poly || (bias && j * C::kKeys + C::kKeys - 1 > me.first);
+            if (!far && cap) {
+                float big = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) big = max3f(big, fabsf(x[q][e]), fabsf(x[q][e + 1]));
+                far = __any_sync(0xffffffffu, !(big <= near_max));
+            }
+            if (far) {
+                // S rewritten: the scores in the log2 domain, -inf where the row does not see. Column kc of a full
+                // block holds position 128 j + kc; in the chunk with the sequence's last block (index lb, loaded lo
+                // rows early) column kc >= 16 lb holds position 128 j + kc - lo and is a token from 16 lb + lo on.
+                const int c0 = j * C::kKeys, lb = nblk - 1 - j * C::kChunkBlocks;
+                const int cut = lb < C::kChunkBlocks ? lb * kBlock : C::kKeys, early = kBlock - last_valid;
+                const int a0 = lo_t - c0, a1 = min(hi_t - c0, cut - 1);
+                const int b0 = max(cut, lo_t - c0) + early, b1 = hi_t - c0 + early;
+                const float at = (float)(pos - c0);
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    float v[32];
+                    tmem_ld32(cols + q * 32, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int kc = q * 32 + e;
+                        float y = cap ? capped(v[e], p.cap_in, p.cap_log2) : v[e] * p.scale_log2;
+                        y = fmaf(-slope, fabsf(at - (kc >= cut ? kc - early : kc)), y);
+                        v[e] = (kc >= a0 && kc <= a1) || (kc >= b0 && kc <= b1) ? y : -INFINITY;
+                    }
+                    tmem_st32(cols + q * 32, v);
+                }
+                tmem_wait_st();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(cols + q * 32, x[q]);
+                tmem_wait_ld();
+            } else {
+                const uint64_t c0 = pack_f2(k0, k0), c1 = pack_f2(k1, k1), c2 = pack_f2(k2, k2), c3 = pack_f2(k3, k3);
+                const uint64_t c4 = pack_f2(k4, k4), zero = pack_f2(0.f, 0.f);
+                // the bias of columns 2 i, 2 i + 1 is slope (position - pos)
+                const float at = (float)(j * C::kKeys - pos) * slope;
+                const uint64_t at2 = pack_f2(at, at), slope2 = pack_f2(slope, slope), two = pack_f2(2.f, 2.f);
+                uint64_t col = pack_f2(0.f, 1.f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const uint64_t r = pack_f2(x[q][e], x[q][e + 1]);
+                        uint64_t f = c0;
+                        if (cap) {
+                            const uint64_t r2 = fma_f2(r, r, zero);
+                            f = fma_f2(fma_f2(fma_f2(fma_f2(c4, r2, c3), r2, c2), r2, c1), r2, c0);
+                        }
+                        unpack_f2(fma_f2(r, f, bias ? fma_f2(col, slope2, at2) : zero), x[q][e], x[q][e + 1]);
+                        if (bias) col = add_f2(col, two);
+                    }
+            }
+            float mxs[8];  // independent partial maxima (a single chain would be 128 dependent steps)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) mxs[i] = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) mxs[(e >> 1) & 7] = max3f(mxs[(e >> 1) & 7], x[q][e], x[q][e + 1]);
+            const float mx = fmaxf(fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3])),
+                                   fmaxf(fmaxf(mxs[4], mxs[5]), fmaxf(mxs[6], mxs[7])));
+            const float m_new = fmaxf(m, mx);
+            const bool move = m_new > m + 8.f;
+            const float m_use = move ? m_new : m;
+            const float ms = m_use == -INFINITY ? 0.f : m_use;
+            const float alpha = ex2_approx(m - ms);
+            // this tile's O is quiescent here (P V of the previous chunk ran before S of this one)
+            if (j > me.c0 && __any_sync(0xffffffffu, move && m != -INFINITY)) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(cols + C::kOCol + c * 32, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                    tmem_st32(cols + C::kOCol + c * 32, o);
+                }
+            }
+            m = m_use;
+            // P = 2^(x - reference max) in bf16 over each quarter's own score columns: keys 32 q + 2 i, + 1 at column
+            // 32 q + i, their rounding remainders at + 16. The row sum takes the unrounded weights.
+            auto write_p = [&](auto split_c) -> float {
+                constexpr bool split = decltype(split_c)::value;
+                const uint64_t nms2 = pack_f2(-ms, -ms);
+                uint64_t rss[4];  // independent partial sums, two lanes each
+#pragma unroll
+                for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t hi[16], rem[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float e0, e1;
+                        unpack_f2(add_f2(pack_f2(x[q][2 * i], x[q][2 * i + 1]), nms2), e0, e1);
+                        e0 = ex2_approx(e0);
+                        e1 = ex2_approx(e1);
+                        rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
+                        const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
+                        hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
+                        if constexpr (split) {
+                            const float2 fh = __bfloat1622float2(ph);
+                            const __nv_bfloat162 pl = __floats2bfloat162_rn(e0 - fh.x, e1 - fh.y);
+                            rem[i] = *reinterpret_cast<const uint32_t *>(&pl);
+                        }
+                    }
+                    tmem_st16(cols + q * 32, hi);
+                    if constexpr (split) tmem_st16(cols + q * 32 + 16, rem);
+                }
+                tmem_wait_st();
+                float r[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) unpack_f2(rss[i], r[2 * i], r[2 * i + 1]);
+                return ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
+            };
+            const float rs = me.split(see, bias, j) ? write_p(BoolConst<true>{}) : write_p(BoolConst<false>{});
+            l = l * alpha + rs;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.p_full[t]);
+        }
+        if (me.t0 < n) {
+            if (ok) ok = warp_wait(&b.o_done[t], 0);
+            if (!ok) {
+                raise_error(PKV_DEVERR_TIMEOUT);
+            } else {
+                tc_fence_after();
+                const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
+                __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
+                                     ((size_t)(q0 + me.t0 + (row_ok ? row_token : 0)) * p.num_q_heads + h * g + row_head) * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(cols + C::kOCol + c * 32, o);
+                    tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 v2 = __floats2bfloat162_rn(o[q * 8 + 2 * e] * inv,
+                                                                                o[q * 8 + 2 * e + 1] * inv);
+                                w[e] = *reinterpret_cast<const uint32_t *>(&v2);
+                            }
+                            *reinterpret_cast<uint4 *>(dst + c * 32 + q * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (__builtin_expect(*reinterpret_cast<volatile int *>(&b.any_bad) != 0, 0) && row_ok) {
+                    // what was zeroed shows in its element of the rows that see it, whatever its weight
+                    for (int j = me.c0; j < me.c1; ++j) {
+                        bool clean = false;
+#pragma unroll
+                        for (int u = 0; u < C::kTiles; ++u)
+                            clean |= active(u, j) && (!tl[u].whole(see, j, nblk) || tl[u].split(see, bias, j));
+                        if (clean)
+                            scored_add_zeroed(p, s, h, max(lo_t, j * C::kKeys), min(hi_t, j * C::kKeys + C::kKeys - 1), D, dst);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::kTmemCols);
+    }
+}
+
+}  // namespace pkv

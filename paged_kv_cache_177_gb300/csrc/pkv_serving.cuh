@@ -211,6 +211,27 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
     return check_launch();
 }
 
+template <int D>
+int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                          const pkv::ScoredPrefillParams &sp, dim3 grid, cudaStream_t st) {
+    using C = pkv::TcCfg<D>;
+    auto kern = pkv::prefill_scored_kernel<D>;
+    static thread_local int configured_device = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
+    if (configured_device != dev) {
+        // the register split draws on the registers the CTA is launched with
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
+        if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + C::kTiles * 128 * C::kHighRegs) return PKV_ERR_UNSUPPORTED;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured_device = dev;
+    }
+    kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, sp);
+    return check_launch();
+}
+
 // CTAs of the cluster that takes a sequence. Few sequences share their rows among up to eight CTAs, as long as all fit
 // the card at once (two an SM) and a CTA's warps have a step each; rows of more than 512 KB are shared anyway, so that the
 // sequences whose drafts are refused more than once, which read on when the others are done, take less long.
@@ -512,6 +533,49 @@ int paged_decode_attention_scored(void *out, const void *q, const void *k_cache,
     return decode_dispatch(out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, num_seqs,
                            num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len, dtype,
                            partition_tokens, workspace, workspace_bytes, stream, kLaunch, &scores);
+}
+
+int paged_prefill_attention_scored(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                   const int32_t *block_tables, const int32_t *context_lens,
+                                   const int32_t *query_start, float scale, float softcap, int window,
+                                   const float *slopes, const int32_t *prefix_lens, int num_kv_heads, int num_seqs,
+                                   int num_q_heads, int head_dim, int max_blocks_per_seq, int num_blocks,
+                                   int num_queries, int max_query_len, int max_context_len, pkv_dtype dtype,
+                                   void *stream) {
+    pkv::ScoredPrefillParams sp{};
+    pkv::PrefillParams &pp = sp.pp;
+    int rc;
+    if ((rc = attention_params(pp.d, out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads,
+                               num_seqs, num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len,
+                               64)) != PKV_OK)
+        return rc;
+    if (max_query_len < 0 || num_queries < 0) return PKV_ERR_ARG;
+    if ((rc = score_params(pp.d, {softcap, window, slopes}, scale)) != PKV_OK) return rc;
+    if (dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+    if ((reinterpret_cast<uintptr_t>(prefix_lens) & 3) != 0) return PKV_ERR_ALIGN;
+    const int g = pp.d.group, tile_tokens = 128 / g;
+    const long long pairs = (max_query_len + 2LL * tile_tokens - 1) / (2 * tile_tokens);
+    if (pairs > 65535) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_query_len == 0 || num_queries == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start) return PKV_ERR_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
+    if (window == 0) pp.d.window = INT32_MAX;
+    sp.prefix_lens = prefix_lens;
+    pp.query_start = query_start;
+    pp.tile_tokens = tile_tokens;
+    pp.max_query_len = max_query_len;
+    pp.num_queries = num_queries;
+    // CTA order as for paged_prefill_attention
+    pp.seq_major = max_context_len >= 2LL * max_query_len ? 1 : 0;
+    const dim3 grid = pp.seq_major ? dim3(num_kv_heads, (unsigned)pairs, num_seqs)
+                                   : dim3(num_kv_heads, num_seqs, (unsigned)pairs);
+    alignas(64) CUtensorMap tmq, tmk, tmv;
+    if ((rc = encode_q_map(&tmq, q, num_queries, num_q_heads, head_dim, g, tile_tokens)) != PKV_OK) return rc;
+    if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim, true)) != PKV_OK) return rc;
+    if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return head_dim == 128 ? launch_prefill_scored<128>(tmq, tmk, tmv, sp, grid, st)
+                           : launch_prefill_scored<64>(tmq, tmk, tmv, sp, grid, st);
 }
 
 int verify_drafts(int32_t *accepted, int max_accepted, int32_t *num_accepted, int64_t *next_tokens,

@@ -57,10 +57,10 @@ def attend(q, k, v, scale, pos, cap=0.0, slopes=None, window=0, prefix=0, dtype=
     return out, bound
 
 
-def paged(seed, lens, hkv, d, dtype, window=0, extra=0, gain=1.0):
-    """Caches and tables for contexts of these lengths.  What a decode call with this window must not read is poisoned:
-    rows it does not see are NaN or infinite, table entries of blocks it does not read are out of range.
-    Returns (k_cache, v_cache, tables, k rows by sequence, v rows by sequence); the rows hold 0 where poisoned."""
+def paged(seed, lens, hkv, d, dtype, window=0, first_seen=None, gain=1.0):
+    """Caches and tables for contexts of these lengths.  What a call must not read is poisoned: rows that nothing sees
+    (before first_seen[s]; of a decode call with this window if that is None) are NaN or infinite, table entries of
+    blocks before them out of range.  Returns (k_cache, v_cache, tables, k rows by sequence, v rows by sequence); the rows hold 0 where poisoned."""
     rng = np.random.default_rng(seed)
     tables, nb = S.layout(rng, lens)
     t = lambda x: torch.from_numpy(x).to(dtype)
@@ -71,7 +71,7 @@ def paged(seed, lens, hkv, d, dtype, window=0, extra=0, gain=1.0):
     for s, n in enumerate(lens):
         kr.append(S.gather(S.f64(k), tables[s], n, nb))
         vr.append(S.gather(S.f64(v), tables[s], n, nb))
-        first = max(0, n - window) if window else 0
+        first = first_seen[s] if first_seen else max(0, n - window) if window else 0
         for i in range(first, n):
             dead[tables[s, i // BLOCK], i % BLOCK] = False
         kr[-1][:first] = vr[-1][:first] = 0.0
@@ -80,8 +80,8 @@ def paged(seed, lens, hkv, d, dtype, window=0, extra=0, gain=1.0):
     pick = torch.from_numpy(rng.integers(0, 3, size=k.shape))
     k, v = torch.where(where, poison[pick].to(dtype), k), torch.where(where, poison[pick.flip(0)].to(dtype), v)
     for s, n in enumerate(lens):
-        first = max(0, n - window) // BLOCK if window else 0
-        tables[s, :first] = -5
+        first = first_seen[s] if first_seen else max(0, n - window) if window else 0
+        tables[s, :first // BLOCK] = -5
     return k.cuda(), v.cuda(), torch.from_numpy(tables).cuda(), kr, vr
 
 

@@ -35,6 +35,20 @@ def test_decode_refusals(lib):
     assert f(S=0) == OK and f(S=0, slopes=None, cap=0.0, win=0) == OK
 
 
+def test_prefill_refusals(lib):
+    f = caller(lib, "paged_prefill_attention_scored", [
+        ("out", VP, A), ("q", VP, A), ("kc", VP, A), ("vc", VP, A), ("bt", VP, A), ("cl", VP, A), ("qs", VP, A),
+        ("scale", CF, 0.1), ("cap", CF, 30.0), ("win", CI, 7), ("slopes", VP, A), ("pre", VP, A), ("hkv", CI, 8), ("S", CI, 4),
+        ("hq", CI, 32), ("d", CI, 128), ("maxb", CI, 8), ("nb", CI, 64), ("T", CI, 40), ("maxq", CI, 16), ("maxlen", CI, 128),
+        ("dt", CI, 1), ("st", VP, None)])
+    assert f(cap=-1.0) == ARG and f(cap=NAN) == ARG and f(win=-1) == ARG and f(scale=INF) == ARG
+    assert f(S=-1) == ARG and f(hq=33) == ARG and f(T=-1) == ARG and f(maxq=-1) == ARG and f(qs=None) == ARG
+    assert f(slopes=A + 2) == ALIGN and f(pre=A + 2) == ALIGN and f(vc=A + 8) == ALIGN
+    assert f(dt=0) == UNSUPPORTED and f(dt=2) == UNSUPPORTED and f(d=80) == UNSUPPORTED and f(hq=8 * 65) == UNSUPPORTED
+    assert f(maxq=1 << 30) == UNSUPPORTED and f(nb=1 << 28) == UNSUPPORTED and f(maxb=1 << 28) == UNSUPPORTED
+    assert f(S=0) == OK and f(T=0) == OK and f(maxq=0, pre=None, slopes=None) == OK
+
+
 def test_the_form_by_hand():
     """Two keys: scores 4 and 0 capped to 2 tanh 2 and 0; a bias of 1 a token; a window that leaves one key."""
     q, k = np.array([[[2.0]]]), np.array([[[2.0]], [[0.0]]])
