@@ -211,11 +211,12 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
     return check_launch();
 }
 
-template <int D>
+template <int D, bool kCap, bool kBias>
 int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                           const pkv::ScoredPrefillParams &sp, dim3 grid, cudaStream_t st) {
-    using C = pkv::TcCfg<D>;
-    auto kern = pkv::prefill_scored_kernel<D>;
+    using C = pkv::ScoredCfg<D>;
+    static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
+    auto kern = pkv::prefill_scored_kernel<D, kCap, kBias>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -223,13 +224,25 @@ int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const 
         // the register split draws on the registers the CTA is launched with
         cudaFuncAttributes fa{};
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
-        if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + C::kTiles * 128 * C::kHighRegs) return PKV_ERR_UNSUPPORTED;
+        if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + C::kSoftmaxWarps * 32 * C::kHighRegs)
+            return PKV_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return PKV_ERR_CUDA;
         configured_device = dev;
     }
     kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, sp);
     return check_launch();
+}
+
+template <int D>
+int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
+                          const pkv::ScoredPrefillParams &sp, dim3 grid, cudaStream_t st) {
+    const bool bias = sp.pp.d.slopes != nullptr;
+    if (sp.pp.d.cap_log2 != 0.f)
+        return bias ? launch_prefill_scored<D, true, true>(tmq, tmk, tmv, sp, grid, st)
+                    : launch_prefill_scored<D, true, false>(tmq, tmk, tmv, sp, grid, st);
+    return bias ? launch_prefill_scored<D, false, true>(tmq, tmk, tmv, sp, grid, st)
+                : launch_prefill_scored<D, false, false>(tmq, tmk, tmv, sp, grid, st);
 }
 
 // CTAs of the cluster that takes a sequence. Few sequences share their rows among up to eight CTAs, as long as all fit
