@@ -629,6 +629,41 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
 
 /*
  * ---------------------------------------------------------------------------
+ * A prefix shared by many sequences
+ * ---------------------------------------------------------------------------
+ * paged_decode_attention for groups of consecutive sequences of any size that
+ * share their first blocks -- a batch under one system prompt. A group's prefix is
+ * attended once, for all its sequences' heads, on the tcgen05 tensor cores (K and V
+ * are read once per 256 rows of a kv head); each sequence then goes on from
+ * that state over its own blocks. (paged_decode_attention_shared_prefix reads a prefix
+ * once per 16 rows, for groups of any sequences that small.)
+ *
+ * Group z is sequences group_start[z] .. group_start[z+1]-1; group_start: int32
+ *   [num_groups + 1], non-decreasing, within [0, num_seqs]; num_groups <= num_seqs. shared_blocks: int32
+ *   [num_groups], leading blocks that the members' tables have in common; at most
+ *   the full blocks of the group's shortest member are used, read through its
+ *   first member's table. A sequence in no group is attended as it is.
+ *   max_group_size: host-side bound on the groups. A group past it or out of range
+ *   raises PKV_DEVERR_LENGTH and shares nothing.
+ * Results as of paged_decode_attention (weights of the prefix are rounded to bf16 in
+ * another order). bf16; num_q_heads / num_kv_heads at most 16; at most 8192 sequences.
+ * workspace: pkv_common_prefix_workspace_bytes(...) bytes, zero-filled once like any decode
+ *   workspace (its first PKV_DECODE_COUNTER_BYTES are the same counters). Concurrent
+ *   calls must not share it.
+ */
+int paged_decode_attention_common_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                         const int32_t *block_tables, const int32_t *context_lens, float scale,
+                                         int num_kv_heads, int num_seqs, int num_q_heads, int head_dim,
+                                         int max_blocks_per_seq, int num_blocks, int max_context_len,
+                                         const int32_t *group_start, const int32_t *shared_blocks, int num_groups,
+                                         int max_group_size, pkv_dtype dtype, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/* Workspace bytes paged_decode_attention_common_prefix needs. */
+size_t pkv_common_prefix_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim);
+
+/*
+ * ---------------------------------------------------------------------------
  * Transformed scores
  * ---------------------------------------------------------------------------
  * paged_decode_attention for layers that change their scores before the softmax

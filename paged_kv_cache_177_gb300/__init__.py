@@ -24,6 +24,7 @@ _BINDING_NAMES = {
     "paged_decode_attention_e4m3", "e4m3_workspace_bytes", "qk_norm_rope_append", "tree_masks",
     "paged_tree_attention", "tree_workspace_bytes", "kv_accept_layers", "verify_drafts",
     "paged_decode_attention_scored", "paged_prefill_attention_scored",
+    "paged_decode_attention_common_prefix", "common_prefix_workspace_bytes",
 }
 
 

@@ -85,6 +85,9 @@ _scored = _decl("paged_decode_attention_scored", _i, _vp, _vp, _vp, _vp, _vp, _v
                 _i, _i, _i, _i, _vp, _sz, _vp)
 _prefill_scored = _decl("paged_prefill_attention_scored", _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f, _f, _i, _vp, _vp, _i,
                         _i, _i, _i, _i, _i, _i, _i, _i, _i, _vp)
+_common = _decl("paged_decode_attention_common_prefix", _i, _vp, _vp, _vp, _vp, _vp, _vp, _f, _i, _i, _i, _i, _i, _i, _i, _vp,
+                _vp, _i, _i, _i, _vp, _sz, _vp)
+_common_ws = _decl("pkv_common_prefix_workspace_bytes", _sz, _i, _i, _i, _i)
 _verify = _decl("verify_drafts", _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i, _i, _i, _i, _i,
                 _vp)
 _device_error = _decl("pkv_device_error", _i, ctypes.POINTER(ctypes.c_uint32), _i)
@@ -1044,6 +1047,52 @@ def paged_prefill_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: 
             query_start.data_ptr(), float(scale), float(softcap), int(window), _slopes(slopes, Hq, dev),
             _p(prefix_lens), cache[1], S, Hq, D, tables[1] if S else 1, cache[0], T, int(max_query_len),
             int(max_context_len), PKV_BF16)
+    return out
+
+
+def common_prefix_workspace_bytes(num_seqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    """Workspace bytes of paged_decode_attention_common_prefix."""
+    return int(_common_ws(num_seqs, num_q_heads, num_kv_heads, head_dim))
+
+
+def paged_decode_attention_common_prefix(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor,
+                                         v_cache: torch.Tensor, block_tables: torch.Tensor,
+                                         context_lens: torch.Tensor, scale: float, group_start: torch.Tensor,
+                                         shared_blocks: torch.Tensor, *, max_group_size: Optional[int] = None,
+                                         max_context_len: Optional[int] = None,
+                                         workspace: Optional[torch.Tensor] = None,
+                                         stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """paged_decode_attention for groups of consecutive sequences that share
+    leading blocks (a batch under one system prompt): a group's prefix is
+    attended once for all its sequences, of which there may be any number, and
+    each sequence's own blocks behind it; see include/pagedkv.h.
+
+    group_start: int32 [G + 1], group z being sequences group_start[z] ..
+    group_start[z+1]-1; shared_blocks: int32 [G].  Sequences in no group share
+    nothing.  bf16, up to 16 query heads to a kv head.  ``max_group_size`` and
+    ``max_context_len`` default to the maxima of the device arrays (a sync).
+    ``workspace``: at least ``common_prefix_workspace_bytes(...)`` bytes,
+    zero-filled before its first use; calls that may overlap must not share it."""
+    dev = _index(out, q, k_cache, v_cache, block_tables, context_lens, group_start, shared_blocks)
+    if q.dtype != torch.bfloat16:
+        raise TypeError("common-prefix decode is bf16")
+    S, Hq, D, NB, Hkv, max_blocks = _decode_shapes(out, q, k_cache, v_cache, block_tables, context_lens)
+    if group_start.dtype != torch.int32 or shared_blocks.dtype != torch.int32 or shared_blocks.dim() != 1 \
+            or group_start.shape != (shared_blocks.shape[0] + 1,):
+        raise TypeError("expected group_start int32 [G + 1] and shared_blocks int32 [G]")
+    G = shared_blocks.shape[0]
+    if max_group_size is None:
+        max_group_size = int((group_start[1:] - group_start[:-1]).max().item()) if G else 0
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if S else 0
+    if workspace is None and S:
+        with torch.cuda.stream(stream):           # zero-filled, on the call's stream
+            workspace = torch.zeros(_common_ws(S, Hq, Hkv, D), dtype=torch.uint8, device=k_cache.device)
+    keep, ws, ws_bytes = _workspace(0, workspace, dev, stream)
+    _launch(_common, "paged_decode_attention_common_prefix", dev, stream, out.data_ptr(), q.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale), Hkv, S,
+            Hq, D, max_blocks, NB, int(max_context_len), group_start.data_ptr() if G else None,
+            shared_blocks.data_ptr() if G else None, G, int(max_group_size), PKV_BF16, ws, ws_bytes)
     return out
 
 

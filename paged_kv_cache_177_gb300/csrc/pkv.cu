@@ -275,11 +275,13 @@ int launch_f32(const pkv::DecodeParams &p, dim3 grid, cudaStream_t st, bool pdl)
     if (g == 1) return launch_f32_staged<D, 1, FORM>(tmk, tmv, p, grid, st, pdl);
     if (g == 2) return launch_f32_staged<D, 2, FORM>(tmk, tmv, p, grid, st, pdl);
     if (g <= 4) return launch_f32_staged<D, 4, FORM>(tmk, tmv, p, grid, st, pdl);
-    if (kF32Tc)
+    if constexpr (kF32Tc) {
         return g <= 8 ? launch_f32_tc<D, 8, FORM>(tmk, tmv, p, grid, st, pdl)
                       : launch_f32_tc<D, 16, FORM>(tmk, tmv, p, grid, st, pdl);
-    if (g <= 8) return launch_f32_staged<D, 8, FORM>(tmk, tmv, p, grid, st, pdl);
-    return launch_f32_staged<D, 16, FORM>(tmk, tmv, p, grid, st, pdl);
+    } else {
+        return g <= 8 ? launch_f32_staged<D, 8, FORM>(tmk, tmv, p, grid, st, pdl)
+                      : launch_f32_staged<D, 16, FORM>(tmk, tmv, p, grid, st, pdl);
+    }
 }
 
 template <int D, int NT>

@@ -1118,9 +1118,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
             for (int i = tid; i < p.num_q_heads * D; i += C::kThreads) {
                 float v = 0.f;
                 if constexpr (FORM == kBehindPrefix) {
-                    const size_t row = (size_t)s * p.num_q_heads + i / D;
-                    const float l = __ldcg(p.prefix_ml + 2 * row + 1);
-                    if (l != 0.f) v = __ldcg(p.prefix_o + row * D + i % D) / l;
+                    if (seq_len(p, s, false) > 0) {
+                        const size_t row = (size_t)s * p.num_q_heads + i / D;
+                        v = __ldcg(p.prefix_o + row * D + i % D) / __ldcg(p.prefix_ml + 2 * row + 1);
+                    }
                 }
                 o[i] = to_out<OutT>(v);
             }
@@ -1239,7 +1240,7 @@ __global__ void __launch_bounds__(NW * 32, 1)
     auto begin = [&]() {
         if constexpr (FORM == kScored) wa.load_slopes(p.slopes ? p.slopes + c.h * g : nullptr, g, lane);
         if constexpr (FORM == kBehindPrefix) {
-            if (seg_j0 == 0) {
+            if (seg_j0 == 0 && first > 0) {
                 const size_t row = (size_t)c.s * p.num_q_heads + (size_t)c.h * g;
                 wa.load_state(p.prefix_ml + 2 * row, p.prefix_o + row * D, g, lane);
                 return;

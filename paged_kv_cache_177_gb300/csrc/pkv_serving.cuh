@@ -150,12 +150,12 @@ bool tree_whole_units(int max_context_len) { return max_context_len <= 512; }
 // Two row tiles to a unit where one does not hold the largest tree's rows.
 bool tree_pair(int g, int max_query_len) { return max_query_len > 128 / g; }
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kPrefix = false>
 int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::TreeParams &tp,
                 int q_tokens, void *workspace, cudaStream_t st) {
     using C = pkv::TreeCfg<D, kPair>;
     static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
-    auto kern = pkv::tree_attention_kernel<D, kPair>;
+    auto kern = pkv::tree_attention_kernel<D, kPair, kPrefix>;
     static thread_local int configured_device = -1;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
@@ -183,8 +183,8 @@ int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMa
     if (rc != PKV_OK || whole) return rc;
     const int per_set = C::kTiles * tile_tokens;
     const int rows = (tp.max_query_len < per_set ? tp.max_query_len : per_set) * g;  // of the largest unit
-    return launch_pdl(pkv::tree_merge_kernel<D>, dim3(grid, (rows + 7) / 8), dim3(256), 0, st,
-                      static_cast<__nv_bfloat16 *>(tp.d.out), static_cast<const float *>(partials),
+    return launch_pdl(pkv::tree_merge_kernel<D, kPrefix>, dim3(grid, (rows + 7) / 8), dim3(256), 0, st,
+                      static_cast<__nv_bfloat16 *>(tp.d.out), tp.prefix_ml, tp.prefix_o, static_cast<const float *>(partials),
                       static_cast<const pkv::TreeCut *>(cuts), C::kUnitRows, g, tp.d.num_q_heads, tile_tokens);
 }
 
@@ -534,6 +534,93 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
     pkv::kv_accept_kernel<<<dim3((num_kv_heads + heads - 1) / heads, num_layers, num_seqs), 128, smem,
                             static_cast<cudaStream_t>(stream)>>>(p);
     return check_launch();
+}
+
+// The workspace of paged_decode_attention_common_prefix: the decode workspace of the persistent kernel, the tree kernel's
+// records and states (its own counter header unused), the plan, and the rows' states of the prefix.
+static size_t common_prefix_states(int num_seqs, int num_q_heads, int head_dim) {
+    return (size_t)num_seqs * num_q_heads * (2 + (size_t)head_dim) * sizeof(float);
+}
+static size_t common_prefix_plan_bytes(int num_seqs) { return (2 * (size_t)num_seqs * sizeof(int32_t) + 255) / 256 * 256; }
+static size_t common_prefix_tree_bytes(int head_dim) {
+    return kCounterBytes + kPersistMaxCtas * (sizeof(pkv::TreeCut) + 2 * 256 * (2 + (size_t)head_dim) * sizeof(float));
+}
+
+size_t pkv_common_prefix_workspace_bytes(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim) {
+    if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_q_heads % num_kv_heads != 0)
+        return 0;
+    return (persist_workspace_bytes(num_q_heads, num_kv_heads, head_dim) + 255) / 256 * 256 +
+           common_prefix_tree_bytes(head_dim) + common_prefix_plan_bytes(num_seqs) +
+           common_prefix_states(num_seqs, num_q_heads, head_dim);
+}
+
+int paged_decode_attention_common_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
+                                         const int32_t *block_tables, const int32_t *context_lens, float scale,
+                                         int num_kv_heads, int num_seqs, int num_q_heads, int head_dim,
+                                         int max_blocks_per_seq, int num_blocks, int max_context_len,
+                                         const int32_t *group_start, const int32_t *shared_blocks, int num_groups,
+                                         int max_group_size, pkv_dtype dtype, void *workspace, size_t workspace_bytes,
+                                         void *stream) {
+    pkv::DecodeParams p{};
+    int rc;
+    if ((rc = attention_params(p, out, q, k_cache, v_cache, block_tables, context_lens, scale, num_kv_heads, num_seqs,
+                               num_q_heads, head_dim, max_blocks_per_seq, num_blocks, max_context_len, 16)) != PKV_OK)
+        return rc;
+    if (num_groups < 0 || max_group_size < 0 || num_groups > num_seqs) return PKV_ERR_ARG;
+    if (dtype != PKV_BF16 || num_seqs > kPersistMaxSeqs) return PKV_ERR_UNSUPPORTED;
+    // the decode kernel counts a launch's blocks in 32 bits
+    if (std::min<int64_t>(((int64_t)max_context_len + 15) / 16, max_blocks_per_seq) * num_seqs > INT32_MAX)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens) return PKV_ERR_ARG;
+    if (num_groups > 0 && (!group_start || !shared_blocks)) return PKV_ERR_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
+    const size_t need = pkv_common_prefix_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim);
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return PKV_ERR_WORKSPACE;
+    char *ws = static_cast<char *>(workspace);
+    p.counters = reinterpret_cast<int *>(ws);
+    p.partials = reinterpret_cast<float *>(ws + kCounterBytes);
+    ws += (persist_workspace_bytes(num_q_heads, num_kv_heads, head_dim) + 255) / 256 * 256;
+    char *tree = ws;
+    ws += common_prefix_tree_bytes(head_dim);
+    int32_t *tokens = reinterpret_cast<int32_t *>(ws), *first_blocks = tokens + num_seqs;
+    ws += common_prefix_plan_bytes(num_seqs);
+    float *prefix_ml = reinterpret_cast<float *>(ws), *prefix_o = prefix_ml + 2 * (size_t)num_seqs * num_q_heads;
+    p.first_blocks = first_blocks;
+    p.prefix_ml = prefix_ml;
+    p.prefix_o = prefix_o;
+
+    const int g = p.group, tile_tokens = 128 / g;
+    alignas(64) CUtensorMap tmq, tmk, tmk_half, tmv;
+    if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    pkv::common_prefix_plan_kernel<<<1, 1024, 0, st>>>(p, group_start, shared_blocks, num_groups, max_group_size, tokens,
+                                                       first_blocks);
+    if ((rc = check_launch()) != PKV_OK) return rc;
+    if (num_groups > 0 && max_group_size > 0) {
+        const int q_tokens = max_group_size < tile_tokens ? max_group_size : tile_tokens;
+        if ((rc = encode_q_map(&tmq, q, num_seqs, num_q_heads, head_dim, g, q_tokens)) != PKV_OK) return rc;
+        if ((rc = encode_cache_map(&tmk_half, k_cache, num_blocks, num_kv_heads, head_dim, true)) != PKV_OK) return rc;
+        pkv::TreeParams tp{};
+        tp.d = p;
+        tp.d.context_lens = tokens;
+        tp.d.num_seqs = num_groups;
+        tp.query_start = group_start;
+        tp.num_queries = num_seqs;
+        tp.max_query_len = max_group_size;
+        tp.prefix_ml = prefix_ml;
+        tp.prefix_o = prefix_o;
+        const bool pair = tree_pair(g, max_group_size);
+        rc = head_dim == 128 ? (pair ? launch_tree<128, true, true>(tmq, tmk_half, tmv, tp, q_tokens, tree, st)
+                                     : launch_tree<128, false, true>(tmq, tmk_half, tmv, tp, q_tokens, tree, st))
+                             : (pair ? launch_tree<64, true, true>(tmq, tmk_half, tmv, tp, q_tokens, tree, st)
+                                     : launch_tree<64, false, true>(tmq, tmk_half, tmv, tp, q_tokens, tree, st));
+        if (rc != PKV_OK) return rc;
+    }
+    constexpr int ns128 = PKV_PERSIST_STAGES_D128, ns64 = PKV_PERSIST_STAGES_D64;
+    return persistent_by_shape<__nv_bfloat16, ns128, ns64, kPersistWarps, pkv::kBehindPrefix>(
+        tmk, tmv, p, st, num_groups > 0 && max_group_size > 0, head_dim, g);
 }
 
 int paged_decode_attention_scored(void *out, const void *q, const void *k_cache, const void *v_cache,

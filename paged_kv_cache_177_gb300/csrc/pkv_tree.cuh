@@ -12,6 +12,10 @@ struct TreeParams {
     const int32_t *query_start;  // [num_seqs + 1]
     const int64_t *mask;         // [num_queries][mask_words]
     int mask_words, num_queries, max_query_len;
+    // A prefix that a group of sequences shares (kPrefix): d.context_lens are the prefixes' tokens, a group's rows are its
+    // sequences' queries, its blocks those of its first sequence's table, and a row's state goes here
+    float *prefix_ml;            // [num_queries][Hq][2]: max (log2 domain), sum
+    float *prefix_o;             // [num_queries][Hq][D]: unnormalised output
 };
 
 // A sequence's first row and number of drafts; false (flagged by the caller's
@@ -163,7 +167,7 @@ constexpr int kTreeUnitCost = 3;
 __device__ __forceinline__ int tree_workers(long long T) { return (int)min((long long)gridDim.x, max(1LL, T / 4)); }
 
 // A worker's way along the line: one segment (a unit's chunks c0 .. c1 - 1) at a time.
-template <int D, bool kPair>
+template <int D, bool kPair, bool kPrefix>
 struct TreeWalk {
     using C = TreeCfg<D, kPair>;
     int s, unit, units;       // sequence, unit within it (kv head major, then row set), its units
@@ -175,10 +179,11 @@ struct TreeWalk {
     __device__ __forceinline__ static long long weigh(const TreeParams &tp, int s, int per_set, bool flag, int &len,
                                                 int &q0, int &n) {
         len = seq_len(tp.d, s, flag);
-        if (!tree_rows(tp.query_start, s, len, tp.max_query_len, tp.num_queries, q0, n)) {
+        if (!tree_rows(tp.query_start, s, kPrefix ? INT_MAX : len, tp.max_query_len, tp.num_queries, q0, n)) {
             if (flag) raise_error(PKV_DEVERR_LENGTH);
             n = 0;
         }
+        if (kPrefix && len == 0) n = 0;
         const int sets = (n + per_set - 1) / per_set;
         return (long long)sets * tp.d.num_kv_heads * ((len + C::kKeys - 1) / C::kKeys + kTreeUnitCost);
     }
@@ -219,6 +224,8 @@ struct TreeWalk {
         c1 = whole ? chunks : (int)max(0LL, min((long long)chunks, end - x - kTreeUnitCost));
         return c1 > 0;
     }
+    __device__ __forceinline__ int ctx() const { return kPrefix ? len : len - n; }        // tokens that every row sees
+    __device__ __forceinline__ int table_row() const { return kPrefix ? q0 : s; }
     // (one tile's worth of rows holds every tree where units are single tiles: one set)
     __device__ __forceinline__ int head() const { return kPair ? unit / sets : unit; }
     __device__ __forceinline__ int first_draft(int per_set) const { return kPair ? (unit % sets) * per_set : 0; }
@@ -257,9 +264,9 @@ __device__ __forceinline__ unsigned long long tree_columns(unsigned long long vi
 
 // One warp's copies, issued by its first lane: the K chunks of the worker's range and each unit's Q rows, or the V
 // chunks. Lane i < 8 holds the id of a chunk's i-th block, and the next chunk's ahead of use.
-template <int D, bool kPair, bool kKeysAndQ>
+template <int D, bool kPair, bool kPrefix, bool kKeysAndQ>
 __device__ __forceinline__ void tree_produce(const CUtensorMap &tm, const CUtensorMap &tmq, const TreeParams &tp,
-                                             TreeWalk<D, kPair> at, uint8_t *base, TreeBars &b, int per_set,
+                                             TreeWalk<D, kPair, kPrefix> at, uint8_t *base, TreeBars &b, int per_set,
                                              int tile_tokens, int q_tokens, bool whole, int lane) {
     using C = TreeCfg<D, kPair>;
     constexpr int NS = C::kStages, CB = C::kChunkBlocks;
@@ -272,7 +279,7 @@ __device__ __forceinline__ void tree_produce(const CUtensorMap &tm, const CUtens
     do {
         const int h = at.head();
         const int nblk = (at.len + kBlock - 1) / kBlock, last_valid = at.len - (nblk - 1) * kBlock;
-        const int32_t *table = p.block_tables + (size_t)at.s * p.max_blocks_per_seq;
+        const int32_t *table = p.block_tables + (size_t)at.table_row() * p.max_blocks_per_seq;
         auto id_of = [&](int j) { return lane < CB && j * CB + lane < nblk ? __ldg(table + j * CB + lane) : -1; };
         int ahead = id_of(at.c0);
         for (int j = at.c0; j < at.c1; ++j, ++r) {
@@ -355,7 +362,7 @@ __device__ __noinline__ void tree_add_zeroed(const DecodeParams &p, const int64_
     }
 }
 
-template <int D, bool kPair>
+template <int D, bool kPair, bool kPrefix>
 __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     tree_attention_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const TreeParams tp, float *partials,
@@ -413,7 +420,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         int len, q0, n;
         long long local = 0;
         for (int s = s_lo; s < s_hi; ++s)
-            local += TreeWalk<D, kPair>::weigh(tp, s, per_set, blockIdx.x == 0, len, q0, n);
+            local += TreeWalk<D, kPair, kPrefix>::weigh(tp, s, per_set, blockIdx.x == 0, len, q0, n);
         long long incl = local;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         if ((int)blockIdx.x < W && start >= before && start < before + local) {
             long long at = before;
             for (int s = s_lo; s < s_hi; ++s) {
-                const long long wt = TreeWalk<D, kPair>::weigh(tp, s, per_set, false, len, q0, n);
+                const long long wt = TreeWalk<D, kPair, kPrefix>::weigh(tp, s, per_set, false, len, q0, n);
                 if (start < at + wt) {
                     b.start_seq = s;
                     b.start_in = start - at;
@@ -451,7 +458,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     const uint32_t tmem = b.tmem_base;
     const long long T = b.total;
     const int W = tree_workers(T), w = blockIdx.x;
-    TreeWalk<D, kPair> at;
+    TreeWalk<D, kPair, kPrefix> at;
     bool work = w < W && T > 0;
     if (work) {
         const long long start = T * w / W;
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
         setmaxnreg_dec<C::kLowRegs>();
         if (warp == 0) {
             // ------------------------------ TMA: Q and K ------------------------------
-            tree_produce<D, kPair, true>(tmk, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole, lane);
+            tree_produce<D, kPair, kPrefix, true>(tmk, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole, lane);
         } else if (warp == 1) {
             // ------------------------------ MMA issuer ------------------------------
             if (lane == 0) {
@@ -537,7 +544,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             ok = values_ready(k) && (k + 1 == nc || wait_k(r0 + k + 1));
                             for (int t = 0; t < tiles && ok; ++t) {
                                 if (!(ok = weights_ready(t))) break;
-                                issue_pv(t, r0 + k, k == 0, tree_split(at.len - at.n));
+                                issue_pv(t, r0 + k, k == 0, tree_split(at.ctx()));
                                 if (k + 1 < nc) {
                                     issue_s(t, r0 + k + 1);
                                     umma_commit(&b.s_full[t]);
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             if (k + 1 < nc && !(ok = scores(k + 1))) break;
                             if (k < 0) continue;
                             if (!(ok = values_ready(k) && weights_ready(k & 1))) break;
-                            issue_pv(k & 1, r0 + k, k < 2, tree_split(at.len - at.n));
+                            issue_pv(k & 1, r0 + k, k < 2, tree_split(at.ctx()));
                             umma_commit(&b.v_empty[(r0 + k) % NS]);
                             if (k + 2 >= nc) umma_commit(&b.o_done[k & 1]);
                         }
@@ -582,13 +589,13 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             __syncwarp();
         } else if (warp == 2) {
             // ------------------------------ TMA: V ------------------------------
-            tree_produce<D, kPair, false>(tmv, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole, lane);
+            tree_produce<D, kPair, kPrefix, false>(tmv, tmq, tp, at, base, b, per_set, tile_tokens, q_tokens, whole, lane);
         } else {
             // ------------------------------ the drafts' values ------------------------------
             bool ok = true;
             int r0 = 0;
             do {
-                const int nc = at.c1 - at.c0, first = tree_first_clean(at.len - at.n);
+                const int nc = at.c1 - at.c0, first = tree_first_clean(at.ctx());
                 const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
                 // every chunk is waited for and passed on, drafts or not, so that no stage's phase runs
                 // away from this role's count
@@ -648,9 +655,10 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             const int rows = max(0, min(at.n - tok0, tile_tokens)) * g;
             const bool row_ok = row < rows;
             const int draft = tok0 + row_draft;
-            const int64_t *words = tp.mask + (size_t)(at.q0 + (row_ok ? draft : 0)) * tp.mask_words;
-            const unsigned long long word0 = (unsigned long long)__ldg(reinterpret_cast<const long long *>(words));
-            const int ctx = at.len - at.n;
+            const int64_t *words = kPrefix ? nullptr : tp.mask + (size_t)(at.q0 + (row_ok ? draft : 0)) * tp.mask_words;
+            const unsigned long long word0 =
+                kPrefix ? 0ull : (unsigned long long)__ldg(reinterpret_cast<const long long *>(words));
+            const int ctx = at.ctx();
             const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
             const bool warp_rows = quad * 32 < rows;   // a warp without rows only keeps the barriers' count
             float m = -INFINITY, l = 0.f;
@@ -675,7 +683,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 2; ++i) {
                                 const int blk = j * C::kChunkBlocks + 4 * i;
-                                see[i] = tree_columns(tree_visible(words, word0, blk * kBlock, ctx, at.n), blk, nblk, lo);
+                                see[i] = tree_columns(tree_visible(words, word0, blk * kBlock, ctx, kPrefix ? 0 : at.n), blk,
+                                                      nblk, lo);
                             }
                         }
 #pragma unroll 1
@@ -818,7 +827,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     f[side ^ 1] = ex2_approx(other.x - ms);
                     L = l * f[side] + other.y * f[side ^ 1];
                 }
-                const float inv = !uncut ? 1.f : L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // (NaN stays)
+                const float inv = kPrefix || !uncut ? 1.f : L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;  // (NaN stays)
                 f[0] *= inv;
                 f[1] *= inv;
                 constexpr int kMine = kPair ? D : D / 2;   // columns this side writes
@@ -827,9 +836,14 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                 float *slot = partials + (size_t)(2 * w + (at.c0 == 0 ? 1 : 0)) * C::kUnitRows * (2 + D);
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
                                      ((size_t)(at.q0 + (row_ok ? draft : 0)) * p.num_q_heads + h * g + row_head) * D + d0;
-                if (!uncut && d0 == 0 && row_ok)
-                    *reinterpret_cast<float2 *>(slot + 2 * unit_row) = make_float2(M, L);
-                float *po = slot + 2 * C::kUnitRows + (size_t)unit_row * D + d0;
+                float *ml = slot + 2 * unit_row, *po = slot + 2 * C::kUnitRows + (size_t)unit_row * D + d0;
+                const bool state = kPrefix || !uncut;      // the row leaves a state, not an output
+                if (kPrefix && uncut) {
+                    const size_t r = (size_t)(at.q0 + (row_ok ? draft : 0)) * p.num_q_heads + h * g + row_head;
+                    ml = tp.prefix_ml + 2 * r;
+                    po = tp.prefix_o + r * D + d0;
+                }
+                if (state && d0 == 0 && row_ok) *reinterpret_cast<float2 *>(ml) = make_float2(M, L);
                 const uint64_t g0 = pack_f2(f[0], f[0]), g1 = pack_f2(f[1], f[1]), zero = pack_f2(0.f, 0.f);
                 const uint32_t col0 = (kPair ? cols : lane_cols) + C::kOCol + d0;
 #pragma unroll 1
@@ -844,7 +858,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                         if (!kPair && both) v = fma_f2(pack_f2(o1[e], o1[e + 1]), g1, v);
                         unpack_f2(v, o[e], o[e + 1]);
                     }
-                    if (row_ok && uncut) {
+                    if (row_ok && !state) {
                         uint32_t v[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -861,8 +875,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     }
                 }
                 if (__builtin_expect(row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0, 0))
-                    tree_add_zeroed(p, words, at.s, h, max(tree_first_clean(ctx), at.c0 * C::kKeys),
-                                    min(at.len, at.c1 * C::kKeys), ctx, D, d0, kMine, uncut ? dst : nullptr, po);
+                    tree_add_zeroed(p, words, at.table_row(), h, max(tree_first_clean(ctx), at.c0 * C::kKeys),
+                                    min(at.len, at.c1 * C::kKeys), ctx, D, d0, kMine, state ? nullptr : dst, po);
                 tc_fence_before();
             }
             if (!uncut && at.c0 == 0) {  // begun here, ends further on (a worker cuts at most one unit so)
@@ -894,11 +908,11 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     }
 }
 
-// Joins the states of every cut unit: a warp per row, four segments' loads in flight.
-template <int D>
+// Joins the states of every cut unit: a warp per row, four segments' loads in flight. prefix_ml (kPrefix): into states.
+template <int D, bool kPrefix>
 __global__ void __launch_bounds__(256)
-    tree_merge_kernel(__nv_bfloat16 *out, const float *__restrict__ partials, const TreeCut *__restrict__ cuts,
-                      int unit_rows, int g, int num_q_heads, int tile_tokens) {
+    tree_merge_kernel(__nv_bfloat16 *out, float *prefix_ml, float *prefix_o, const float *__restrict__ partials,
+                      const TreeCut *__restrict__ cuts, int unit_rows, int g, int num_q_heads, int tile_tokens) {
     constexpr int PER = D / 32, NB = 4;
     const int w1 = blockIdx.x, lane = threadIdx.x & 31;
     const int i = blockIdx.y * 8 + (threadIdx.x >> 5);  // (draft, head) of the unit
@@ -944,10 +958,44 @@ __global__ void __launch_bounds__(256)
             for (int e = 0; e < PER; ++e) acc[e] = fmaf(o[b][e], f, acc[e]);
         }
     }
+    const size_t r = (size_t)(cut.q_row + draft) * num_q_heads + cut.head + hg;
+    if constexpr (kPrefix) {
+        if (lane == 0) *reinterpret_cast<float2 *>(prefix_ml + 2 * r) = make_float2(M, L);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) prefix_o[r * D + lane + 32 * e] = acc[e];
+        return;
+    }
     const float inv = L > 0.f ? 1.f / L : L == 0.f ? 0.f : L;
-    __nv_bfloat16 *dst = out + ((size_t)(cut.q_row + draft) * num_q_heads + cut.head + hg) * D;
+    __nv_bfloat16 *dst = out + r * D;
 #pragma unroll
     for (int e = 0; e < PER; ++e) dst[lane + 32 * e] = __float2bfloat16_rn(acc[e] * inv);
+}
+
+// =====================================================================================
+// A prefix shared by many sequences: what the two kernels behind it need to know, from one CTA. A group's prefix is
+// cut to the full blocks of its shortest sequence. tokens [num_groups], first_blocks [num_seqs].
+// =====================================================================================
+__global__ void __launch_bounds__(1024)
+    common_prefix_plan_kernel(const DecodeParams p, const int32_t *group_start, const int32_t *shared_blocks,
+                              int num_groups, int max_group_size, int32_t *tokens, int32_t *first_blocks) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    for (int s = tid; s < p.num_seqs; s += blockDim.x) first_blocks[s] = 0;
+    __syncthreads();
+    for (int z = tid >> 5; z < num_groups; z += blockDim.x >> 5) {
+        const int s0 = __ldg(group_start + z);
+        const long long n = (long long)__ldg(group_start + z + 1) - s0;
+        int blocks = max(__ldg(shared_blocks + z), 0);
+        if (s0 < 0 || n < 0 || n > max_group_size || s0 + n > p.num_seqs) {
+            if (lane == 0) raise_error(PKV_DEVERR_LENGTH);
+            blocks = 0;
+        } else {
+            for (int i = lane; i < n; i += 32) blocks = min(blocks, seq_len(p, s0 + i, true) / kBlock);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) blocks = min(blocks, __shfl_xor_sync(0xffffffffu, blocks, o));
+            for (int i = lane; i < n; i += 32) first_blocks[s0 + i] = blocks;
+        }
+        if (lane == 0) tokens[z] = n > 0 ? blocks * kBlock : 0;
+    }
 }
 
 // =====================================================================================

@@ -49,6 +49,25 @@ def test_prefill_refusals(lib):
     assert f(S=0) == OK and f(T=0) == OK and f(maxq=0, pre=None, slopes=None) == OK
 
 
+def test_common_prefix_refusals(lib):
+    f = caller(lib, "paged_decode_attention_common_prefix", [
+        ("out", VP, A), ("q", VP, A), ("kc", VP, A), ("vc", VP, A), ("bt", VP, A), ("cl", VP, A), ("scale", CF, 0.1),
+        ("hkv", CI, 8), ("S", CI, 4), ("hq", CI, 32), ("d", CI, 128), ("maxb", CI, 8), ("nb", CI, 64), ("maxlen", CI, 128),
+        ("gs", VP, A), ("sb", VP, A), ("G", CI, 2), ("maxg", CI, 3), ("dt", CI, 1), ("ws", VP, None), ("wsb", SZ, 0),
+        ("st", VP, None)])
+    assert f(S=-1) == ARG and f(hkv=0) == ARG and f(hq=33) == ARG and f(maxb=0) == ARG and f(maxlen=-1) == ARG
+    assert f(G=-1) == ARG and f(maxg=-1) == ARG and f(G=5) == ARG and f(gs=None) == ARG and f(sb=None) == ARG
+    assert f(scale=INF) == ARG and f(out=None) == ARG and f(q=A + 8) == ALIGN
+    assert f(dt=0) == UNSUPPORTED and f(dt=2) == UNSUPPORTED and f(d=80) == UNSUPPORTED and f(hq=8 * 17) == UNSUPPORTED
+    assert f(S=8193) == UNSUPPORTED and f(nb=1 << 28) == UNSUPPORTED and f(S=4096, maxb=1 << 20, maxlen=1 << 30) == UNSUPPORTED
+    assert f() == WORKSPACE and f(ws=A, wsb=1 << 20) == WORKSPACE
+    assert f(S=0, G=0) == OK
+    g = lib.pkv_common_prefix_workspace_bytes
+    g.restype, g.argtypes = SZ, [CI] * 4
+    assert g(0, 8, 2, 64) == 0 and g(4, 9, 2, 64) == 0
+    assert g(8, 8, 2, 64) - g(4, 8, 2, 64) == 4 * 8 * 66 * 4
+
+
 def test_the_form_by_hand():
     """Two keys: scores 4 and 0 capped to 2 tanh 2 and 0; a bias of 1 a token; a window that leaves one key."""
     q, k = np.array([[[2.0]]]), np.array([[[2.0]], [[0.0]]])
