@@ -20,42 +20,35 @@ struct ScoredPrefillParams {
 // Roles and pipelines are those of prefill_tc_kernel (a CTA per pair of 128-row tiles, K and V chunks in two-stage
 // rings, S and P in the same tensor-memory columns). What differs:
 //  - each tile has its own first and last chunk; the pair walks their union, in which there is no gap;
-//  - two threads share a row, 64 of a chunk's keys each, which agree on the row's maximum through shared memory: sixteen
-//    softmax warps hide the latencies that eight leave open when the scores are transformed as well
-//    (512-token chunks behind 16K-32K tokens, 32 q / 8 kv heads, a cap of 50: 2210 us, 2471 with eight; scores past the
-//    polynomial 2870, 4977);
 //  - a warp cleans values: a row that does not see a key must not meet its NaN or infinity (0 times either is NaN),
 //    so in chunks that not every row sees whole such elements are zeroed before P V, and added at the end,
 //    element by element, to the rows that see them;
-//  - capped scores come from a polynomial in registers, raw Q(raw^2) with Q that of cap tanh(y) / raw, y = raw scale /
-//    cap, for |y| <= 3/4, 5.7e-7 of the score off. tanh by exponentials takes two more instructions a score on the
+//  - capped scores come from a polynomial, raw Q(raw^2) with Q that of cap tanh(y) / raw, y = raw scale / cap, for
+//    |y| <= 3/4, 5.7e-7 of the score off. tanh by exponentials takes two more instructions a score on the
 //    special-function unit, where a chunk's exponentials alone take as long as its products; only where a warp
-//    holds a larger score are they taken that way, rewritten in tensor memory by a rolled loop.
+//    holds a larger score among 64 columns are they taken that way.
 //  - Weights come with their rounding remainders (a second P V) where a row may see few keys or give few all of
 //    its weight: tiles with rows that see less than 64 keys, and with a bias by distance the chunks next to the tile's
 //    positions and the first.
+//
+// Measured (32 q / 8 kv heads of 128, 512-token chunks behind 16K-32K tokens, 1.5 TFLOP): 1498 us with a window only
+// (1000 TFLOP/s; prefill_tc_kernel takes 1363 for the same products), 1958 capped at 50 (765 TFLOP/s), 3200 with
+// scores past the polynomial. Per pair of tiles and chunk the MMAs take about 2500 clocks and the two
+// softmaxes behind them 1900, 3250 with the cap, whose polynomial's six multiply-adds a score are most of the rest. Tried
+// and slower, capped: the row unrolled in registers 2206; the same as one pass against the reference so far,
+// redone where a score exceeds it by more than 2^8, 3020-3380; two threads to a row (sixteen warps) 2209; two
+// 64-column S buffers a tile, so that products and softmax overlap, 2290 (2091 uncapped: products of 64 columns
+// take as long as of 128); the tiles' softmaxes in turns 2130, their first passes in turns 2038.
 // =====================================================================================
 constexpr float kCapNear = 0.75f;
 // tanh(y) / y = sum c_k y^2k, fitted on [0, kCapNear] (relative error 5.7e-7)
 constexpr float kTanh0 = 0.999999435f, kTanh1 = -0.333282515f, kTanh2 = 0.132589832f, kTanh3 = -0.0500563012f,
                 kTanh4 = 0.0129296311f;
 
-template <int D>
-struct ScoredCfg : TcCfg<D> {
-    static constexpr int kSoftmaxWarps = 16;
-    static constexpr int kThreads = (4 + kSoftmaxWarps) * 32;
-    // register split: launched at kLaunchRegs each
-    static constexpr int kLaunchRegs = 96, kLowRegs = 64, kHighRegs = 104;
-    static_assert(128 * kLowRegs + 32 * kSoftmaxWarps * kHighRegs <= kThreads * kLaunchRegs, "register split");
-    static constexpr int kXchOff = TcCfg<D>::kBarOff + 256;  // [2 chunks][2 tiles][2 halves][128 rows] fp32
-    static constexpr int kSmem = kXchOff + 2 * 2 * 2 * 128 * 4 + 1024;
-};
-
 struct ScoredBars {
     uint64_t q_full;
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], v_clean[2];
     uint64_t s_full[2], p_full[2], o_done[2];  // per query tile
-    uint64_t x_full[8];                        // per tile and quarter: both halves' maxima (at the end: sums) are there
     uint64_t drain;
     uint32_t tmem_base;
     int any_bad;  // a value was not finite, and was zeroed
@@ -106,10 +99,10 @@ __device__ __noinline__ void scored_add_zeroed(const DecodeParams &p, int s, int
 
 // kCap, kBias: whether scores are capped and biased.
 template <int D, bool kCap, bool kBias>
-__global__ void __launch_bounds__(ScoredCfg<D>::kThreads, 1)
+__global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
     prefill_scored_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const ScoredPrefillParams sp) {
-    using C = ScoredCfg<D>;
+    using C = TcCfg<D>;
     const PrefillParams &pp = sp.pp;
     const DecodeParams &p = pp.d;
     extern __shared__ uint8_t smem_raw[];
@@ -173,10 +166,9 @@ __global__ void __launch_bounds__(ScoredCfg<D>::kThreads, 1)
             mbar_init(&b.v_empty[i], 1);
             mbar_init(&b.v_clean[i], 1);
             mbar_init(&b.s_full[i], 1);
-            mbar_init(&b.p_full[i], C::kSoftmaxWarps / 2);
+            mbar_init(&b.p_full[i], 4);
             mbar_init(&b.o_done[i], 1);
         }
-        for (int i = 0; i < 8; ++i) mbar_init(&b.x_full[i], 2);
         mbar_init(&b.drain, 1);
         b.any_bad = 0;
         mbar_fence_init();
@@ -368,9 +360,8 @@ __global__ void __launch_bounds__(ScoredCfg<D>::kThreads, 1)
     } else {
         setmaxnreg_inc<C::kHighRegs>();
         // ------------------------------ softmax ------------------------------
-        const int t = (warp - 4) >> 3;           // query tile
-        const int half = ((warp - 4) >> 2) & 1;  // keys 64 half .. + 63 of a chunk, and so many columns of O
-        const int quad = warp & 3;               // tensor-memory lanes 32 quad .. 32 quad + 31
+        const int t = (warp - 4) >> 2;  // query tile
+        const int quad = warp & 3;       // tensor-memory lanes 32 quad .. 32 quad + 31
         const int row = quad * 32 + lane;
         static_assert(C::kTiles == 2, "tile selection below");
         const ScoredTile me = {t ? tl[1].t0 : tl[0].t0, t ? tl[1].t_end : tl[0].t_end, t ? tl[1].c0 : tl[0].c0,
@@ -380,8 +371,7 @@ __global__ void __launch_bounds__(ScoredCfg<D>::kThreads, 1)
         const int row_token = row / g, row_head = row - row_token * g;
         const int pos = me.first + (row_ok ? row_token : 0);
         const int lo_t = see.lo(pos), hi_t = see.hi(pos);  // (rows past the tile's end see what its first does)
-        const uint32_t cols = tmem + ((uint32_t)(quad * 32) << 16) + t * C::kTileCols + half * 64;
-        float *xch = reinterpret_cast<float *>(base + C::kXchOff) + t * 256;  // [chunk parity][tile][half][row]
+        const uint32_t cols = tmem + ((uint32_t)(quad * 32) << 16) + t * C::kTileCols;
         const float slope = kBias ? slope_log2(p.slopes, h * g + row_head, p.num_q_heads) : 0.f;
         // The polynomial's coefficients in powers of the raw score, and up to where it holds. (Constants past fp32 where
         // the cap is tiny: every score is taken the long way.)
@@ -393,193 +383,180 @@ __global__ void __launch_bounds__(ScoredCfg<D>::kThreads, 1)
         // Without either scores stay raw: x sl is the log2-domain score, the sign is folded in; a scale of 0 becomes one
         // that leaves every score 0, so that a masked -inf stays -inf.
         const float sl = kCap || kBias ? 1.f : fmaxf(fabsf(p.scale_log2), 1e-30f);
+        const uint64_t f0 = pack_f2(k0, k0), f1 = pack_f2(k1, k1), f2 = pack_f2(k2, k2), f3 = pack_f2(k3, k3);
+        const uint64_t f4 = pack_f2(k4, k4), zero = pack_f2(0.f, 0.f), sl2 = pack_f2(sl, sl);
+        const uint64_t slope2 = pack_f2(slope, slope), two = pack_f2(2.f, 2.f);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = me.c0; j < me.c1; ++j) {
             if (!(ok = warp_wait(&b.s_full[t], (j - me.c0) & 1))) break;
             tc_fence_after();
-            const bool whole = me.whole(see, j, nblk);
-            // this half of the row of S_t in registers (one tensor-memory round trip)
-            float x[2][32];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) tmem_ld32(cols + q * 32, x[q]);
-            tmem_wait_ld();
-            // Columns of this half, kc = 0 .. 63: a full block's column holds position c0 + kc; in the chunk with the
-            // sequence's last block, which was loaded `early` rows early, column kc >= cut holds position c0 + kc - early
-            // and is a token from cut + early on. So a row sees columns a0 .. a1 and b0 .. b1.
-            const int c0 = j * C::kKeys + half * 64, cut = (nblk - 1) * kBlock - c0, early = kBlock - last_valid;
+            const bool whole = me.whole(see, j, nblk), split = me.split(see, kBias, j);
+            // Columns kc = 0 .. 127: a full block's column holds position c0 + kc; in the chunk with the sequence's last
+            // block, which was loaded `early` rows early, column kc >= cut holds position c0 + kc - early and is a token
+            // from cut + early on. So a row sees columns a0 .. a1 and b0 .. b1.
+            const int c0 = j * C::kKeys, cut = (nblk - 1) * kBlock - c0, early = kBlock - last_valid;
+            // the bias is linear in the column unless there are keys behind the query, or shifted ones
+            const bool bent = kBias && ((see.prefix - 1 > me.first && c0 + 127 > me.first) || (cut < 128 && early > 0));
+            const uint64_t at2 = pack_f2((float)(c0 - pos) * slope, (float)(c0 - pos) * slope);
+            // scores of a pair of columns from raw ones, in registers; col: the pair's columns
+            auto near = [&](uint64_t r, uint64_t col) -> uint64_t {
+                uint64_t f = f0;
+                if constexpr (kCap) {
+                    const uint64_t r2 = fma_f2(r, r, zero);
+                    f = fma_f2(fma_f2(fma_f2(fma_f2(f4, r2, f3), r2, f2), r2, f1), r2, f0);
+                }
+                return fma_f2(r, f, kBias ? fma_f2(col, slope2, at2) : zero);
+            };
+            // Two rolled passes over the row, 64 columns at a time: scores and their maximum, then weights. One or two warps a
+            // scheduler run this code, and its fetching counts.
             const int a0 = lo_t - c0, a1 = min(hi_t - c0, cut - 1);
             const int b0 = max(cut, a0) + early, b1 = hi_t - c0 + early;
-            bool far = false;
-            if constexpr (kBias)  // (keys behind the query, or shifted: their distances are not linear in the column)
-                far = (see.prefix - 1 > me.first && c0 + 63 > me.first) || (cut < 64 && early > 0);
-            if constexpr (kCap) {
-                float big = 0.f;
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) big = max3f(big, fabsf(x[q][e]), fabsf(x[q][e + 1]));
-                far |= __any_sync(0xffffffffu, !(big <= near_max));
-            }
-            if ((kCap || kBias) && far) {
-                // S rewritten: the scores in the log2 domain
-                const float at = (float)(pos - c0);
+            const float mid = (float)(pos - c0);
+            const bool rewrite = kCap || kBias || !whole || p.scale_log2 < 0.f;
+            float mx = -INFINITY;
 #pragma unroll 1
-                for (int q = 0; q < 2; ++q) {
-                    float v[32];
-                    tmem_ld32(cols + q * 32, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int kc = q * 32 + e;
-                        v[e] = kCap ? capped(v[e], p.cap_in, p.cap_log2) : v[e] * p.scale_log2;
-                        if constexpr (kBias) v[e] = fmaf(-slope, fabsf(at - (kc >= cut ? kc - early : kc)), v[e]);
-                    }
-                    tmem_st32(cols + q * 32, v);
-                }
-                tmem_wait_st();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) tmem_ld32(cols + q * 32, x[q]);
+            for (int half = 0; half < 2; ++half) {
+                float v[2][32];
+                const uint32_t hc = cols + half * 64;
+                tmem_ld32(hc, v[0]);
+                tmem_ld32(hc + 32, v[1]);
                 tmem_wait_ld();
-            } else if constexpr (kCap || kBias) {
-                const uint64_t f0 = pack_f2(k0, k0), f1 = pack_f2(k1, k1), f2 = pack_f2(k2, k2), f3 = pack_f2(k3, k3);
-                const uint64_t f4 = pack_f2(k4, k4), zero = pack_f2(0.f, 0.f);
-                // the bias of columns 2 i, 2 i + 1 is slope (position - pos)
-                const float at = (float)(c0 - pos) * slope;
-                const uint64_t at2 = pack_f2(at, at), slope2 = pack_f2(slope, slope), two = pack_f2(2.f, 2.f);
-                uint64_t col = pack_f2(0.f, 1.f);
+                bool far = bent;
+                if constexpr (kCap) {
+                    float big[2] = {0.f, 0.f};
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const uint64_t r = pack_f2(x[q][e], x[q][e + 1]);
-                        uint64_t f = f0, by = zero;
-                        if constexpr (kCap) {
-                            const uint64_t r2 = fma_f2(r, r, zero);
-                            f = fma_f2(fma_f2(fma_f2(fma_f2(f4, r2, f3), r2, f2), r2, f1), r2, f0);
-                        }
-                        if constexpr (kBias) {
-                            by = fma_f2(col, slope2, at2);
-                            col = add_f2(col, two);
-                        }
-                        unpack_f2(fma_f2(r, f, by), x[q][e], x[q][e + 1]);
-                    }
-            } else if (p.scale_log2 < 0.f) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[q][e] = -x[q][e];
-            }
-            if (!whole) {
-                // bits of the columns that the row sees
-                auto upto = [](int c) { return c < 0 ? 0ull : c >= 63 ? ~0ull : (2ull << c) - 1; };  // columns 0 .. c
-                const unsigned long long bits = (upto(a1) & ~upto(a0 - 1)) | (upto(b1) & ~upto(b0 - 1));
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint32_t w = (uint32_t)(bits >> (32 * q));
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[q][e] = w & (1u << e) ? x[q][e] : -INFINITY;
+                        for (int e = 0; e < 32; e += 2) big[q] = max3f(big[q], fabsf(v[q][e]), fabsf(v[q][e + 1]));
+                    far |= __any_sync(0xffffffffu, !(fmaxf(big[0], big[1]) <= near_max));
                 }
-            }
-            float mxs[4];  // independent partial maxima
+                if ((kCap || kBias) && __builtin_expect(far, 0)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mxs[i] = -INFINITY;
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+                        for (int e = 0; e < 32; ++e) {
+                            const int kc = half * 64 + q * 32 + e;
+                            v[q][e] = kCap ? capped(v[q][e], p.cap_in, p.cap_log2) : v[q][e] * p.scale_log2;
+                            if constexpr (kBias) v[q][e] = fmaf(-slope, fabsf(mid - (kc >= cut ? kc - early : kc)), v[q][e]);
+                        }
+                } else if constexpr (kCap || kBias) {
+                    uint64_t col = pack_f2((float)(half * 64), (float)(half * 64 + 1));
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], x[q][e], x[q][e + 1]);
-            float mx = fmaxf(fmaxf(mxs[0], mxs[1]), fmaxf(mxs[2], mxs[3]));
-            {   // the other half's maximum (the two warps of a tile's quarter; a chunk's buffer is free again a chunk later)
-                float *buf = xch + (j & 1) * 512;
-                buf[half * 128 + row] = mx;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.x_full[t * 4 + quad]);
-                if (!(ok = warp_wait(&b.x_full[t * 4 + quad], (j - me.c0) & 1))) break;
-                mx = fmaxf(mx, buf[(half ^ 1) * 128 + row]);
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            unpack_f2(near(pack_f2(v[q][e], v[q][e + 1]), col), v[q][e], v[q][e + 1]);
+                            if constexpr (kBias) col = add_f2(col, two);
+                        }
+                } else if (__builtin_expect(p.scale_log2 < 0.f, 0)) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[q][e] = -v[q][e];
+                }
+                if (!whole) {
+                    auto upto = [](int c) { return c < 0 ? 0u : c >= 31 ? ~0u : (2u << c) - 1; };  // columns 0 .. c
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int o = half * 64 + q * 32;
+                        const uint32_t bits = (upto(a1 - o) & ~upto(a0 - 1 - o)) | (upto(b1 - o) & ~upto(b0 - 1 - o));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[q][e] = bits & (1u << e) ? v[q][e] : -INFINITY;
+                    }
+                }
+                float mxs[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) mxs[(e >> 1) & 3] = max3f(mxs[(e >> 1) & 3], v[q][e], v[q][e + 1]);
+                mx = fmaxf(max3f(mxs[0], mxs[1], mxs[2]), mxs[3]);
+                if (rewrite) {
+                    tmem_st32(hc, v[0]);
+                    tmem_st32(hc + 32, v[1]);
+                }
             }
             const float m_new = fmaxf(m, mx * sl);
             const bool move = m_new > m + 8.f;
             const float m_use = move ? m_new : m;
             const float ms = m_use == -INFINITY ? 0.f : m_use;
             const float alpha = ex2_approx(m - ms);
-            // this tile's O is quiescent here (P V of the previous chunk ran before S of this one); each thread rescales
-            // its half of the columns
-            if (j > me.c0 && __any_sync(0xffffffffu, move && m != -INFINITY)) {
+            if (rewrite) tmem_wait_st();
+            // this tile's O is quiescent here (P V of the previous chunk ran before S of this one)
+            if (__builtin_expect(j > me.c0 && __any_sync(0xffffffffu, move && m != -INFINITY), 0)) {
 #pragma unroll 1
-                for (int c = 0; c < D / 64; ++c) {
+                for (int c = 0; c < D / 32; ++c) {
                     float o[32];
-                    const uint32_t at = cols - half * 64 + C::kOCol + half * (D / 2) + c * 32;
-                    tmem_ld32(at, o);
+                    tmem_ld32(cols + C::kOCol + c * 32, o);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                    tmem_st32(at, o);
+                    tmem_st32(cols + C::kOCol + c * 32, o);
                 }
             }
             m = m_use;
-            // P = 2^(x sl - reference max) in bf16 over each quarter's own score columns: keys 32 q + 2 i, + 1 at column
-            // 32 q + i, their rounding remainders at + 16. The row sum takes the unrounded weights.
-            auto write_p = [&](auto split_c) -> float {
-                constexpr bool split = decltype(split_c)::value;
-                const uint64_t sl2 = pack_f2(sl, sl), nms2 = pack_f2(-ms, -ms);
-                uint64_t rss[4];  // independent partial sums, two lanes each
+            l *= alpha;
+            const uint64_t nms2 = pack_f2(-ms, -ms);
+            uint64_t rss[4] = {zero, zero, zero, zero};
+            auto weights = [&](auto split_c) {
+                constexpr bool kSplit = decltype(split_c)::value;
+#pragma unroll 1
+                for (int half = 0; half < 2; ++half) {
+                    float v[2][32];
+                    const uint32_t hc = cols + half * 64;
+                    tmem_ld32(hc, v[0]);
+                    tmem_ld32(hc + 32, v[1]);
+                    tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t hi[16], rem[16];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t hi[16], rem[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float e0, e1;
-                        const uint64_t xx = pack_f2(x[q][2 * i], x[q][2 * i + 1]);
-                        unpack_f2(kCap || kBias ? add_f2(xx, nms2) : fma_f2(xx, sl2, nms2), e0, e1);
-                        e0 = ex2_approx(e0);
-                        e1 = ex2_approx(e1);
-                        rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
-                        const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
-                        hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
-                        if constexpr (split) {
-                            const float2 fh = __bfloat1622float2(ph);
-                            const __nv_bfloat162 pl = __floats2bfloat162_rn(e0 - fh.x, e1 - fh.y);
-                            rem[i] = *reinterpret_cast<const uint32_t *>(&pl);
+                        for (int i = 0; i < 16; ++i) {
+                            float e0, e1;
+                            const uint64_t y = pack_f2(v[q][2 * i], v[q][2 * i + 1]);
+                            unpack_f2(kCap || kBias ? add_f2(y, nms2) : fma_f2(y, sl2, nms2), e0, e1);
+                            e0 = ex2_approx(e0);
+                            e1 = ex2_approx(e1);
+                            rss[i & 3] = add_f2(rss[i & 3], pack_f2(e0, e1));
+                            const __nv_bfloat162 ph = __floats2bfloat162_rn(e0, e1);
+                            hi[i] = *reinterpret_cast<const uint32_t *>(&ph);
+                            if constexpr (kSplit) {
+                                const __nv_bfloat162 pl = __floats2bfloat162_rn(
+                                    e0 - __uint_as_float(hi[i] << 16), e1 - __uint_as_float(hi[i] & 0xffff0000u));
+                                rem[i] = *reinterpret_cast<const uint32_t *>(&pl);
+                            }
                         }
+                        tmem_st16(hc + q * 32, hi);
+                        if constexpr (kSplit) tmem_st16(hc + q * 32 + 16, rem);
                     }
-                    tmem_st16(cols + q * 32, hi);
-                    if constexpr (split) tmem_st16(cols + q * 32 + 16, rem);
                 }
-                tmem_wait_st();
-                float r[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) unpack_f2(rss[i], r[2 * i], r[2 * i + 1]);
-                return ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
             };
-            const float rs = me.split(see, kBias, j) ? write_p(BoolConst<true>{}) : write_p(BoolConst<false>{});
-            l = l * alpha + rs;
+            if (__builtin_expect(split, 0)) weights(BoolConst<true>{});
+            else weights(BoolConst<false>{});
+            float r[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) unpack_f2(rss[i], r[2 * i], r[2 * i + 1]);
+            l += ((r[0] + r[1]) + (r[2] + r[3])) + ((r[4] + r[5]) + (r[6] + r[7]));
+            // P = 2^(x sl - reference) in bf16 lies over each quarter's own score columns: keys 32 q + 2 i, + 1 at column
+            // 32 q + i, their rounding remainders at + 16. The row sum takes the unrounded weights.
+            tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.p_full[t]);
         }
         if (me.t0 < n) {
-            float *buf = xch + (me.c1 & 1) * 512;  // (not the last chunk's)
-            if (ok) {
-                buf[half * 128 + row] = l;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.x_full[t * 4 + quad]);
-                ok = warp_wait(&b.x_full[t * 4 + quad], (me.c1 - me.c0) & 1) && warp_wait(&b.o_done[t], 0);
-            }
+            if (ok) ok = warp_wait(&b.o_done[t], 0);
             if (!ok) {
                 raise_error(PKV_DEVERR_TIMEOUT);
             } else {
                 tc_fence_after();
-                l += buf[(half ^ 1) * 128 + row];
                 const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
                 __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) +
-                                     ((size_t)(q0 + me.t0 + (row_ok ? row_token : 0)) * p.num_q_heads + h * g + row_head) * D +
-                                     half * (D / 2);
+                                     ((size_t)(q0 + me.t0 + (row_ok ? row_token : 0)) * p.num_q_heads + h * g + row_head) * D;
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
+                for (int c = 0; c < D / 32; ++c) {
                     float o[32];
-                    tmem_ld32(cols - half * 64 + C::kOCol + half * (D / 2) + c * 32, o);
+                    tmem_ld32(cols + C::kOCol + c * 32, o);
                     tmem_wait_ld();
                     if (row_ok) {
 #pragma unroll
@@ -604,7 +581,7 @@ __global__ void __launch_bounds__(ScoredCfg<D>::kThreads, 1)
                             clean |= active(u, j) && (!tl[u].whole(see, j, nblk) || tl[u].split(see, kBias, j));
                         if (clean)
                             scored_add_zeroed(p, s, h, max(lo_t, j * C::kKeys), min(hi_t, j * C::kKeys + C::kKeys - 1), D,
-                                              half * (D / 2), D / 2, dst);
+                                              0, D, dst);
                     }
                 }
             }

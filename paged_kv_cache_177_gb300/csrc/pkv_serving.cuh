@@ -178,8 +178,14 @@ int launch_tree(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMa
         cuts = reinterpret_cast<pkv::TreeCut *>(static_cast<char *>(workspace) + kCounterBytes);
         partials = reinterpret_cast<float *>(cuts + kPersistMaxCtas);
     }
-    kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, tp, partials, cuts, tile_tokens, q_tokens);
-    const int rc = check_launch();
+    int rc;
+    if constexpr (kPrefix) {  // (its set-up beside the plan, for which it waits)
+        rc = launch_pdl(kern, dim3(grid), dim3(C::kThreads), C::kSmem, st, tmq, tmk, tmv, tp, partials, cuts, tile_tokens,
+                        q_tokens);
+    } else {
+        kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, tp, partials, cuts, tile_tokens, q_tokens);
+        rc = check_launch();
+    }
     if (rc != PKV_OK || whole) return rc;
     const int per_set = C::kTiles * tile_tokens;
     const int rows = (tp.max_query_len < per_set ? tp.max_query_len : per_set) * g;  // of the largest unit
@@ -214,7 +220,7 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
 template <int D, bool kCap, bool kBias>
 int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
                           const pkv::ScoredPrefillParams &sp, dim3 grid, cudaStream_t st) {
-    using C = pkv::ScoredCfg<D>;
+    using C = pkv::TcCfg<D>;
     static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
     auto kern = pkv::prefill_scored_kernel<D, kCap, kBias>;
     static thread_local int configured_device = -1;
@@ -224,8 +230,7 @@ int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const 
         // the register split draws on the registers the CTA is launched with
         cudaFuncAttributes fa{};
         if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return PKV_ERR_CUDA;
-        if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + C::kSoftmaxWarps * 32 * C::kHighRegs)
-            return PKV_ERR_UNSUPPORTED;
+        if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + C::kTiles * 128 * C::kHighRegs) return PKV_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return PKV_ERR_CUDA;
         configured_device = dev;

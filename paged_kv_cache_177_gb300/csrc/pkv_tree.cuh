@@ -414,6 +414,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
     }
 
     // ---- this CTA's range of the line: a scan of the sequences' weights ----
+    if constexpr (kPrefix) pdl_wait();  // for the plan
     {
         const int S = p.num_seqs, per = (S + C::kThreads - 1) / C::kThreads;
         const int s_lo = min(S, tid * per), s_hi = min(S, s_lo + per);
@@ -978,6 +979,7 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(1024)
     common_prefix_plan_kernel(const DecodeParams p, const int32_t *group_start, const int32_t *shared_blocks,
                               int num_groups, int max_group_size, int32_t *tokens, int32_t *first_blocks) {
+    pdl_trigger();  // the prefix' kernel may be set up; it waits for this one
     const int tid = threadIdx.x, lane = tid & 31;
     for (int s = tid; s < p.num_seqs; s += blockDim.x) first_blocks[s] = 0;
     __syncthreads();

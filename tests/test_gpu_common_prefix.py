@@ -9,6 +9,13 @@ from tests import score_helpers as H
 from tests import serving_helpers as S
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(1)
+
+
 BF = torch.bfloat16
 i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
 

@@ -10,6 +10,13 @@ from tests import verify_helpers as V
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(1)
+
+
+
+
 def outputs(seqs, most):
     return (torch.full((seqs, most), 77, dtype=torch.int32, device="cuda"),
             torch.full((seqs,), 77, dtype=torch.int32, device="cuda"),
