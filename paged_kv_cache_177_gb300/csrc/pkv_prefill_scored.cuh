@@ -20,9 +20,9 @@ struct ScoredPrefillParams {
 // Roles and pipelines are those of prefill_tc_kernel (a CTA per pair of 128-row tiles, K and V chunks in two-stage
 // rings, S and P in the same tensor-memory columns). What differs:
 //  - each tile has its own first and last chunk; the pair walks their union, in which there is no gap;
-//  - a warp cleans values: a row that does not see a key must not meet its NaN or infinity (0 times either is NaN),
-//    so in chunks that not every row sees whole such elements are zeroed before P V, and added at the end,
-//    element by element, to the rows that see them;
+//  - two warps clean values: a row that does not see a key must not meet its NaN or infinity (0 times either is NaN),
+//    so in blocks that not every row sees such elements are zeroed before P V, and added at the end, element by
+//    element, to the rows that see them;
 //  - capped scores come from a polynomial, raw Q(raw^2) with Q that of cap tanh(y) / raw, y = raw scale / cap, for
 //    |y| <= 3/4, 5.7e-7 of the score off. tanh by exponentials takes two more instructions a score on the
 //    special-function unit, where a chunk's exponentials alone take as long as its products; only where a warp
@@ -31,14 +31,16 @@ struct ScoredPrefillParams {
 //    its weight: tiles with rows that see less than 64 keys, and with a bias by distance the chunks next to the tile's
 //    positions and the first.
 //
-// Measured (32 q / 8 kv heads of 128, 512-token chunks behind 16K-32K tokens, 1.5 TFLOP): 1498 us with a window only
-// (1000 TFLOP/s; prefill_tc_kernel takes 1363 for the same products), 1958 capped at 50 (765 TFLOP/s), 3200 with
+// Measured (32 q / 8 kv heads of 128, 512-token chunks behind 16K-32K tokens, 1.5 TFLOP): 1471 us with nothing transformed
+// (1018 TFLOP/s; prefill_tc_kernel takes 1360), 2035 capped at 50 (735 TFLOP/s), 3195 with
 // scores past the polynomial. Per pair of tiles and chunk the MMAs take about 2500 clocks and the two
 // softmaxes behind them 1900, 3250 with the cap, whose polynomial's six multiply-adds a score are most of the rest. Tried
 // and slower, capped: the row unrolled in registers 2206; the same as one pass against the reference so far,
 // redone where a score exceeds it by more than 2^8, 3020-3380; two threads to a row (sixteen warps) 2209; two
 // 64-column S buffers a tile, so that products and softmax overlap, 2290 (2091 uncapped: products of 64 columns
 // take as long as of 128); the tiles' softmaxes in turns 2130, their first passes in turns 2038.
+// 32 prompts of 64-2048 tokens, window 1024, capped: 721 us (591 uncapped); with one warp that cleans whole chunks 830, two
+// 742, two that take only blocks with rows that are not seen 721.
 // =====================================================================================
 constexpr float kCapNear = 0.75f;
 // tanh(y) / y = sum c_k y^2k, fitted on [0, kCapNear] (relative error 5.7e-7)
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
             mbar_init(&b.k_empty[i], 1);
             mbar_init(&b.v_full[i], 1);
             mbar_init(&b.v_empty[i], 1);
-            mbar_init(&b.v_clean[i], 1);
+            mbar_init(&b.v_clean[i], 2);
             mbar_init(&b.s_full[i], 1);
             mbar_init(&b.p_full[i], 4);
             mbar_init(&b.o_done[i], 1);
@@ -321,35 +323,48 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
             mbar_wait(&b.drain, 0);
         }
         __syncwarp();
-      } else if (warp == 2) {
+      } else {
         // ------------------------------ values that not every row sees ------------------------------
         bool ok = true;
         for (int j = j0; j < j1 && ok; ++j) {
             const int r = j - j0, st = r & 1;
             if (!(ok = warp_wait(&b.v_full[st], (r >> 1) & 1))) break;
-            bool clean = false;
+            // blocks with positions that some row does not see: before `low` and after `high`
+            int low = INT_MIN, high = INT_MAX;
 #pragma unroll
             for (int t = 0; t < C::kTiles; ++t)
-                clean |= active(t, j) && (!tl[t].whole(see, j, nblk) || tl[t].split(see, kBias, j));
-            if (clean) {
-                uint8_t *vst = base + C::kVOff + st * C::kStage;
-                for (int i = lane; i < C::kStage / 16; i += 32) {
+                if (active(t, j)) {
+                    if (tl[t].split(see, kBias, j)) low = INT_MAX;  // (a remainder may be negative: the whole chunk)
+                    low = max(low, see.lo(tl[t].last));
+                    high = min(high, see.hi(tl[t].first));
+                }
+            const int blk0 = j * C::kChunkBlocks, blocks = min(C::kChunkBlocks, nblk - blk0);
+            const int upto = low > blk0 * kBlock ? min(blocks, (min(low, len) - 1) / kBlock + 1 - blk0) : 0;
+            const int from = high < len ? max(upto, (high + 1) / kBlock - blk0) : blocks;
+            uint8_t *vst = base + C::kVOff + st * C::kStage;
+            constexpr int kVecs = C::kBlockBytes / 16;
+            auto clean = [&](int b_lo, int b_hi) {
+#pragma unroll 1
+                for (int i = b_lo * kVecs + (warp - 2) * 32 + lane; i < b_hi * kVecs; i += 64) {
                     const uint4 v = reinterpret_cast<const uint4 *>(vst)[i];
                     const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t keep[4];
-                    bool bad = false;
+                    uint32_t bad[4];  // the top bit of each half whose exponent is all ones
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        keep[e] = ((x[e] & 0x7f80u) == 0x7f80u ? 0u : 0xffffu) |
-                                  ((x[e] & 0x7f800000u) == 0x7f800000u ? 0u : 0xffff0000u);
-                        bad |= keep[e] != ~0u;
-                    }
-                    if (bad) {
+                    for (int e = 0; e < 4; ++e) bad[e] = ((x[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+                    if ((bad[0] | bad[1]) | (bad[2] | bad[3])) {
+                        uint32_t keep[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            keep[e] = (bad[e] & 0x8000u ? 0u : 0xffffu) | (bad[e] & 0x80000000u ? 0u : 0xffff0000u);
                         reinterpret_cast<uint4 *>(vst)[i] =
                             make_uint4(x[0] & keep[0], x[1] & keep[1], x[2] & keep[2], x[3] & keep[3]);
                         *reinterpret_cast<volatile int *>(&b.any_bad) = 1;
                     }
                 }
+            };
+            if (upto > 0 || from < blocks) {
+                clean(0, upto);
+                clean(from, blocks);
                 fence_proxy_async_smem();
             }
             __syncwarp();
