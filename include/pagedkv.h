@@ -678,7 +678,8 @@ size_t pkv_common_prefix_workspace_bytes(int num_seqs, int num_q_heads, int num_
  * slopes: fp32 [num_q_heads], device, finite (NULL: none). softcap: finite, not
  *   negative (0: none). window: tokens (0: all). Every other argument, the
  *   workspace, an empty context and errors as for paged_decode_attention;
- *   dtype PKV_BF16 or PKV_F32. max_context_len bounds the contexts, not the window.
+ *   dtype PKV_BF16 or PKV_F32. max_context_len bounds the contexts, not the window;
+ *   the workspace is that of contexts of at most 16 ((window - 1) / 16 + 2) tokens.
  */
 int paged_decode_attention_scored(void *out, const void *q, const void *k_cache, const void *v_cache,
                                   const int32_t *block_tables, const int32_t *context_lens, float scale, float softcap,

@@ -993,7 +993,8 @@ def paged_decode_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: t
         max_context_len = int(context_lens.max().item()) if S else 0
     max_context_len = int(max_context_len)
     if workspace is None:
-        need = _workspace_bytes(S, Hq, Hkv, D, max_context_len, partition_tokens)
+        read = min(max_context_len, ((int(window) - 1) // 16 + 2) * 16) if window > 0 else max_context_len
+        need = _workspace_bytes(S, Hq, Hkv, D, read, partition_tokens)
         if need:
             with torch.cuda.stream(stream):       # zero-filled, on the call's stream
                 workspace = torch.zeros(need, dtype=torch.uint8, device=k_cache.device)

@@ -487,6 +487,11 @@ int score_params(pkv::DecodeParams &p, const ScoreArgs &a, float scale) {
     return PKV_OK;
 }
 
+// Tokens of a context that a call reads at most: a window of W tokens touches (W - 1) / 16 + 2 blocks at most.
+int read_context_len(int max_context_len, int window) {
+    return window > 0 ? (int)std::min<int64_t>(max_context_len, ((window - 1LL) / 16 + 2) * 16) : max_context_len;
+}
+
 // Shared by the decode entry points once the workspace is known.
 int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v_cache, const int32_t *block_tables,
                     const int32_t *context_lens, float scale, int num_kv_heads, int num_seqs, int num_q_heads,
@@ -946,10 +951,11 @@ int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
     const int pt = pkv_decode_partition_tokens(num_seqs, num_kv_heads, max_context_len, partition_tokens);
     if (pt % 16 != 0) return PKV_ERR_ARG;
-    const int mp = max_parts_for(max_context_len, pt);
+    const int read_len = read_context_len(max_context_len, scores ? scores->window : 0);
+    const int mp = max_parts_for(read_len, pt);
     const bool persistent = use_persistent(dtype, partition_tokens, num_seqs, num_kv_heads);
     if (!persistent && mp > kMaxParts) return PKV_ERR_UNSUPPORTED;
-    const size_t need = pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
+    const size_t need = pkv_decode_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, read_len,
                                                    partition_tokens);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
     if (mode == kCheckOnly) return PKV_OK;
@@ -988,13 +994,10 @@ int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v
                    : persistent_by_shape<__nv_bfloat16, ns128, ns64, nw, pkv::kWhole>(tmk, tmv, p, st, pdl, head_dim, g);
     }
 
-    const size_t grid_ws = grid_workspace_bytes(num_seqs, num_q_heads, head_dim, max_context_len, pt);
+    const size_t grid_ws = grid_workspace_bytes(num_seqs, num_q_heads, head_dim, read_len, pt);
     p.ws_ml = grid_ws ? reinterpret_cast<float *>(static_cast<char *>(workspace) + kCounterBytes) : nullptr;
     p.ws_o = grid_ws ? p.ws_ml + (size_t)num_seqs * num_q_heads * mp * 2 : nullptr;
-    int parts = mp;  // that a sequence can have: a window of W tokens touches at most (W - 2) / 16 + 2 blocks
-    if (scores && scores->window > 0)
-        parts = (int)std::min<long long>(mp, ((scores->window - 1LL) / 16 + 2 + p.part_blocks - 1) / p.part_blocks);
-    dim3 grid(parts, num_kv_heads, num_seqs);
+    dim3 grid(mp, num_kv_heads, num_seqs);
     int rc;
     if (dtype == PKV_BF16) {
         alignas(64) CUtensorMap tmk, tmv;
@@ -1010,7 +1013,7 @@ int decode_dispatch(void *out, const void *q, const void *k_cache, const void *v
         rc = head_dim == 128 ? launch_f32<128, pkv::kWhole>(p, grid, st, pdl)
                              : launch_f32<64, pkv::kWhole>(p, grid, st, pdl);
     }
-    if (rc != PKV_OK || parts <= 1) return rc;
+    if (rc != PKV_OK || mp <= 1) return rc;
     const pkv_dtype out_dt = f32_out ? PKV_F32 : dtype;
     if (scores)
         return head_dim == 128 ? launch_reduce<128, pkv::kScored>(p, out_dt, st)

@@ -114,6 +114,19 @@ def test_many_sequences_share_a_workspace_with_other_calls():
         run(14, [2000, 1], 8, 2, 128, BF, slopes=H.alibi(8), workspace=ws)
 
 
+@pytest.mark.parametrize("window", [1, 16, 17, 200])
+def test_a_windows_workspace_is_that_of_what_it_reads(window):
+    """A long context's window in as much workspace as the description says, and not a byte less."""
+    B = S.lib()
+    read = 16 * ((window - 1) // 16 + 2)
+    need = B.workspace_bytes(2, 8, 2, 64, min(read, 3000), 16)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    for n in (3000, 2991, 2990):
+        run(window, [n, 40], 8, 2, 64, BF, window=window, workspace=ws, partition_tokens=16)
+    with pytest.raises(B.PagedKVError):
+        run(window, [3000, 40], 8, 2, 64, BF, window=window, workspace=ws[:need - 16], partition_tokens=16)
+
+
 def test_bad_pages_in_the_window_read_as_zeros():
     B = S.lib()
     k, v, tables, kr, vr = H.paged(15, [100, 100], 2, 64, BF, window=50)

@@ -31,7 +31,8 @@ def test_decode_refusals(lib):
     assert f(S=-1) == ARG and f(hkv=0) == ARG and f(hq=33) == ARG and f(maxb=0) == ARG and f(maxlen=-1) == ARG
     assert f(part=-2) == ARG and f(part=17) == ARG and f(scale=NAN) == ARG and f(out=None) == ARG
     assert f(d=96) == UNSUPPORTED and f(hq=8 * 17) == UNSUPPORTED and f(dt=2) == UNSUPPORTED and f(dt=4) == UNSUPPORTED
-    assert f() == WORKSPACE                                                   # 128 tokens in partitions of 16
+    assert f(win=0) == WORKSPACE                                              # 128 tokens in partitions of 16
+    assert f(win=100) == WORKSPACE and f(win=100, ws=A, wsb=10240 + 4 * 32 * 8 * 130 * 4 - 1) == WORKSPACE
     assert f(S=0) == OK and f(S=0, slopes=None, cap=0.0, win=0) == OK
 
 
