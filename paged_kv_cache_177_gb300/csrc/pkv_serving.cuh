@@ -251,13 +251,15 @@ int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const 
 }
 
 // CTAs of the cluster that takes a sequence. Few sequences share their rows among up to eight CTAs, as long as all fit
-// the card at once (two an SM) and a CTA's warps have a step each; rows of more than 512 KB are shared anyway, so that the
-// sequences whose drafts are refused more than once, which read on when the others are done, take less long.
-// (With one, two, four and eight: 16 trees of 131072 tokens, p and q in fp32, 42, 27, 19.5, 15.9 us; 64 48, 32, 27, 27;
-// 256 79, 64, 62, 80; 64 of 32000 21, 17, 17, 23; without q, 64 rows of 131072 24, 17, 16, 22, 256 42, 42, 49, 72.)
-int verify_ctas(int num_seqs, int vocab, size_t row_bytes, int sms) {
+// the card at once (two an SM) and a CTA's warps have a step each; large rows are shared anyway, down to 512 KB of p a CTA, or
+// 128 KB each of p and q, which are read again for every further refusal while other sequences are done.
+// (With one, two, four and eight: trees of up to six drafts over 131072 tokens, fp32, 16 sequences 42, 27, 20, 16 us; 64 47,
+// 32, 27, 26; 128 60, 48, 41, 48; 256 79, 63, 60, 78; over 32000 64 21, 17, 17, 21, 256 30, 30, 41, 69; without q, over
+// 131072, 16 17, 13, 11, 11, 64 20, 16, 15, 22; 256 38, 40, 46, 69.)
+int verify_ctas(int num_seqs, int vocab, int elem, bool draft, int sms) {
+    const int64_t weight = (int64_t)vocab * elem * (draft ? 4 : 1);
     int c = 8;
-    while (c > 1 && (((long long)num_seqs * c > 2LL * sms && row_bytes <= (size_t)c << 18) || vocab < 2048LL * c)) c /= 2;
+    while (c > 1 && (((long long)num_seqs * c > 2LL * sms && weight < (int64_t)c << 19) || vocab < 2048LL * c)) c /= 2;
     return c;
 }
 
@@ -265,7 +267,7 @@ template <typename T>
 int launch_verify(const pkv::VerifyParams &p, int num_seqs, cudaStream_t st) {
     int sms = 0;
     if (sm_count(&sms) != PKV_OK) return PKV_ERR_CUDA;
-    const int c = verify_ctas(num_seqs, p.vocab, sizeof(T) * p.vocab * (p.draft ? 2 : 1), sms);
+    const int c = verify_ctas(num_seqs, p.vocab, sizeof(T), p.draft != nullptr, sms);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)num_seqs * c);
     cfg.blockDim = dim3(pkv::kVerifyThreads);

@@ -141,12 +141,13 @@ __device__ __forceinline__ Fixed warp_sum(Fixed x) {
 template <typename T, int E>
 __device__ __forceinline__ Fixed sum_residual(const T *p, const T *q, Multiple A, int lo, int hi, int vocab, bool vec,
                                               int lane) {
-    constexpr int kStep = 32 * E, kUnroll = sizeof(T) == 4 ? 4 : 2;
+    constexpr int kStep = 32 * E;
     Fixed sum = 0;
-    // the cuts of a round's elements are summed in 32 bits: at most 16 numbers of 22 bits
+    // the cuts of a round's elements are summed in 32 bits: at most 32 numbers of 22 bits
     uint32_t a = 0, b = 0;
     auto each = [&](auto with_q, auto add, auto flush) {
         constexpr bool kQ = decltype(with_q)::value;
+        constexpr int kUnroll = (kQ ? 16 : 32) / E;  // 32 registers of loads in flight
         int v0 = lo;
         if (vec) {
             for (; v0 + kStep * kUnroll <= hi; v0 += kStep * kUnroll) {
