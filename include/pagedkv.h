@@ -31,8 +31,11 @@
  *    Each cites its passage below.
  *  - Around them, for a serving loop: the cache in 8-bit floating point
  *    (kv_append_e4m3, dequantize_blocks, paged_decode_attention_e4m3), the
- *    pass from the projections to the cache (qk_norm_rope_append), and trees
- *    of drafted tokens (tree_masks, paged_tree_attention, kv_accept_layers).
+ *    pass from the projections to the cache (qk_norm_rope_append), trees
+ *    of drafted tokens (tree_masks, paged_tree_attention, verify_drafts,
+ *    kv_accept_layers), attention with transformed scores
+ *    (paged_decode_attention_scored, paged_prefill_attention_scored) and over a
+ *    prefix that many sequences share (paged_decode_attention_common_prefix).
  *
  * Conventions shared by every call
  * --------------------------------

@@ -5,8 +5,11 @@ The compute path is the CUDA library ``libpagedkv.so`` (C ABI in
 ``paged_decode_attention``, ``kv_append``, ``copy_blocks`` and the checks
 around them, and the serving calls beside those: the cache in 8-bit floating
 point (``kv_append_e4m3``, ``paged_decode_attention_e4m3``), the pass from the
-projections to the cache (``qk_norm_rope_append``) and trees of drafted tokens
-(``paged_tree_attention``, ``kv_accept_layers``).  ``block_manager`` and ``scheduler`` are the host-side paging and
+projections to the cache (``qk_norm_rope_append``), trees of drafted tokens
+(``paged_tree_attention``, ``verify_drafts``, ``kv_accept_layers``), attention
+with transformed scores (``paged_decode_attention_scored``,
+``paged_prefill_attention_scored``) and over a prefix that many sequences share
+(``paged_decode_attention_common_prefix``).  ``block_manager`` and ``scheduler`` are the host-side paging and
 continuous-batching logic that produce the calls' metadata; ``workloads``
 draws seeded synthetic inputs.
 

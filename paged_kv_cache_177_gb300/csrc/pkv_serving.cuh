@@ -1,6 +1,7 @@
 // pkv_serving.cuh -- host side of the serving calls around the cache: the
-// 8-bit cache, the pass from the projections to the cache, and trees of
-// drafted tokens. Included by pkv.cu, whose helpers it uses.
+// 8-bit cache, the pass from the projections to the cache, trees of drafted
+// tokens and their verification, transformed scores, and prefixes shared by
+// many sequences. Included by pkv.cu, whose helpers it uses.
 #pragma once
 
 namespace {

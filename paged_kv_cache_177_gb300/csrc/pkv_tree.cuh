@@ -1,6 +1,7 @@
 // pkv_tree.cuh -- drafted tokens: the mask of a tree from its parents,
 // attention of a tree's rows over the paged cache, and the move of the
-// accepted path's keys and values to consecutive positions.
+// accepted path's keys and values to consecutive positions. The attention
+// kernel also takes a prefix that many sequences share (kPrefix).
 #pragma once
 
 #include "pkv_prefill_tc.cuh"
@@ -973,8 +974,15 @@ __global__ void __launch_bounds__(256)
 }
 
 // =====================================================================================
-// A prefix shared by many sequences: what the two kernels behind it need to know, from one CTA. A group's prefix is
-// cut to the full blocks of its shortest sequence. tokens [num_groups], first_blocks [num_seqs].
+// A prefix shared by many sequences. A group's rows (sequence, query head) go through tree_attention_kernel as a tree
+// whose rows see all of the context and no drafts: 4 D flops a row and token against 4 D bytes a token for 256 rows of a
+// kv head, so from a few hundred rows on the tensor cores bound it. Each row's state (maximum, sum, unnormalised output,
+// fp32) is what the persistent decode kernel then starts the row's own blocks from, so nothing is joined at the end. 128 sequences
+// under 16384 tokens with 16-1024 own, 32 q / 8 kv heads: 113 us, of which the own blocks take 59 (as in plain
+// decode) and the prefix about 35; plain decode of all takes 650, groups of four that share their reads 692.
+//
+// The plan, from one CTA: a group's prefix cut to the full blocks of its shortest sequence. tokens [num_groups],
+// first_blocks [num_seqs].
 // =====================================================================================
 __global__ void __launch_bounds__(1024)
     common_prefix_plan_kernel(const DecodeParams p, const int32_t *group_start, const int32_t *shared_blocks,
