@@ -170,7 +170,7 @@ constexpr int kWhole = 0, kScored = 1, kBehindPrefix = 2;
 template <int FORM>
 __device__ __forceinline__ int first_block(const DecodeParams &p, int s, int len) {
     if constexpr (FORM == kScored) return p.window > 0 && len > p.window ? (len - p.window) / kBlock : 0;
-    else if constexpr (FORM == kBehindPrefix) return min(max(__ldg(p.first_blocks + s), 0), len / kBlock);
+    else if constexpr (FORM == kBehindPrefix) return min(__ldcg(p.first_blocks + s), len / kBlock);
     else return 0;
 }
 

@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) big[q] = max3f(big[q], fabsf(v[q][e]), fabsf(v[q][e + 1]));
-                    far |= __any_sync(0xffffffffu, !(fmaxf(big[0], big[1]) <= near_max));
+                    far |= __any_sync(0xffffffffu, row_ok && !(fmaxf(big[0], big[1]) <= near_max));
                 }
                 if ((kCap || kBias) && __builtin_expect(far, 0)) {
 #pragma unroll
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
             const float alpha = ex2_approx(m - ms);
             if (rewrite) tmem_wait_st();
             // this tile's O is quiescent here (P V of the previous chunk ran before S of this one)
-            if (__builtin_expect(j > me.c0 && __any_sync(0xffffffffu, move && m != -INFINITY), 0)) {
+            if (__builtin_expect(j > me.c0 && __any_sync(0xffffffffu, row_ok && move && m != -INFINITY), 0)) {
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];

@@ -546,8 +546,8 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
 
 // The workspace of paged_decode_attention_common_prefix: the decode workspace of the persistent kernel, the tree kernel's
 // records and states (its own counter header unused), the plan, and the rows' states of the prefix.
-static size_t common_prefix_states(int num_seqs, int num_q_heads, int head_dim) {
-    return (size_t)num_seqs * num_q_heads * (2 + (size_t)head_dim) * sizeof(float);
+static size_t common_prefix_sums(int num_seqs, int num_q_heads) {  // (the outputs behind them are written 16 bytes at a time)
+    return ((size_t)num_seqs * num_q_heads * 2 * sizeof(float) + 255) / 256 * 256;
 }
 static size_t common_prefix_plan_bytes(int num_seqs) { return (2 * (size_t)num_seqs * sizeof(int32_t) + 255) / 256 * 256; }
 static size_t common_prefix_tree_bytes(int head_dim) {
@@ -559,7 +559,7 @@ size_t pkv_common_prefix_workspace_bytes(int num_seqs, int num_q_heads, int num_
         return 0;
     return (persist_workspace_bytes(num_q_heads, num_kv_heads, head_dim) + 255) / 256 * 256 +
            common_prefix_tree_bytes(head_dim) + common_prefix_plan_bytes(num_seqs) +
-           common_prefix_states(num_seqs, num_q_heads, head_dim);
+           common_prefix_sums(num_seqs, num_q_heads) + (size_t)num_seqs * num_q_heads * head_dim * sizeof(float);
 }
 
 int paged_decode_attention_common_prefix(void *out, const void *q, const void *k_cache, const void *v_cache,
@@ -593,7 +593,8 @@ int paged_decode_attention_common_prefix(void *out, const void *q, const void *k
     ws += common_prefix_tree_bytes(head_dim);
     int32_t *tokens = reinterpret_cast<int32_t *>(ws), *first_blocks = tokens + num_seqs;
     ws += common_prefix_plan_bytes(num_seqs);
-    float *prefix_ml = reinterpret_cast<float *>(ws), *prefix_o = prefix_ml + 2 * (size_t)num_seqs * num_q_heads;
+    float *prefix_ml = reinterpret_cast<float *>(ws);
+    float *prefix_o = reinterpret_cast<float *>(ws + common_prefix_sums(num_seqs, num_q_heads));
     p.first_blocks = first_blocks;
     p.prefix_ml = prefix_ml;
     p.prefix_o = prefix_o;

@@ -179,7 +179,8 @@ struct TreeWalk {
     // Positions of sequence s; flag: whether this call reports bad lengths and row counts.
     __device__ __forceinline__ static long long weigh(const TreeParams &tp, int s, int per_set, bool flag, int &len,
                                                 int &q0, int &n) {
-        len = seq_len(tp.d, s, flag);
+        // (a prefix' tokens come from the kernel before, beside which this one was started)
+        len = kPrefix ? __ldcg(tp.d.context_lens + s) : seq_len(tp.d, s, flag);
         if (!tree_rows(tp.query_start, s, kPrefix ? INT_MAX : len, tp.max_query_len, tp.num_queries, q0, n)) {
             if (flag) raise_error(PKV_DEVERR_LENGTH);
             n = 0;

@@ -94,6 +94,17 @@ def test_groups_of_every_size(seqs):
     run(seqs, [0, seqs], lens, [10], 4, 4, 64)
 
 
+@pytest.mark.parametrize("seqs,hq,hkv", [(3, 15, 5), (23, 15, 5), (1, 7, 1), (5, 3, 1), (7, 5, 5)])
+def test_an_odd_number_of_rows(seqs, hq, hkv):
+    """The workspace's parts stay aligned whatever lies before them; whole prefixes, and prefixes cut among workers."""
+    rng = np.random.default_rng(seqs)
+    for d in (64, 128):
+        for shared in (2, 3, 70):
+            lens = [16 * shared + int(x) for x in rng.integers(0, 13, seqs)]
+            run(seqs, [0, seqs], lens, [shared], hq, hkv, d)
+            run(seqs, [0, (seqs + 1) // 2, seqs], lens, [shared, shared], hq, hkv, d)
+
+
 def test_contexts_that_end_with_the_prefix():
     """Nothing behind the prefix: the output is the prefix' alone, cut or not."""
     run(1, [0, 5], [160] * 5, [10], 8, 2, 64)

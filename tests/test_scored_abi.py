@@ -67,6 +67,10 @@ def test_common_prefix_refusals(lib):
     g.restype, g.argtypes = SZ, [CI] * 4
     assert g(0, 8, 2, 64) == 0 and g(4, 9, 2, 64) == 0
     assert g(8, 8, 2, 64) - g(4, 8, 2, 64) == 4 * 8 * 66 * 4
+    for s in range(1, 70):                     # sums of an odd number of rows are padded to where outputs are aligned
+        for hq in (3, 5, 7, 8):
+            rest = g(s, hq, 1, 64) - s * hq * 64 * 4
+            assert rest % 256 == 0 and rest - (g(1, hq, 1, 64) - hq * 64 * 4) >= s * hq * 8 - 256
 
 
 def test_the_form_by_hand():
