@@ -3,6 +3,8 @@
 // to a window, over a prefix that is seen from both sides.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "pkv_prefill_tc.cuh"
 
 namespace pkv {
@@ -10,6 +12,7 @@ namespace pkv {
 struct ScoredPrefillParams {
     PrefillParams pp;
     const int32_t *prefix_lens;  // [num_seqs] or null
+    int ctas;                    // CTAs of the cluster that takes a pair of tiles
 };
 
 // =====================================================================================
@@ -39,6 +42,10 @@ struct ScoredPrefillParams {
 // redone where a score exceeds it by more than 2^8, 3020-3380; two threads to a row (sixteen warps) 2209; two
 // 64-column S buffers a tile, so that products and softmax overlap, 2290 (2091 uncapped: products of 64 columns
 // take as long as of 128); the tiles' softmaxes in turns 2130, their first passes in turns 2038.
+// Where pairs of tiles are few, a cluster of CTAs takes each: a CTA takes a run of the pair's chunks as if there were no
+// others and leaves its rows' O, not yet divided, with their references and sums in its shared memory, whose rings are
+// free by then; the cluster's CTAs then share the rows and join what all of them left through distributed shared memory.
+// (16 tokens behind 16K, capped, 32 q / 8 kv heads of 128: 333 us with a CTA to a pair, 53 with eight.)
 // 32 prompts of 64-2048 tokens, window 1024, capped: 721 us (591 uncapped); with one warp that cleans whole chunks 830, two
 // 742, two that take only blocks with rows that are not seen 721.
 // =====================================================================================
@@ -56,6 +63,16 @@ struct ScoredBars {
     int any_bad;  // a value was not finite, and was zeroed
 };
 static_assert(sizeof(ScoredBars) <= 256, "barrier area");
+
+// What a CTA of a cluster leaves of its pair of tiles, over the staging areas: O by row, padded so that threads with a row
+// each write to different banks; and the rows' references and sums.
+template <int D>
+struct ScoredPart {
+    static constexpr int kPitch = D + 4;
+    float o[2][128][kPitch];
+    float2 ml[2][128];
+    static_assert(sizeof(float) * 2 * 128 * (kPitch + 2) <= TcCfg<D>::kBarOff, "staging areas");
+};
 
 // What a sequence's rows see.
 struct Sight {
@@ -99,6 +116,67 @@ __device__ __noinline__ void scored_add_zeroed(const DecodeParams &p, int s, int
     }
 }
 
+// All threads of the cluster's CTAs, each of which comes here at the end of its bounded waits.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Joins what the cluster's CTAs left of a pair of tiles that starts at token t0. Every CTA takes each ctas-th row, eight lanes
+// to a row, so that a warp has the loads of four rows under way.
+template <int D>
+__device__ __noinline__ void scored_join(const DecodeParams &p, Sight see, ScoredPart<D> &part, int *any_bad, int ctas,
+                                         int rank, int warp, int lane, int s, int h, int q0, int n, int t0, int tt,
+                                         int first_pos) {
+    namespace cg = cooperative_groups;
+    constexpr int kVecs = D / 32;  // float4s of a lane: columns 4 sub + 32 v
+    cg::cluster_group cluster = cg::this_cluster();
+    const int g = p.group, tile_rows = tt * g, sub = lane & 7;
+    const int rows = (min(n, t0 + 2 * tt) - t0) * g;  // of both tiles
+    const int bad = sub < ctas ? *cluster.map_shared_rank(any_bad, sub) : 0;
+#pragma unroll 1
+    for (int base = rank + warp * 4 * ctas; base < rows; base += 32 * ctas) {
+        const int i = base + (lane >> 3) * ctas;
+        const bool mine = i < rows;
+        const int t = mine && i >= tile_rows, row = mine ? i - t * tile_rows : 0;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (mine && sub < ctas) ml = cluster.map_shared_rank(&part, sub)->ml[t][row];
+        float ms = ml.x;
+#pragma unroll
+        for (int d = 4; d; d >>= 1) ms = fmaxf(ms, __shfl_xor_sync(0xffffffffu, ms, d));
+        const float w = ex2_approx(ml.x - (ms == -INFINITY ? 0.f : ms));
+        float l = 0.f;
+        float4 o[kVecs] = {};
+#pragma unroll 2
+        for (int r = 0; r < ctas; ++r) {
+            const float wr = __shfl_sync(0xffffffffu, w, r, 8), lr = __shfl_sync(0xffffffffu, ml.y, r, 8);
+            if (lr == 0.f) continue;  // the row saw nothing there
+            l = fmaf(wr, lr, l);
+            const float4 *src = reinterpret_cast<const float4 *>(cluster.map_shared_rank(&part, r)->o[t][row]) + sub;
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const float4 x = src[v * 8];
+                o[v] = make_float4(fmaf(wr, x.x, o[v].x), fmaf(wr, x.y, o[v].y), fmaf(wr, x.z, o[v].z), fmaf(wr, x.w, o[v].w));
+            }
+        }
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // (NaN stays)
+        const int token = t0 + i / g, head = h * g + i % g;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.out) + ((size_t)(q0 + token) * p.num_q_heads + head) * D + sub * 4;
+        if (mine)
+#pragma unroll
+            for (int v = 0; v < kVecs; ++v) {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(o[v].x * inv, o[v].y * inv);
+                const __nv_bfloat162 c = __floats2bfloat162_rn(o[v].z * inv, o[v].w * inv);
+                *reinterpret_cast<uint2 *>(dst + v * 32) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&c));
+            }
+        // what was zeroed shows in its element of the rows that see it (what was not shows already)
+        if (__builtin_expect(__any_sync(0xffffffffu, bad != 0), 0) && mine)
+            for (int v = 0; v < kVecs; ++v)
+                scored_add_zeroed(p, s, h, see.lo(first_pos + token), see.hi(first_pos + token), D, sub * 4 + v * 32, 4,
+                                  dst + v * 32);
+    }
+}
+
 // kCap, kBias: whether scores are capped and biased.
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
@@ -109,7 +187,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
     const DecodeParams &p = pp.d;
     extern __shared__ uint8_t smem_raw[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int h = blockIdx.x;
+    const int ctas = sp.ctas, h = blockIdx.x / ctas, rank = blockIdx.x - h * ctas;
     int s, pair;
     if (pp.seq_major) {
         pair = gridDim.y - 1 - blockIdx.y;
@@ -118,7 +196,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         s = blockIdx.y;
         pair = gridDim.z - 1 - blockIdx.z;
     }
-    const bool flagger = h == 0 && pair == 0;  // one CTA per sequence reports bad lengths
+    const bool flagger = blockIdx.x == 0 && pair == 0;  // one CTA per sequence reports bad lengths
     const int g = p.group;
     const int q0 = __ldg(pp.query_start + s);
     const long long nn = (long long)__ldg(pp.query_start + s + 1) - q0;
@@ -129,7 +207,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
     see.prefix = min(max(see.prefix, 0), len);
     if (nn < 0 || nn > len || nn > pp.max_query_len || q0 < 0 || q0 + nn > pp.num_queries) {
         if (tid == 0 && flagger) raise_error(PKV_DEVERR_LENGTH);
-        return;
+        return;  // (the whole cluster, as below)
     }
     const int n = (int)nn;
     if (pair * C::kTiles * tt >= n) return;
@@ -149,7 +227,17 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
             x.c0 = x.c1 = tl[0].c1;  // (an empty second tile)
         }
     }
-    const int j0 = tl[0].c0, j1 = max(tl[0].c1, tl[1].c1);
+    int j0 = tl[0].c0, j1 = max(tl[0].c1, tl[1].c1);
+    if (ctas > 1) {  // this CTA's run of the chunks, which may be empty
+        const int chunks = j1 - j0, from = j0;
+        j0 = from + (int)((long long)chunks * rank / ctas);
+        j1 = from + (int)((long long)chunks * (rank + 1) / ctas);
+#pragma unroll
+        for (int t = 0; t < C::kTiles; ++t) {
+            tl[t].c0 = min(max(tl[t].c0, j0), j1);
+            tl[t].c1 = max(min(tl[t].c1, j1), tl[t].c0);
+        }
+    }
     const int nblk = (len + kBlock - 1) / kBlock;
     const int last_valid = len - (nblk - 1) * kBlock;
     const int first_blk = see.lo(tl[0].first) / kBlock;  // blocks before it are not read
@@ -190,7 +278,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
       setmaxnreg_dec<C::kLowRegs>();
       if (warp == 0) {
         // ------------------------------ TMA producer ------------------------------
-        if (lane == 0) {
+        if (lane == 0 && j0 < j1) {
             bool ok = true;
             int qbytes = 0;
 #pragma unroll
@@ -260,7 +348,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         }
       } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0) {
+        if (lane == 0 && j0 < j1) {
             constexpr uint32_t idesc_s = idesc_bf16_f32(C::kRows, C::kKeys, false, false);
             constexpr uint32_t idesc_o = idesc_bf16_f32(C::kRows, D, false, true);
             auto issue_s = [&](int t, int r) {
@@ -371,6 +459,10 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(&b.v_clean[st]);
         }
         if (!ok && lane == 0) raise_error(PKV_DEVERR_TIMEOUT);
+      }
+      if (ctas > 1) {
+          __syncwarp();
+          cluster_barrier();
       }
     } else {
         setmaxnreg_inc<C::kHighRegs>();
@@ -559,7 +651,33 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.p_full[t]);
         }
-        if (me.t0 < n) {
+        if (ctas > 1) {
+            // both tiles are through with the staging areas
+#pragma unroll
+            for (int u = 0; u < C::kTiles; ++u)
+                if (ok && tl[u].c0 < tl[u].c1) ok = warp_wait(&b.o_done[u], 0);
+            if (!ok) raise_error(PKV_DEVERR_TIMEOUT);
+            tc_fence_after();
+            ScoredPart<D> &part = *reinterpret_cast<ScoredPart<D> *>(base);
+            const bool some = ok && me.c0 < me.c1;
+            if (row_ok) part.ml[t][row] = some ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+            if (some) {
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32(cols + C::kOCol + c * 32, o);
+                    tmem_wait_ld();
+                    if (row_ok) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(&part.o[t][row][c * 32 + e]) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+            }
+            cluster_barrier();
+            scored_join<D>(p, see, part, &b.any_bad, ctas, rank, warp - 4, lane, s, h, q0, n, tl[0].t0, tt, first_pos);
+        } else if (me.t0 < n) {
             if (ok) ok = warp_wait(&b.o_done[t], 0);
             if (!ok) {
                 raise_error(PKV_DEVERR_TIMEOUT);
@@ -608,6 +726,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, C::kTmemCols);
     }
+    if (ctas > 1) cluster_barrier();  // no CTA leaves while others read what it left
 }
 
 }  // namespace pkv

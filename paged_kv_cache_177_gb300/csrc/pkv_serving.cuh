@@ -218,13 +218,43 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
     return check_launch();
 }
 
+// CTAs of the cluster that takes a pair of query tiles: pairs, of which there are so many at most, each over `chunks` chunks
+// at most; resident[i]: clusters of 2^i CTAs that the card holds. A round of clusters is taken to last as long as the
+// chunks of one of its CTAs and eight more; up to three chunks, joining costs more than it saves.
+// (With one, two, four and eight, 32 q / 8 kv heads of 128, capped: 16 tokens behind 16K 333, 173, 93, 53 us, behind 1K 27,
+// 18, 14, 13; 512 behind 8K 197, 110, 124, 199; 8 x 64 behind 1K 34, 27, 43, 95, behind 4K 105, 63, 79, 142; 24 x 64 behind 4K
+// 208, 183, 228, 371; 18 x 64 107, 124, 156, 285; prompts of 256 13.4, 15.0, 14.9, 41, of 512 20, 19, 30, 71, of 768 26, 32, 48, 105.
+// The card holds 76, 36 and 15 clusters of two, four and eight.)
+int prefill_scored_ctas(long long pairs, long long chunks, const int (&resident)[4]) {
+    int best = 0;
+    long long least = 0;
+    for (int i = 0; i < (chunks > 3 ? 4 : 1) && resident[i] > 0; ++i) {
+        const long long c = 1 << i, rounds = (pairs + resident[i] - 1) / resident[i];
+        const long long cost = rounds * ((chunks + c - 1) / c + 8);
+        if (i == 0 || cost < least) {
+            best = i;
+            least = cost;
+        }
+    }
+    return 1 << best;
+}
+
 template <int D, bool kCap, bool kBias>
 int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                          const pkv::ScoredPrefillParams &sp, dim3 grid, cudaStream_t st) {
+                          pkv::ScoredPrefillParams sp, dim3 grid, long long pairs, long long chunks, cudaStream_t st) {
     using C = pkv::TcCfg<D>;
     static_assert(C::kSmem <= (int)kSmemLimit, "shared memory");
     auto kern = pkv::prefill_scored_kernel<D, kCap, kBias>;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     static thread_local int configured_device = -1;
+    static thread_local int resident[4];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     if (configured_device != dev) {
@@ -234,21 +264,36 @@ int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const 
         if (fa.numRegs * C::kThreads < 128 * C::kLowRegs + C::kTiles * 128 * C::kHighRegs) return PKV_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem) != cudaSuccess)
             return PKV_ERR_CUDA;
+        if (sm_count(&resident[0]) != PKV_OK) return PKV_ERR_CUDA;
+        for (int i = 1; i < 4; ++i) {
+            attr[0].val.clusterDim.x = 1 << i;
+            cfg.gridDim = dim3(1 << i);
+            if (cudaOccupancyMaxActiveClusters(&resident[i], kern, &cfg) != cudaSuccess) return PKV_ERR_CUDA;
+        }
         configured_device = dev;
     }
-    kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, sp);
-    return check_launch();
+    sp.ctas = prefill_scored_ctas(pairs, chunks, resident);
+    if (sp.ctas == 1) {
+        kern<<<grid, C::kThreads, C::kSmem, st>>>(tmq, tmk, tmv, sp);
+        return check_launch();
+    }
+    grid.x *= sp.ctas;
+    cfg.gridDim = grid;
+    cfg.stream = st;
+    attr[0].val.clusterDim.x = sp.ctas;
+    return cudaLaunchKernelEx(&cfg, kern, tmq, tmk, tmv, sp) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 template <int D>
 int launch_prefill_scored(const CUtensorMap &tmq, const CUtensorMap &tmk, const CUtensorMap &tmv,
-                          const pkv::ScoredPrefillParams &sp, dim3 grid, cudaStream_t st) {
+                          const pkv::ScoredPrefillParams &sp, dim3 grid, long long pairs, long long chunks,
+                          cudaStream_t st) {
     const bool bias = sp.pp.d.slopes != nullptr;
     if (sp.pp.d.cap_log2 != 0.f)
-        return bias ? launch_prefill_scored<D, true, true>(tmq, tmk, tmv, sp, grid, st)
-                    : launch_prefill_scored<D, true, false>(tmq, tmk, tmv, sp, grid, st);
-    return bias ? launch_prefill_scored<D, false, true>(tmq, tmk, tmv, sp, grid, st)
-                : launch_prefill_scored<D, false, false>(tmq, tmk, tmv, sp, grid, st);
+        return bias ? launch_prefill_scored<D, true, true>(tmq, tmk, tmv, sp, grid, pairs, chunks, st)
+                    : launch_prefill_scored<D, true, false>(tmq, tmk, tmv, sp, grid, pairs, chunks, st);
+    return bias ? launch_prefill_scored<D, false, true>(tmq, tmk, tmv, sp, grid, pairs, chunks, st)
+                : launch_prefill_scored<D, false, false>(tmq, tmk, tmv, sp, grid, pairs, chunks, st);
 }
 
 // CTAs of the cluster that takes a sequence. Few sequences share their rows among up to eight CTAs, as long as all fit
@@ -683,8 +728,12 @@ int paged_prefill_attention_scored(void *out, const void *q, const void *k_cache
     if ((rc = encode_cache_map(&tmk, k_cache, num_blocks, num_kv_heads, head_dim, true)) != PKV_OK) return rc;
     if ((rc = encode_cache_map(&tmv, v_cache, num_blocks, num_kv_heads, head_dim)) != PKV_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return head_dim == 128 ? launch_prefill_scored<128>(tmq, tmk, tmv, sp, grid, st)
-                           : launch_prefill_scored<64>(tmq, tmk, tmv, sp, grid, st);
+    // At most so many pairs hold tokens. A pair sees its tokens and what the window leaves before them and, under
+    // prefixes, behind.
+    const long long in_use = num_kv_heads * std::min(pairs * num_seqs, num_queries / (2LL * tile_tokens) + num_seqs);
+    const long long seen = std::min<long long>(max_context_len, 2LL * tile_tokens + (prefix_lens ? 2LL : 1LL) * pp.d.window);
+    return head_dim == 128 ? launch_prefill_scored<128>(tmq, tmk, tmv, sp, grid, in_use, seen / 128 + 1, st)
+                           : launch_prefill_scored<64>(tmq, tmk, tmv, sp, grid, in_use, seen / 128 + 1, st);
 }
 
 int verify_drafts(int32_t *accepted, int max_accepted, int32_t *num_accepted, int64_t *next_tokens,
