@@ -1059,6 +1059,64 @@ __device__ __forceinline__ void merge_segments(const float *partials, size_t slo
     }
 }
 
+// The same for units cut into many segments or of many heads: the states of all heads are taken in one row, 32 maxima and
+// sums at a time (the next ones on their way) and eight outputs, so that the merge waits for memory g nseg / 8 times.
+template <int D, typename OutT>
+__device__ __noinline__ void merge_segments_wide(const float *partials, size_t slot_floats, int w1, int nseg, int g,
+                                                 OutT *out_rows, int lane) {
+    constexpr int PER = D / 32;
+    const int count = g * nseg;
+    auto seg_row = [&](int x) {  // of head x / nseg and segment x % nseg
+        const int head = x / nseg, k = x - head * nseg;
+        return partials + (size_t)(2 * (w1 + k) + (k == 0 ? 1 : 0)) * slot_floats + (size_t)head * (2 + D);
+    };
+    auto sums = [&](int x0) -> float2 {
+        const float *r = seg_row(min(x0 + lane, count - 1));
+        return make_float2(__ldcg(r), __ldcg(r + 1));
+    };
+    float2 next = sums(0), ml{};
+    float M = -INFINITY, L = 0.f, acc[PER] = {};
+    int head = 0, k = 0;
+    for (int x0 = 0; x0 < count; x0 += 8) {
+        if ((x0 & 31) == 0) {
+            ml = next;
+            if (x0 + 32 < count) next = sums(x0 + 32);
+        }
+        float v[8][PER];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            const float *r = seg_row(min(x0 + y, count - 1)) + 2 + lane;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) v[y][i] = __ldcg(r + 32 * i);
+        }
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+            if (x0 + y >= count) break;
+            const float mx = __shfl_sync(0xffffffffu, ml.x, (x0 + y) & 31), lx = __shfl_sync(0xffffffffu, ml.y, (x0 + y) & 31);
+            if (lx != 0.f) {  // (else the row sees nothing there)
+                const float m_new = fmaxf(M, mx), ms = m_new == -INFINITY ? 0.f : m_new;
+                const float a = ex2_approx(M - ms), c = ex2_approx(mx - ms);
+                L = fmaf(L, a, lx * c);
+#pragma unroll
+                for (int i = 0; i < PER; ++i) acc[i] = fmaf(acc[i], a, v[y][i] * c);
+                M = m_new;
+            }
+            if (++k == nseg) {
+                const float inv = 1.f / L;
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    out_rows[(size_t)head * D + lane + 32 * i] = to_out<OutT>(acc[i] * inv);
+                    acc[i] = 0.f;
+                }
+                M = -INFINITY;
+                L = 0.f;
+                k = 0;
+                ++head;
+            }
+        }
+    }
+}
+
 // WA: the per-block step -- WarpAttn (tensor cores, any group up to 8 NT) or
 // WarpAttnScalar (CUDA cores, one query head per kv head).
 template <int D, int NT, int NS, int NW, typename OutT = __nv_bfloat16, class WA = WarpAttn<D, NT>, int FORM = kWhole>
@@ -1135,8 +1193,18 @@ __global__ void __launch_bounds__(NW * 32, 1)
     // W = min(warps, T) workers, so every worker's range is non-empty and the
     // workers covering a unit are consecutive
     const long long T = (long long)Hkv * prefix[S];
-    const int W = (int)min((long long)gridDim.x * NW, T);
-    const int w = blockIdx.x * NW + warp;
+    long long parts = T;
+    if constexpr (FORM == kBehindPrefix) {
+        // Own contexts may be few and short, or few and long, and W workers would cut each into many segments: a worker takes
+        // at least so many blocks that its chain of them and the merge of its unit's g heads' segments take about as long.
+        // (6 sequences of one kv head, 7 query heads, 2.3-2.8K own tokens: a block or two each 215 us, four 69, eight 50,
+        // this rule's sixteen 48; 26 of two, 16 query heads, 0.7-1.6K: 101, 101, 75, 69; 9 of eight, 4 query heads, 74-243: 30,
+        // 25 with this rule's three.) And workers that follow one another are on different SMs.
+        const int least = max(1, (int)sqrtf(0.25f * (float)g * (float)prefix[S] / (float)S));
+        parts = (T + least - 1) / least;
+    }
+    const int W = (int)min((long long)gridDim.x * NW, parts);
+    const int w = FORM == kBehindPrefix ? warp * gridDim.x + blockIdx.x : blockIdx.x * NW + warp;
     if (w >= W) return;
     const long long start = T * w / W, end = T * (w + 1) / W;
     const int cnt = (int)(end - start);
@@ -1316,7 +1384,10 @@ __global__ void __launch_bounds__(NW * 32, 1)
             prev = __shfl_sync(0xffffffffu, prev, 0);
             if (prev == w2 - w1) {
                 __syncwarp();  // lane 0's acquire covers the lanes reading the other segments
-                merge_segments<D, OutT>(p.partials, slot_floats, w1, w2 - w1 + 1, g, out + orow0 * D, lane);
+                if constexpr (FORM == kBehindPrefix)
+                    merge_segments_wide<D, OutT>(p.partials, slot_floats, w1, w2 - w1 + 1, g, out + orow0 * D, lane);
+                else
+                    merge_segments<D, OutT>(p.partials, slot_floats, w1, w2 - w1 + 1, g, out + orow0 * D, lane);
                 if (lane == 0) p.counters[w1] = 0;  // ready for the next call
             }
         }
