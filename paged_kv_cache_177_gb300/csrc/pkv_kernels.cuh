@@ -2430,6 +2430,45 @@ __global__ void __launch_bounds__(D *PG) lse_reduce_kernel(const DecodeParams p)
     }
 }
 
+// The same, up to 32 partitions, a warp to a row: batches of many rows, where 512 threads and two of their reductions a
+// row would take longer than the rows' partitions (140 sequences of 32 query heads in two: the call 47 us, so 29). Started while the kernel before ends.
+constexpr int kFewParts = 32, kFewRows = 8;
+
+template <typename OutT, int D, int FORM>
+__global__ void __launch_bounds__(32 * kFewRows) lse_reduce_few_kernel(const DecodeParams p) {
+    constexpr int PER = D / 32;
+    const long long row = (long long)blockIdx.x * kFewRows + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    pdl_wait();
+    if (row >= (long long)p.num_seqs * p.num_q_heads) return;
+    const int s = (int)(row / p.num_q_heads), len = seq_len(p, s, false);
+    const int nblk = (len + kBlock - 1) / kBlock - first_block<FORM>(p, s, len);
+    const int npart = (nblk + p.part_blocks - 1) / p.part_blocks;
+    if (npart <= 1) return;
+    const float *ml = p.ws_ml + row * p.max_parts * 2, *o = p.ws_o + row * p.max_parts * D + lane;
+    float m = -INFINITY, w = 0.f;
+    if (lane < npart) {
+        m = __ldcg(ml + 2 * lane);
+        w = __ldcg(ml + 2 * lane + 1);
+    }
+    float M = m;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+    if (lane < npart) w *= exp2f(m - M);
+    float W = w, r[PER] = {};
+#pragma unroll
+    for (int d = 16; d; d >>= 1) W += __shfl_xor_sync(0xffffffffu, W, d);
+#pragma unroll 4
+    for (int i = 0; i < npart; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) r[e] = fmaf(wi, __ldcg(o + (size_t)i * D + 32 * e), r[e]);
+    }
+    OutT *out = static_cast<OutT *>(p.out) + row * D + lane;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) out[32 * e] = to_out<OutT>(r[e] / W);
+}
+
 // =====================================================================================
 // K3: KV append. One thread per 16-byte vector of (token, kv head, head-dim
 // chunk), so even a one-token-per-sequence step spreads over many CTAs.
