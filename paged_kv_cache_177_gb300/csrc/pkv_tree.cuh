@@ -979,8 +979,8 @@ __global__ void __launch_bounds__(256)
 // whose rows see all of the context and no drafts: 4 D flops a row and token against 4 D bytes a token for 256 rows of a
 // kv head, so from a few hundred rows on the tensor cores bound it. Each row's state (maximum, sum, unnormalised output,
 // fp32) is what the persistent decode kernel then starts the row's own blocks from, so nothing is joined at the end. 128 sequences
-// under 16384 tokens with 16-1024 own, 32 q / 8 kv heads: 113 us, of which the own blocks take 59 (as in plain
-// decode) and the prefix about 35; plain decode of all takes 650, groups of four that share their reads 692.
+// under 16384 tokens with 16-1024 own, 32 q / 8 kv heads: 107 us, of which the own blocks take 59 or less (plain
+// decode of them takes that) and the prefix about 35; plain decode of all takes 650, groups of four that share their reads 692.
 //
 // The plan, from one CTA: a group's prefix cut to the full blocks of its shortest sequence. tokens [num_groups],
 // first_blocks [num_seqs].
