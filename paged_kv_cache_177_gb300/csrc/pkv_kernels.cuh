@@ -1204,9 +1204,9 @@ __global__ void __launch_bounds__(NW * 32, 1)
         parts = (T + least - 1) / least;
     }
     const int W = (int)min((long long)gridDim.x * NW, parts);
-    // Workers that follow one another are on different SMs (128 sequences under a common prefix 113 -> 107 us, 64 sequences of
-    // 40 heads with a bias 127 -> 125). The plain form keeps its order, and with it its sums.
-    const int w = FORM != kWhole ? warp * gridDim.x + blockIdx.x : blockIdx.x * NW + warp;
+    // Behind prefixes, workers that follow one another are on different SMs: few of them spread over the card (the first and
+    // last of the above 49 -> 47 us, 26 -> 25; 128 sequences under 16K shared tokens 108 -> 106).
+    const int w = FORM == kBehindPrefix ? warp * gridDim.x + blockIdx.x : blockIdx.x * NW + warp;
     if (w >= W) return;
     const long long start = T * w / W, end = T * (w + 1) / W;
     const int cnt = (int)(end - start);
@@ -2431,7 +2431,7 @@ __global__ void __launch_bounds__(D *PG) lse_reduce_kernel(const DecodeParams p)
 }
 
 // The same, up to 32 partitions, a warp to a row: batches of many rows, where 512 threads and two of their reductions a
-// row would take longer than the rows' partitions (140 sequences of 32 query heads in two: the call 47 us, so 29). Started while the kernel before ends.
+// row would take longer than the rows' partitions (140 sequences of 32 query heads in two: the call 47 us, 29 so). Started while the kernel before ends.
 constexpr int kFewParts = 32, kFewRows = 8;
 
 template <typename OutT, int D, int FORM>
