@@ -144,7 +144,7 @@ __device__ __forceinline__ float capped_exact(float raw, float cap_in, float cap
 // not shifted or zero-filled, so what other rows hold must not meet a weight of zero: see seen().
 // HBM still bounds the decode kernels: a score is a few instructions among the D multiply-adds it comes from. 256 contexts around
 // 1000, 32 q / 8 kv heads, cap 50: 217 us, 0.96 of what its bytes take at the measured copy rate; windows of 4096 of 64
-// contexts of 2K-16K 166 us, 0.92; 64 contexts around 400 of 40 heads with a bias 125 us, 0.98.
+// contexts of 2K-16K 166 us, 0.92; 64 contexts around 400 of 40 heads with a bias 124-127 us, 0.96-0.98.
 template <bool kExact>
 struct ScoredRowsOf {
     static constexpr bool kScored = true;
