@@ -38,10 +38,10 @@ struct ScoredPrefillParams {
 // transformed (1042 TFLOP/s; prefill_tc_kernel takes 1362), 1688 with a bias, 1869 capped at 50 (801 TFLOP/s), 2968 with
 // scores past the polynomial. Per pair of tiles and chunk the MMAs take about 2500 clocks and the two
 // softmaxes behind them 1900, 3250 with the cap, whose polynomial's six multiply-adds a score are most of the rest. Tried
-// and slower, capped, where a CTA to a pair took 2035: the row unrolled in registers 2206; the same as one pass against the reference so far,
-// redone where a score exceeds it by more than 2^8, 3020-3380; two threads to a row (sixteen warps) 2209; two
-// 64-column S buffers a tile, so that products and softmax overlap, 2290 (2091 uncapped: products of 64 columns
-// take as long as of 128); the tiles' softmaxes in turns 2130, their first passes in turns 2038.
+// and slower, capped, where a CTA to a pair took 2035: the row unrolled in registers 2206; the same as one pass against the
+// reference so far, redone where a score exceeds it by more than 2^8, 3020-3380; two threads to a row (sixteen warps)
+// 2209; two 64-column S buffers a tile, so that products and softmax overlap, 2290 (2091 uncapped: products of 64
+// columns take as long as of 128); the tiles' softmaxes in turns 2130, their first passes in turns 2038.
 // Where pairs of tiles are few, a cluster of CTAs takes each: a CTA takes a run of the pair's chunks as if there were no
 // others and leaves its rows' O, not yet divided, with their references and sums in its shared memory, whose rings are
 // free by then; the cluster's CTAs then share the rows and join what all of them left through distributed shared memory.
