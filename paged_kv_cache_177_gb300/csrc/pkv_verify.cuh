@@ -215,6 +215,10 @@ __device__ __forceinline__ Fixed sum_residual(const T *p, const T *q, Multiple A
     return warp_sum(sum);
 }
 
+// A barrier of the cluster in two parts, for all its threads: what lies between them overlaps the wait.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 struct VerifyShared {
     int parent[kVerifyMaxRows];          // -1: never tried
     int token[kVerifyMaxRows];           // -1: outside the vocabulary
@@ -249,6 +253,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_drafts_k
         }
         return;
     }
+    cluster_arrive();  // this CTA runs: its shared memory may be written by the others (waited for in the first pass)
     const int n = (int)nn, V = a.vocab;
     const T *target = static_cast<const T *>(a.target) + (size_t)q0 * a.target_stride;
     const T *draft = a.draft ? static_cast<const T *>(a.draft) + (size_t)q0 * a.draft_stride : nullptr;
@@ -293,6 +298,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_drafts_k
         __syncthreads();  // (the last pass's sums have been read)
         if (lane == 0) sh.warp_sums[warp] = mine;
         __syncthreads();
+        if (passes == 0) cluster_wait();
         const int slot = passes++ & 1;
         if (warp == 0 && lane < ctas) {
             Fixed sum = 0;
