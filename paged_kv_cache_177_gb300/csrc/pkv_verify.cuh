@@ -271,8 +271,8 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_drafts_k
                 if (up < 0 || up >= i) up = -1;
             }
             if (up >= 0 && known) {
-                px = prob(target + (size_t)up * a.target_stride, x);
-                if (draft) qx = prob(draft + (size_t)up * a.draft_stride, x);
+                px = clean(prob(target + (size_t)up * a.target_stride, x));
+                if (draft) qx = clean(prob(draft + (size_t)up * a.draft_stride, x));
             }
             sh.token[i] = known ? (int)x : -1;
             sh.u[i] = __ldg(a.uniforms + q0 + i);
