@@ -748,7 +748,9 @@ int paged_prefill_attention_scored(void *out, const void *q, const void *k_cache
  *   draft_stride elements apart (at least vocab; any alignment, 16 bytes is faster).
  * Probabilities enter sums as multiples of 2^-44, rounded to nearest, in integers:
  *   results do not depend on any order of addition. Negative ones and NaN count as
- *   0, ones above 1 as 1, in the sums and where a draft is tried.
+ *   0, ones above 1 as 1, in the sums and where a draft is tried; a remainder
+ *   p - a q of less than 2^-44 counts as 0. A row's sum has to be less than 512
+ *   (that of a distribution is 1).
  * A sequence without rows, or with bad ones (n_s as for paged_tree_attention;
  *   PKV_DEVERR_LENGTH), gets 0 rows and token -1; so does next_tokens where a
  *   row holds no positive probability. A parent outside [0, i) makes a draft

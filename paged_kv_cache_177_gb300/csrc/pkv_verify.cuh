@@ -80,8 +80,8 @@ __device__ __forceinline__ Multiple to_multiple(Fixed a) {
 // off. (In fp64, which every warp would pay 16 clocks an operation for, a draft's test took 0.8 us.)
 __device__ __forceinline__ bool below(float u, float q, Fixed Z, Fixed r) {
     const Multiple z = to_multiple(Z), a = to_multiple(r);
-    const float x = u * q, e = fmaf(u, q, -x);
-    const float h = x * z.hi, l = fmaf(x, z.hi, -h) + fmaf(x, z.lo, e * z.hi);
+    const float x = __fmul_rn(u, q), e = fmaf(u, q, -x);
+    const float h = __fmul_rn(x, z.hi), l = fmaf(x, z.hi, -h) + fmaf(x, z.lo, e * z.hi);
     return (h - a.hi) + (l - a.lo) < 0.f;
 }
 
@@ -91,14 +91,16 @@ __device__ __forceinline__ bool below(float u, float q, float p) {
     return x == p ? fmaf(u, q, -x) < 0.f : x < p;
 }
 
-// A q as the sum of two fp32 numbers, 2^-48 of it off; whether p exceeds it.
+// A q as the sum of two fp32 numbers, 2^-48 of it off; whether p exceeds it by a unit or more. (p, x and y are each
+// rounded to units, so what exceeds by less could come out as -1, and with it a whole sum. x is the rounded
+// product, which must not be fused into the difference.)
 __device__ __forceinline__ bool exceeds(float p, float q, Multiple A, float &x, float &y) {
-    x = A.hi * q;
+    x = __fmul_rn(A.hi, q);
     y = fmaf(A.lo, q, fmaf(A.hi, q, -x));
-    return (p - x) - y > 0.f;
+    return (p - x) - y >= 0x1p-44f;
 }
 
-// max(p - A q, 0); where it is less than a unit roundings can make it -1.
+// max(p - A q, 0), less than a unit of it as 0: never negative.
 __device__ __forceinline__ Fixed residual(float p, float q, Multiple A) {
     p = clean(p);
     q = clean(q);
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_drafts_k
             const Fixed taken1 = refusals ? taken + Z : 1ll << 44;
             const Multiple A1 = to_multiple(taken1);
             const Fixed Z1 = pass(node, A1);
-            if (Z1 == 0) {
+            if (Z1 <= 0) {
                 spent = true;
                 summed = false;   // (the warps' sums are those of nothing)
             } else {
@@ -386,7 +388,7 @@ __global__ void __launch_bounds__(kVerifyThreads, kVerifyBlocks) verify_drafts_k
         for (int i = tid; i < a.max_accepted; i += kVerifyThreads) path_out[i] = i < count ? sh.path[i] : -1;
         if (tid == 0) a.num_accepted[s] = count;
     }
-    if (Z == 0) return;  // a row without a positive probability
+    if (Z <= 0) return;  // a row without a positive probability
     const T *prow = target + (size_t)node * a.target_stride;
     const T *qrow = draft ? draft + (size_t)node * a.draft_stride : nullptr;
     // floor(u Z), u in units of 2^-64

@@ -1,5 +1,8 @@
 """verify_drafts where its numbers are delicate: drafts tried on probabilities
-that are none."""
+that are none, comparisons at their border behind refusals, and remainders of
+less than a unit of the sums."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -63,3 +66,73 @@ def test_without_a_draft_model_too():
     got = call([2] * len(STRANGE), [-1, 0] * len(STRANGE), [0, 1] * len(STRANGE), p, None, [0.0, 0.2] * len(STRANGE),
                [0.5] * len(STRANGE), 2)
     assert got[1].tolist() == [1, 1, 2, 1, 2, 1, 2, 2]
+
+
+def test_at_the_border_behind_refusals():
+    """u q Z against r, at the fp32 number nearest to r / (q Z) and its neighbours, as exact fractions have it: products
+    of three are off by 2^-45, so a border must not move by 2^-25, an fp32 rounding of the product.  A second draft, behind
+    one that p gives nothing, and a third behind two."""
+    rng = np.random.default_rng(3)
+    cases = []
+    while len(cases) < 600:
+        third = len(cases) % 2
+        # multiples of 2^-30 that fp32 holds: every sum, and A q of A = 1, is exact in units of 2^-44
+        p, q = (rng.integers(1, 1 << 24, size=6) / 2.0 ** 27 for _ in range(2))
+        q[5], p[5] = 0.5, 0.0
+        z = sum(max(Fraction(a) - Fraction(b), Fraction(0)) for a, b in zip(p, q))
+        big_a, refused = Fraction(1), 1
+        rest = [max(Fraction(a) - Fraction(b), Fraction(0)) for a, b in zip(p, q)]
+        if third:
+            big_a += z
+            rest = [max(Fraction(a) - big_a * Fraction(b), Fraction(0)) for a, b in zip(p, q)]
+            z, refused = sum(rest), 2
+        # (roundings of r and Z to units: 2^-44 each of the elements, of numbers that shall be large against that)
+        live = [i for i in range(5) if rest[i] > Fraction(1, 100)]
+        if not live or z < Fraction(1, 20):
+            continue
+        x = live[0]
+        mid = np.float32(float(rest[x] / (Fraction(q[x]) * z)))
+        if not 0 < mid < 0.99:
+            continue
+        for u in (np.nextafter(mid, np.float32(0)), mid, np.nextafter(mid, np.float32(1))):
+            diff = Fraction(float(u)) * Fraction(q[x]) * z / rest[x] - 1
+            if abs(diff) < Fraction(1, 1 << 34):       # (6 roundings of 2^-45 against r > 1/100, and 2^-45: 2^-35)
+                continue
+            cases.append((p, q, x, refused, u, diff < 0))
+    n = 4
+    target, draft = (np.repeat(np.stack([c[i] for c in cases]), n, 0) for i in (0, 1))
+    tokens, parents, u = np.full((len(cases), n), 5), np.full((len(cases), n), -1), np.full((len(cases), n), 0.9)
+    for s, (_, _, x, refused, at, _) in enumerate(cases):
+        parents[s, 1:2 + refused] = 0
+        tokens[s, 1 + refused], u[s, 1 + refused] = x, at
+        parents[s, 2 + refused:] = 1                    # (below a refused one: never tried)
+    got = call([n] * len(cases), parents.reshape(-1), tokens.reshape(-1), target, draft, u.reshape(-1),
+               [0.5] * len(cases), 2)
+    stands = np.array([c[5] for c in cases])
+    assert 0.2 < stands.mean() < 0.8
+    assert np.array_equal(got[1] == 2, stands), np.flatnonzero((got[1] == 2) != stands)[:10]
+
+
+# p and q of one token whose remainder p - A q, A = 4 a, is above 0 and less than a unit, and whose p and A q round to
+# units so that the difference of those is -1; the other four, a and 1/4 each, leave nothing
+TINY = [("0x1.7b66fap-2", "0x1.960264p-23", "0x1.11f3f8p-23"), ("0x1.70ed70p-2", "0x1.f73244p-23", "0x1.5d2b6ap-23"),
+        ("0x1.72b108p-2", "0x1.ee09dap-23", "0x1.552efcp-23"), ("0x1.7563dcp-2", "0x1.a7b3f4p-23", "0x1.227eb8p-23")]
+
+
+@pytest.mark.parametrize("drafts", [2, 3, 5])
+def test_remainders_of_less_than_a_unit_count_as_nothing(drafts):
+    """Drafts of a token that p gives nothing: the first leaves (a - 1/4 four times, p - q), the others less than a
+    unit, so that what the first left stays, and a token follows."""
+    n = drafts + 1
+    p, q, finals, want = [], [], [], []
+    for a, p1, q1 in TINY:
+        a, p1, q1 = (float.fromhex(x) for x in (a, p1, q1))
+        for final, token in ((0.1, 0), (0.3, 1), (0.6, 2), (0.9, 3)):
+            p += [[a] * 4 + [p1, 0.0]] * n
+            q += [[0.25] * 4 + [q1, 0.5]] * n
+            finals.append(final)
+            want.append(token)
+    s = len(finals)
+    got = call([n] * s, ([-1] + [0] * drafts) * s, [5] * (n * s), np.array(p), np.array(q),
+               [0.5] * (n * s), finals, 2)
+    assert got[1].tolist() == [1] * s and got[2].tolist() == want
