@@ -153,9 +153,17 @@ struct TreeCut {
 // Whether a unit's weights come with their remainders: where a row may see fewer than 64 keys.
 __device__ __forceinline__ bool tree_split(int ctx) { return ctx < kPrefillSplitPositions; }
 
-// The first position whose values are cleaned before P V: the drafts', which not every row sees, and all that a
-// remainder meets.
-__device__ __forceinline__ int tree_first_clean(int ctx) { return tree_split(ctx) ? 0 : ctx; }
+// The same of chunk j (128 positions). Under a prefix the first chunk's do, whatever the context: plain decode gives the
+// weights of a sequence's first 64 tokens their remainders, and many rows give most of their weight to those.
+template <bool kPrefix>
+__device__ __forceinline__ bool tree_chunk_split(int ctx, int j) { return kPrefix ? j == 0 : tree_split(ctx); }
+
+// The positions [from, to) whose values are cleaned before P V, of a sequence of len tokens: the drafts', which not every
+// row sees, and all that a remainder meets.
+template <bool kPrefix>
+__device__ __forceinline__ int tree_clean_from(int ctx) { return kPrefix || tree_split(ctx) ? 0 : ctx; }
+template <bool kPrefix>
+__device__ __forceinline__ int tree_clean_to(int len) { return kPrefix ? min(len, 128) : len; }
 
 // The line that is cut into the workers' ranges: every unit takes kTreeUnitCost positions for its start and end (Q, a
 // masked chunk, the join of the sides, the output: about as long as that many chunks), then one per chunk.
@@ -547,7 +555,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             ok = values_ready(k) && (k + 1 == nc || wait_k(r0 + k + 1));
                             for (int t = 0; t < tiles && ok; ++t) {
                                 if (!(ok = weights_ready(t))) break;
-                                issue_pv(t, r0 + k, k == 0, tree_split(at.ctx()));
+                                issue_pv(t, r0 + k, k == 0, tree_chunk_split<kPrefix>(at.ctx(), at.c0 + k));
                                 if (k + 1 < nc) {
                                     issue_s(t, r0 + k + 1);
                                     umma_commit(&b.s_full[t]);
@@ -577,7 +585,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                             if (k + 1 < nc && !(ok = scores(k + 1))) break;
                             if (k < 0) continue;
                             if (!(ok = values_ready(k) && weights_ready(k & 1))) break;
-                            issue_pv(k & 1, r0 + k, k < 2, tree_split(at.ctx()));
+                            issue_pv(k & 1, r0 + k, k < 2, tree_chunk_split<kPrefix>(at.ctx(), at.c0 + k));
                             umma_commit(&b.v_empty[(r0 + k) % NS]);
                             if (k + 2 >= nc) umma_commit(&b.o_done[k & 1]);
                         }
@@ -598,7 +606,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
             bool ok = true;
             int r0 = 0;
             do {
-                const int nc = at.c1 - at.c0, first = tree_first_clean(at.ctx());
+                const int nc = at.c1 - at.c0, first = tree_clean_from<kPrefix>(at.ctx());
                 const int nblk = (at.len + kBlock - 1) / kBlock, lo = nblk * kBlock - at.len;
                 // every chunk is waited for and passed on, drafts or not, so that no stage's phase runs
                 // away from this role's count
@@ -606,7 +614,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     const int st = (r0 + k) % NS;
                     if (!(ok = warp_wait(&b.v_full[st], ((r0 + k) / NS) & 1))) break;
                     const int blk0 = (at.c0 + k) * C::kChunkBlocks;
-                    const int b_lo = max(0, first / kBlock - blk0), b_hi = min(C::kChunkBlocks, nblk - blk0);
+                    const int b_lo = max(0, first / kBlock - blk0);
+                    const int b_hi = min(C::kChunkBlocks, (kPrefix ? tree_clean_to<kPrefix>(at.len) / kBlock : nblk) - blk0);
                     uint8_t *vst = base + C::kVOff + st * C::kStage;
                     for (int i = b_lo * (C::kBlockBytes / 16) + lane; i < b_hi * (C::kBlockBytes / 16); i += 32) {
                         const uint4 v = reinterpret_cast<const uint4 *>(vst)[i];
@@ -742,7 +751,7 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     uint64_t rss[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) rss[i] = pack_f2(0.f, 0.f);
-                    if (__builtin_expect(tree_split(ctx), 0)) {
+                    if (__builtin_expect(tree_chunk_split<kPrefix>(ctx, at.c0 + k), 0)) {
 #pragma unroll 1
                         for (int q = 0; q < 4; ++q) {
                             float x[32];
@@ -878,8 +887,8 @@ __global__ void __launch_bounds__(TreeCfg<D, kPair>::kThreads, 1)
                     }
                 }
                 if (__builtin_expect(row_ok && *reinterpret_cast<volatile int *>(&b.any_bad) != 0, 0))
-                    tree_add_zeroed(p, words, at.table_row(), h, max(tree_first_clean(ctx), at.c0 * C::kKeys),
-                                    min(at.len, at.c1 * C::kKeys), ctx, D, d0, kMine, state ? nullptr : dst, po);
+                    tree_add_zeroed(p, words, at.table_row(), h, max(tree_clean_from<kPrefix>(ctx), at.c0 * C::kKeys),
+                                    min(tree_clean_to<kPrefix>(at.len), at.c1 * C::kKeys), ctx, D, d0, kMine, state ? nullptr : dst, po);
                 tc_fence_before();
             }
             if (!uncut && at.c0 == 0) {  // begun here, ends further on (a worker cuts at most one unit so)
