@@ -3,6 +3,8 @@
 // to a window, over a prefix that is seen from both sides.
 #pragma once
 
+#include <cfloat>
+
 #include <cooperative_groups.h>
 
 #include "pkv_prefill_tc.cuh"
@@ -480,13 +482,16 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         const int lo_t = see.lo(pos), hi_t = see.hi(pos);  // (rows past the tile's end see what its first does)
         const uint32_t cols = tmem + ((uint32_t)(quad * 32) << 16) + t * C::kTileCols;
         const float slope = kBias ? slope_log2(p.slopes, h * g + row_head, p.num_q_heads) : 0.f;
-        // The polynomial's coefficients in powers of the raw score, and up to where it holds. (Constants past fp32 where
-        // the cap is tiny: every score is taken the long way.)
+        // The polynomial's coefficients in powers of the raw score, and up to where it holds: every score is taken the long
+        // way where the cap is so small that they pass fp32; where it is so large that they fall below its normal numbers,
+        // scores from y = 1/20 on (to where c2 y^4 and what follows are below 2^-20), and from 2^-12 on where c1 does; and
+        // where the square of a raw score would pass fp32.
         const float ci2 = p.cap_in * p.cap_in;
         const float k0 = kCap ? p.scale_log2 * kTanh0 : p.scale_log2, k1 = p.scale_log2 * kTanh1 * ci2;
         const float k2 = p.scale_log2 * kTanh2 * ci2 * ci2, k3 = p.scale_log2 * kTanh3 * ci2 * ci2 * ci2;
         const float k4 = p.scale_log2 * kTanh4 * ci2 * ci2 * ci2 * ci2;
-        const float near_max = fabsf(k4) < INFINITY ? kCapNear / fabsf(p.cap_in) : -1.f;
+        const float near_y = fabsf(k4) >= FLT_MIN ? kCapNear : fabsf(k1) >= FLT_MIN ? 0.05f : 0x1p-12f;
+        const float near_max = fabsf(k4) < INFINITY ? fminf(near_y / fabsf(p.cap_in), 0x1p60f) : -1.f;
         // Without either scores stay raw: x sl is the log2-domain score, the sign is folded in; a scale of 0 becomes one
         // that leaves every score 0, so that a masked -inf stays -inf.
         const float sl = kCap || kBias ? 1.f : fmaxf(fabsf(p.scale_log2), 1e-30f);
