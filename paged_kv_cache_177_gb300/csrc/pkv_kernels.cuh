@@ -181,9 +181,13 @@ __device__ __forceinline__ ScoredRowsOf<kExact> scored_rows(const DecodeParams &
     return {max(start - t0, 0), min(len - t0, kBlock), (float)(len - 1 - t0), p.scale_log2, p.cap_in, p.cap_log2};
 }
 
-// The slope of query head `head` of the group whose slopes these are, in the log2 domain.
+// The slope of query head `head` of the group whose slopes these are, in the log2 domain. Steeper ones than 10^28 count as
+// that: the nearest token (the farthest, of a negative slope) has all the weight with either, but a product with a distance
+// past fp32 would leave a block no finite score, and weights of NaN.
 __device__ __forceinline__ float slope_log2(const float *slopes, int head, int g) {
-    return slopes && head < g ? __ldg(slopes + head) * 1.4426950408889634f : 0.f;
+    constexpr float kSteepest = 1e28f;
+    const float x = slopes && head < g ? __ldg(slopes + head) * 1.4426950408889634f : 0.f;
+    return x > kSteepest ? kSteepest : x < -kSteepest ? -kSteepest : x;
 }
 
 // Weights of a block also enter as their rounding remainders (kSplitBlocks): in a unit's first blocks, and where
