@@ -973,6 +973,12 @@ def _slopes(slopes: Optional[torch.Tensor], num_q_heads: int, index: int):
     return slopes.data_ptr()
 
 
+def _window(window: int) -> int:
+    """A window as the C ABI's 32 bits hold it: one past them sees everything, as 2^31 - 1 does; a negative one is
+    refused there."""
+    return max(-1, min(int(window), (1 << 31) - 1))
+
+
 def paged_decode_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                                   block_tables: torch.Tensor, context_lens: torch.Tensor, scale: float, *,
                                   softcap: float = 0.0, window: int = 0, slopes: Optional[torch.Tensor] = None,
@@ -992,8 +998,9 @@ def paged_decode_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: t
     if max_context_len is None:
         max_context_len = int(context_lens.max().item()) if S else 0
     max_context_len = int(max_context_len)
+    window = _window(window)
     if workspace is None:
-        read = min(max_context_len, ((int(window) - 1) // 16 + 2) * 16) if window > 0 else max_context_len
+        read = min(max_context_len, ((window - 1) // 16 + 2) * 16) if window > 0 else max_context_len
         need = _workspace_bytes(S, Hq, Hkv, D, read, partition_tokens)
         if need:
             with torch.cuda.stream(stream):       # zero-filled, on the call's stream
@@ -1001,7 +1008,7 @@ def paged_decode_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: t
     keep, ws, ws_bytes = _workspace(0, workspace, dev, stream)
     _launch(_scored, "paged_decode_attention_scored", dev, stream, out.data_ptr(), q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(), float(scale), float(softcap),
-            int(window), _slopes(slopes, Hq, dev), Hkv, S, Hq, D, max_blocks, NB, max_context_len, dt,
+            window, _slopes(slopes, Hq, dev), Hkv, S, Hq, D, max_blocks, NB, max_context_len, dt,
             int(partition_tokens), ws, ws_bytes)
     return out
 
@@ -1045,7 +1052,7 @@ def paged_prefill_attention_scored(out: torch.Tensor, q: torch.Tensor, k_cache: 
         max_context_len = int(context_lens.max().item()) if S else 0
     _launch(_prefill_scored, "paged_prefill_attention_scored", dev, stream, out.data_ptr(), q.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), context_lens.data_ptr(),
-            query_start.data_ptr(), float(scale), float(softcap), int(window), _slopes(slopes, Hq, dev),
+            query_start.data_ptr(), float(scale), float(softcap), _window(window), _slopes(slopes, Hq, dev),
             _p(prefix_lens), cache[1], S, Hq, D, tables[1] if S else 1, cache[0], T, int(max_query_len),
             int(max_context_len), PKV_BF16)
     return out
