@@ -3,7 +3,9 @@
 // to a window, over a prefix that is seen from both sides.
 #pragma once
 
+#include <algorithm>
 #include <cfloat>
+#include <cmath>
 
 #include <cooperative_groups.h>
 
@@ -15,6 +17,7 @@ struct ScoredPrefillParams {
     PrefillParams pp;
     const int32_t *prefix_lens;  // [num_seqs] or null
     int ctas;                    // CTAs of the cluster that takes a pair of tiles
+    float near_max;              // raw scores up to this in size are capped by the polynomial
 };
 
 // =====================================================================================
@@ -55,6 +58,18 @@ constexpr float kCapNear = 0.75f;
 // tanh(y) / y = sum c_k y^2k, fitted on [0, kCapNear] (relative error 5.7e-7)
 constexpr float kTanh0 = 0.999999435f, kTanh1 = -0.333282515f, kTanh2 = 0.132589832f, kTanh3 = -0.0500563012f,
                 kTanh4 = 0.0129296311f;
+
+// Up to which raw score the polynomial in powers of it holds. Every score is taken the long way where the cap is so
+// small that its coefficients pass fp32. Where it is so large that they fall below fp32's normal numbers, scores from y = 1/20
+// on are (to where c2 y^4 and what follows are below 2^-20), from 2^-12 on where c1 falls below too; and
+// those whose square would pass fp32.
+inline float capped_near_max(float scale_log2, float cap_in) {
+    const double ci2 = (double)cap_in * cap_in, s = std::fabs((double)scale_log2);
+    const double k1 = s * -kTanh1 * ci2, k4 = s * kTanh4 * ci2 * ci2 * ci2 * ci2;
+    if (!(k4 <= FLT_MAX)) return -1.f;
+    const double y = ci2 < FLT_MIN || k1 < FLT_MIN ? 0x1p-12 : k4 < FLT_MIN ? 0.05 : kCapNear;
+    return cap_in == 0.f ? 0x1p60f : (float)std::min(y / std::fabs((double)cap_in), 0x1p60);
+}
 
 struct ScoredBars {
     uint64_t q_full;
@@ -482,16 +497,11 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
         const int lo_t = see.lo(pos), hi_t = see.hi(pos);  // (rows past the tile's end see what its first does)
         const uint32_t cols = tmem + ((uint32_t)(quad * 32) << 16) + t * C::kTileCols;
         const float slope = kBias ? slope_log2(p.slopes, h * g + row_head, p.num_q_heads) : 0.f;
-        // The polynomial's coefficients in powers of the raw score, and up to where it holds: every score is taken the long
-        // way where the cap is so small that they pass fp32; where it is so large that they fall below its normal numbers,
-        // scores from y = 1/20 on (to where c2 y^4 and what follows are below 2^-20), and from 2^-12 on where c1 does; and
-        // where the square of a raw score would pass fp32.
+        // the polynomial's coefficients in powers of the raw score (capped_near_max)
         const float ci2 = p.cap_in * p.cap_in;
         const float k0 = kCap ? p.scale_log2 * kTanh0 : p.scale_log2, k1 = p.scale_log2 * kTanh1 * ci2;
         const float k2 = p.scale_log2 * kTanh2 * ci2 * ci2, k3 = p.scale_log2 * kTanh3 * ci2 * ci2 * ci2;
         const float k4 = p.scale_log2 * kTanh4 * ci2 * ci2 * ci2 * ci2;
-        const float near_y = fabsf(k4) >= FLT_MIN ? kCapNear : fabsf(k1) >= FLT_MIN ? 0.05f : 0x1p-12f;
-        const float near_max = fabsf(k4) < INFINITY ? fminf(near_y / fabsf(p.cap_in), 0x1p60f) : -1.f;
         // Without either scores stay raw: x sl is the log2-domain score, the sign is folded in; a scale of 0 becomes one
         // that leaves every score 0, so that a masked -inf stays -inf.
         const float sl = kCap || kBias ? 1.f : fmaxf(fabsf(p.scale_log2), 1e-30f);
@@ -541,7 +551,7 @@ __global__ void __launch_bounds__(TcCfg<D>::kThreads, 1)
                     for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) big[q] = max3f(big[q], fabsf(v[q][e]), fabsf(v[q][e + 1]));
-                    far |= __any_sync(0xffffffffu, row_ok && !(fmaxf(big[0], big[1]) <= near_max));
+                    far |= __any_sync(0xffffffffu, row_ok && !(fmaxf(big[0], big[1]) <= sp.near_max));
                 }
                 if ((kCap || kBias) && __builtin_expect(far, 0)) {
 #pragma unroll

@@ -714,6 +714,7 @@ int paged_prefill_attention_scored(void *out, const void *q, const void *k_cache
     if (!out || !q || !k_cache || !v_cache || !block_tables || !context_lens || !query_start) return PKV_ERR_ARG;
     if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_ALIGN;
     if (window == 0) pp.d.window = INT32_MAX;
+    sp.near_max = pkv::capped_near_max(pp.d.scale_log2, pp.d.cap_in);
     sp.prefix_lens = prefix_lens;
     pp.query_start = query_start;
     pp.tile_tokens = tile_tokens;
