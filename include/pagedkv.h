@@ -649,8 +649,7 @@ int kv_accept_layers(void *const *k_caches, void *const *v_caches, int num_layer
  *   max_group_size: host-side bound on the groups. A group past it or out of range
  *   raises PKV_DEVERR_LENGTH and shares nothing.
  * Results as of paged_decode_attention, whose sums it takes in another order: as there the
- * weights of the first 64 tokens have 16 bits (of the first 128 where the prefix holds
- * them), the others 8. bf16; num_q_heads / num_kv_heads at most 16; at most 8192 sequences.
+ * weights of the first 64 tokens have 16 bits, the others 8. bf16; num_q_heads / num_kv_heads at most 16; at most 8192 sequences.
  * workspace: pkv_common_prefix_workspace_bytes(...) bytes, zero-filled once like any decode
  *   workspace (its first PKV_DECODE_COUNTER_BYTES are the same counters). Concurrent
  *   calls must not share it.
