@@ -308,8 +308,9 @@ int launch_cascade(const CUtensorMap &tmk, const CUtensorMap &tmv, const pkv::De
 template <int D, int FORM>
 int launch_reduce(const pkv::DecodeParams &p, pkv_dtype dt, cudaStream_t st) {
     if constexpr (FORM == pkv::kScored) {
-        if (p.max_parts <= pkv::kFewParts) {
-            const long long ctas = ((long long)p.num_seqs * p.num_q_heads + pkv::kFewRows - 1) / pkv::kFewRows;
+        const long long rows = (long long)p.num_seqs * p.num_q_heads;
+        if (p.max_parts <= (rows < pkv::kManyRows ? pkv::kFewParts : pkv::kMostParts)) {
+            const long long ctas = (rows + pkv::kFewRows - 1) / pkv::kFewRows;
             const dim3 few((unsigned)ctas), threads(32 * pkv::kFewRows);
             return dt == PKV_BF16 ? launch_pdl(pkv::lse_reduce_few_kernel<__nv_bfloat16, D, FORM>, few, threads, 0, st, p)
                                   : launch_pdl(pkv::lse_reduce_few_kernel<float, D, FORM>, few, threads, 0, st, p);

@@ -2434,9 +2434,14 @@ __global__ void __launch_bounds__(D *PG) lse_reduce_kernel(const DecodeParams p)
     }
 }
 
-// The same, up to 32 partitions, a warp to a row: batches of many rows, where 512 threads and two of their reductions a
-// row would take longer than the rows' partitions (140 sequences of 32 query heads in two: the call 47 us, 29 so). Started while the kernel before ends.
-constexpr int kFewParts = 32, kFewRows = 8;
+// The same with a warp to a row, started while the kernel before ends: for few partitions, and for up to 32 where rows are
+// many, whose 512 threads each and two of their reductions would take longer than the rows' partitions. A warp reads a row's
+// states four at a time, which costs more than it saves where rows are few and partitions many.
+// (The call with 512 threads and so, partitions of 512 tokens: 8 rows of 128 in 2, 4, 8, 16, 32: 15.4 and 15.0 us, 15.3
+// and 14.9, 15.8 and 16.2, 16.0 and 18.0, 16.0 and 20.2; 512 rows 19.2 and 17.3, 19.6 and 17.9, 22.7 and 22.0, 39.2 and
+// 39.9, 72.7 and 75.6; 1024 21.8 and 17.7, 24.4 and 20.9, 41.9 and 38.6, 74.1 and 73.1, 128.5 and 129.6; 4480 of 64 48 and
+// 31, 65 and 47, 99 and 81, 175 and 157, 318 and 303.)
+constexpr int kFewParts = 4, kMostParts = 32, kManyRows = 1024, kFewRows = 8;
 
 template <typename OutT, int D, int FORM>
 __global__ void __launch_bounds__(32 * kFewRows) lse_reduce_few_kernel(const DecodeParams p) {
