@@ -39,8 +39,8 @@ struct ScoredPrefillParams {
 //    its weight: tiles with rows that see less than 64 keys, and with a bias by distance the chunks next to the tile's
 //    positions and the first.
 //
-// Measured (32 q / 8 kv heads of 128, 512-token chunks behind 16K-32K tokens, 1.5 PFLOP; two CTAs to a pair): 1437 us with nothing
-// transformed (1042 TFLOP/s; prefill_tc_kernel takes 1362), 1688 with a bias, 1869 capped at 50 (801 TFLOP/s), 2968 with
+// Measured (32 q / 8 kv heads of 128, 512-token chunks behind 16K-32K tokens, 1.5 PFLOP; two CTAs to a pair): 1438 us with nothing
+// transformed (1042 TFLOP/s; prefill_tc_kernel takes 1362), 1695 with a bias, 1868 capped at 50 (801 TFLOP/s), 2968 with
 // scores past the polynomial. Per pair of tiles and chunk the MMAs take about 2500 clocks and the two
 // softmaxes behind them 1900, 3250 with the cap, whose polynomial's six multiply-adds a score are most of the rest. Tried
 // and slower, capped, where a CTA to a pair took 2035: the row unrolled in registers 2206; the same as one pass against the
@@ -51,7 +51,7 @@ struct ScoredPrefillParams {
 // others and leaves its rows' O, not yet divided, with their references and sums in its shared memory, whose rings are
 // free by then; the cluster's CTAs then share the rows and join what all of them left through distributed shared memory.
 // (16 tokens behind 16K, capped, 32 q / 8 kv heads of 128: 333 us with a CTA to a pair, 53 with eight.)
-// 32 prompts of 64-2048 tokens, window 1024, capped: 720 us (593 uncapped); with one warp that cleans whole chunks 830, two
+// 32 prompts of 64-2048 tokens, window 1024, capped: 720 us (594 uncapped); with one warp that cleans whole chunks 830, two
 // 742, two that take only blocks with rows that are not seen 720.
 // =====================================================================================
 constexpr float kCapNear = 0.75f;

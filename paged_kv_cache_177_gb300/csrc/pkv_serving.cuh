@@ -225,6 +225,8 @@ int launch_rope(pkv::RopeParams p, bool interleaved, bool e4m3, cudaStream_t st)
 // 18, 14, 13; 512 behind 8K 197, 110, 124, 199; 8 x 64 behind 1K 34, 27, 43, 95, behind 4K 105, 63, 79, 142; 24 x 64 behind 4K
 // 208, 183, 228, 371; 18 x 64 107, 124, 156, 285; prompts of 256 13.4, 15.0, 14.9, 41, of 512 20, 19, 30, 71, of
 // 768 26, 32, 48, 105. The card holds 76, 36 and 15 clusters of two, four and eight.)
+// These are batches of equal lengths. One width serves a launch, so a batch of mixed ones counts as all as long as its longest:
+// 16 tokens behind 16K take 50 us alone, forty sequences of 4 behind 500 47, and both in one call 173, in clusters of two.
 int prefill_scored_ctas(long long pairs, long long chunks, const int (&resident)[4]) {
     int best = 0;
     long long least = 0;
